@@ -83,8 +83,15 @@ extern "C" {
                                   SFC_ROW_TIMEOUT, with tokens -1 and lengths 0 (other outputs undefined),
                                   and the copies that were issued are awaited before the kernel ends */
 
+/* Flag of the distillation calls. */
+#define SFC_FLAG_NORMALISE_TEACHER 16u /* the teacher's values are raw top logits: t = softmax over the row's
+                                          entries of y / T, instead of t = exp(y) of log-probabilities y */
+
 /* Largest packed_width accepted. */
 #define SFC_MAX_PACKED_WIDTH 16384
+
+/* Largest number of drafted tokens per request that the verification calls accept. */
+#define SFC_MAX_DRAFTS 64
 
 /*
  * Bytes of device workspace that sfc_sample_filter_capture needs for these sizes (0: none; workspace
@@ -232,6 +239,148 @@ int sfc_replay_logprob(const void* logits, int dtype, int64_t B, int64_t V, int6
                        const float* temperature, const int32_t* support_ids, const int32_t* lengths,
                        int32_t packed_width, const int32_t* tokens, float* token_logprob,
                        float* support_logprobs, int32_t* row_status, void* stream);
+
+/*
+ * The gradient of sfc_replay_logprob with respect to its logits. With lp_i the log-probabilities over S,
+ * g = grad_token_logprob[r] and G = grad_support_logprobs[r, :] (upstream gradients), and pi_i = exp(lp_i):
+ *   u_i = G_i + g [support_ids[r, i] = tokens[r]],
+ *   grad_logits[r, support_ids[r, i]] = (u_i - pi_i sum_S u) / T,   and 0 outside S.
+ *
+ * grad_token_logprob     [B] float32.
+ * grad_support_logprobs  [B, W] float32, entries j < lengths[r] are read; NULL: all 0.
+ * grad_logits            [B, grad_stride] elements of `dtype` out, the first V of each row are written, each
+ *                        rounded once; aligned to the element size. Must not overlap the logits.
+ * grad_stride            elements between row starts, >= V.
+ * Rows on which the replay gives no log-probability (OVERFLOW, BADPARAM) pass no gradient on: zeros. On
+ * OUTSIDE rows the token's log-probability is the constant -inf: g is not used.
+ * The other arguments are those of sfc_replay_logprob. Returns SFC_OK or a negative code (nothing enqueued).
+ */
+int sfc_replay_backward(const void* logits, int dtype, int64_t B, int64_t V, int64_t row_stride,
+                        const float* temperature, const int32_t* support_ids, const int32_t* lengths,
+                        int32_t packed_width, const int32_t* tokens, const float* grad_token_logprob,
+                        const float* grad_support_logprobs, void* grad_logits, int64_t grad_stride, void* stream);
+
+/*
+ * Distillation from a teacher's top logits: the loss of a student's rows against packed teacher
+ * distributions (the supports and log-probabilities that a capture of the teacher's rows wrote, or its raw
+ * top logits). Per row r, with n = min(lengths[r], W) and z = logits / T:
+ *   t_i = exp(teacher_values[r, i])                                  (log-probabilities), or
+ *   t_i = softmax over i < n of teacher_values[r, i] / T             (SFC_FLAG_NORMALISE_TEACHER)
+ *   ln p = z - ln sum_V exp z                                        (the student, over its whole vocabulary)
+ *   loss[r] = sum_{i < n} t_i (ln t_i - ln p_i),  an entry with t_i = 0 adds 0
+ *   grad_logits[r, j] = grad_loss[r] / T (tau p_j - t_j),  tau = sum_{i < n} t_i,  t_j = 0 for the others
+ * t need not sum to 1 (a teacher cut to its largest probabilities keeps them as they are).
+ *
+ * logits          [B, row_stride] elements of `dtype`, row-major; aligned to the element size. -inf logits
+ *                 have probability 0 (a teacher entry with t_i > 0 there makes the loss +inf).
+ * temperature     [B] float32, finite and > 0.
+ * teacher_ids     [B, W] int32, teacher_values [B, W] float32: entries j < lengths[r] are read; the ids must be
+ *                 distinct — repeated ids give unspecified gradients.
+ * lengths         [B] int32. 0: the row has no teacher (padding, a row that did not capture): its logits are not
+ *                 read, its loss is 0 and its gradient 0. Above W: the first W entries are the teacher
+ *                 (a capture writes the largest first) and the status is SFC_ROW_OVERFLOW.
+ * flags           0 or SFC_FLAG_NORMALISE_TEACHER; other bits: SFC_EINVAL.
+ * loss            [B] float32 out; NaN on BADPARAM rows.
+ * row_stats       [B, 4] float32 out (16-byte aligned), or NULL: what sfc_distill_backward needs of the rows.
+ * row_status      [B] int32 out: SFC_ROW_OK; SFC_ROW_OVERFLOW; SFC_ROW_BADPARAM when T is not finite or <= 0,
+ *                 lengths[r] < 0, an id lies outside [0, V), a logit is NaN or +inf, no logit is finite, a
+ *                 teacher value is NaN or +inf, or (normalised) no teacher value is finite.
+ * Every array is a device pointer owned by the caller; nothing is allocated; results are deterministic.
+ * Returns SFC_OK or a negative code (nothing enqueued).
+ */
+int sfc_distill_forward(const void* logits, int dtype, int64_t B, int64_t V, int64_t row_stride,
+                        const float* temperature, const int32_t* teacher_ids, const float* teacher_values,
+                        const int32_t* lengths, int32_t packed_width, uint32_t flags, float* loss, float* row_stats,
+                        int32_t* row_status, void* stream);
+
+/*
+ * The gradient of sfc_distill_forward with respect to its logits, from the row_stats that the forward call
+ * wrote for the same arguments.
+ *
+ * grad_loss       [B] float32: the upstream gradient of each row's loss.
+ * grad_logits     [B, grad_stride] elements of `dtype` out, the first V of each row are written, each rounded
+ *                 once; aligned to the element size. Must not overlap the logits. BADPARAM rows get zeros.
+ */
+int sfc_distill_backward(const void* logits, int dtype, int64_t B, int64_t V, int64_t row_stride,
+                         const float* temperature, const int32_t* teacher_ids, const float* teacher_values,
+                         const int32_t* lengths, int32_t packed_width, uint32_t flags, const float* row_stats,
+                         const float* grad_loss, void* grad_logits, int64_t grad_stride, void* stream);
+
+/*
+ * Loss and gradient in one call, for callers that know grad_loss beforehand (a mean over the batch): the logits
+ * are read from HBM once instead of twice.
+ */
+int sfc_distill_forward_backward(const void* logits, int dtype, int64_t B, int64_t V, int64_t row_stride,
+                                 const float* temperature, const int32_t* teacher_ids, const float* teacher_values,
+                                 const int32_t* lengths, int32_t packed_width, uint32_t flags, const float* grad_loss,
+                                 float* loss, int32_t* row_status, void* grad_logits, int64_t grad_stride,
+                                 void* stream);
+
+/*
+ * Verification of drafted tokens against the target's distributions (speculative decoding). Per request b with
+ * n = num_drafts[b] drafted tokens x_0 .. x_{n-1}, target rows 0 .. n and draft rows 0 .. n-1:
+ *   p_j = softmax(target_j / T),  q_j = softmax(draft_j / T_d), or q_j(x_j) = 1 without draft rows
+ *   draft j is accepted while u_j q_j(x_j) < p_j(x_j), in order; a = accepted[b] of them are
+ *   w = max(p_a - q_a, 0) if a < n (p_a where that leaves no mass), p_n if a = n
+ *   token = argmax_i w_i / E_i, E_i = -ln v_i, ties to the lowest id
+ * so that the emitted tokens are distributed as the target's own draws. v_i comes from Philox4x32-10 with key
+ * (seed lo, seed hi) and counter (2^31 + i / 4, row, step lo, step hi), row = row_offset + b: word i % 4 of the
+ * block, w, v = (2 (w >> 9) + 1) 2^-24. (The decode step's counters are below 2^31: a draft drawn with the same
+ * seed and step shares no noise with its verification.)
+ *
+ * target_logits   element (b, j, v) at b target_request_stride + j target_row_stride + v, j <= D, of `dtype`;
+ *                 rows aligned to the element size; any strides >= 0 (a shared row is read where it lies). -inf
+ *                 logits have probability 0.
+ * draft_logits    element (b, j, v) at b draft_request_stride + j draft_row_stride + v, j < D; NULL: the drafts
+ *                 are certain (looked up, not drawn).
+ * D               drafted tokens a request can hold, 1 <= D <= SFC_MAX_DRAFTS.
+ * temperature     [B] float32, finite and > 0; 0 with SFC_FLAG_GREEDY_T0: p is 1 at the lowest id among the
+ *                 largest logits. draft_temperature: the draft's, or NULL for the same.
+ * draft_tokens    [B, D] int32. num_drafts [B] int32 in [0, D], or NULL for D everywhere.
+ * uniforms        [B, D] float32 in [0, 1).
+ * flags           0 or SFC_FLAG_GREEDY_T0.
+ * accepted        [B] int32 out: a.
+ * tokens          [B, D + 1] int32 out: the a accepted drafts, the drawn token, then -1.
+ * token_logprobs  [B, D + 1] float32 out: ln p_j of the emitted tokens, then 0.
+ * row_status      [B] int32 out: SFC_ROW_OK, or SFC_ROW_BADPARAM (accepted 0, tokens -1, log-probabilities NaN)
+ *                 when a temperature or num_drafts is out of range, or when, at a position up to a, a row has a
+ *                 NaN or +inf logit or no finite one, or the drafted token is outside [0, V). Rows past the
+ *                 position of the first refusal do not matter.
+ * workspace       device scratch of sfc_verify_workspace_size bytes, 16-byte aligned, with a contract like
+ *                 sfc_workspace_size's: ZERO-FILLED before its first use, left ready for the next verification
+ *                 call (of any size that it holds), used by one call at a time. Not to be shared with
+ *                 sfc_sample_filter_capture.
+ * Returns SFC_OK or a negative code (nothing enqueued).
+ */
+size_t sfc_verify_workspace_size(int64_t B, int32_t D, int64_t V, int dtype);
+int sfc_verify_drafts(const void* target_logits, const void* draft_logits, int dtype, int64_t B, int32_t D, int64_t V,
+                      int64_t target_request_stride, int64_t target_row_stride, int64_t draft_request_stride,
+                      int64_t draft_row_stride, const float* temperature, const float* draft_temperature,
+                      const int32_t* draft_tokens, const int32_t* num_drafts, const float* uniforms, uint64_t seed,
+                      uint64_t step, int64_t row_offset, uint32_t flags, int32_t* accepted, int32_t* tokens,
+                      float* token_logprobs, int32_t* row_status, void* workspace, size_t workspace_bytes,
+                      void* stream);
+
+/*
+ * The same verification over captured supports: p_j and q_j are the filtered distributions that captures of the
+ * target's and the draft's rows wrote, zero outside their supports.
+ *
+ * target_ids, target_logprobs, target_lengths   [B, D + 1, target_width] x 2, [B, D + 1].
+ * draft_ids, draft_logprobs, draft_lengths      [B, D, draft_width] x 2, [B, D]; a row of length 0 is a certain
+ *                 draft; draft_ids NULL: all are. The ids of a row are distinct and below 2^31; their order is free.
+ * row_status      SFC_ROW_OK; SFC_ROW_OVERFLOW when a length at a position up to a exceeds its width (the support
+ *                 is incomplete); SFC_ROW_BADPARAM when num_drafts is out of range, or, at a position up to a, a
+ *                 target length is < 1, a draft length < 0, a drafted token negative, its log-probability NaN or
+ *                 +inf, or at position a an id of the target negative, a log-probability NaN or +inf, or no target
+ *                 entry has any probability. Such requests: accepted 0, tokens -1, log-probabilities NaN.
+ * The other arguments are those of sfc_verify_drafts; no workspace is needed.
+ */
+int sfc_verify_supports(const int32_t* target_ids, const float* target_logprobs, const int32_t* target_lengths,
+                        int32_t target_width, const int32_t* draft_ids, const float* draft_logprobs,
+                        const int32_t* draft_lengths, int32_t draft_width, int64_t B, int32_t D,
+                        const int32_t* draft_tokens, const int32_t* num_drafts, const float* uniforms, uint64_t seed,
+                        uint64_t step, int64_t row_offset, int32_t* accepted, int32_t* tokens, float* token_logprobs,
+                        int32_t* row_status, void* stream);
 
 /*
  * Realized-size packing of captured supports ("[Sampling] Stream sampling masks as per-request

@@ -22,3 +22,5 @@ from .sfc_oracle import (  # noqa: F401
 )
 from .replay import ROW_OUTSIDE, ReplayResult, replay_logprob, replay_row  # noqa: F401
 from .pack import pack_supports  # noqa: F401
+from .distill import DistillResult, distill, replay_gradient  # noqa: F401
+from .verify import VerifyResult, verify_drafts, verify_supports  # noqa: F401

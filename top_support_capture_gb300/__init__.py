@@ -29,13 +29,16 @@ FLAG_GREEDY_T0 = 1
 FLAG_POSITIONAL = 2
 FLAG_MIN_P_FIRST = 4
 FLAG_TEST_STALL = 8
+FLAG_NORMALISE_TEACHER = 16
 MAX_PACKED_WIDTH = 16384
+MAX_DRAFTS = 64
 
 MAX_SLICES = 8
 
 EXPORTED = ("sfc_sample_filter_capture", "sfc_sample_filter_capture_ex", "sfc_workspace_size",
             "sfc_workspace_size_ex", "sfc_strerror", "sfc_replay_logprob", "sfc_pack_supports",
-            "sfc_sample_filter_capture_noalloc")
+            "sfc_sample_filter_capture_noalloc", "sfc_replay_backward", "sfc_distill_forward", "sfc_distill_backward",
+            "sfc_distill_forward_backward", "sfc_verify_workspace_size", "sfc_verify_drafts", "sfc_verify_supports")
 STATIC_SCRATCH_BYTES = 5 * 1024 * 1024
 
 _lib = None
@@ -92,6 +95,40 @@ def load_library() -> ctypes.CDLL:
         c.c_void_p, c.c_void_p, c.c_void_p, c.c_int32, c.c_void_p,  # temperature, ids, lengths, W, tokens
         c.c_void_p, c.c_void_p, c.c_void_p, c.c_void_p,  # token_logprob, support_logprobs, row_status, stream
     ]
+    rows = [c.c_void_p, c.c_int, c.c_int64, c.c_int64, c.c_int64, c.c_void_p]  # logits, dtype, B, V, stride, temperature
+    lib.sfc_replay_backward.restype = c.c_int
+    lib.sfc_replay_backward.argtypes = rows + [
+        c.c_void_p, c.c_void_p, c.c_int32, c.c_void_p,  # ids, lengths, W, tokens
+        c.c_void_p, c.c_void_p, c.c_void_p, c.c_int64, c.c_void_p,  # grad_token, grad_entries, grad, stride, stream
+    ]
+    teacher = [c.c_void_p, c.c_void_p, c.c_void_p, c.c_int32, c.c_uint32]  # ids, values, lengths, W, flags
+    lib.sfc_distill_forward.restype = c.c_int
+    lib.sfc_distill_forward.argtypes = rows + teacher + [c.c_void_p] * 4  # loss, row_stats, row_status, stream
+    lib.sfc_distill_backward.restype = c.c_int
+    lib.sfc_distill_backward.argtypes = rows + teacher + [
+        c.c_void_p, c.c_void_p, c.c_void_p, c.c_int64, c.c_void_p,  # row_stats, grad_loss, grad, stride, stream
+    ]
+    lib.sfc_distill_forward_backward.restype = c.c_int
+    lib.sfc_distill_forward_backward.argtypes = rows + teacher + [
+        c.c_void_p, c.c_void_p, c.c_void_p, c.c_void_p, c.c_int64, c.c_void_p,  # grad_loss, loss, status, grad, stride, stream
+    ]
+    lib.sfc_verify_workspace_size.restype = c.c_size_t
+    lib.sfc_verify_workspace_size.argtypes = [c.c_int64, c.c_int32, c.c_int64, c.c_int]
+    outputs = [c.c_void_p] * 4  # accepted, tokens, token_logprobs, row_status
+    lib.sfc_verify_drafts.restype = c.c_int
+    lib.sfc_verify_drafts.argtypes = [
+        c.c_void_p, c.c_void_p, c.c_int, c.c_int64, c.c_int32, c.c_int64,  # target, draft, dtype, B, D, V
+        c.c_int64, c.c_int64, c.c_int64, c.c_int64, c.c_void_p, c.c_void_p,  # strides, temperature, draft_temperature
+        c.c_void_p, c.c_void_p, c.c_void_p,  # draft_tokens, num_drafts, uniforms
+        c.c_uint64, c.c_uint64, c.c_int64, c.c_uint32,  # seed, step, row_offset, flags
+    ] + outputs + [c.c_void_p, c.c_size_t, c.c_void_p]  # workspace, bytes, stream
+    lib.sfc_verify_supports.restype = c.c_int
+    lib.sfc_verify_supports.argtypes = [
+        c.c_void_p, c.c_void_p, c.c_void_p, c.c_int32,  # target ids, logprobs, lengths, width
+        c.c_void_p, c.c_void_p, c.c_void_p, c.c_int32,  # draft ids, logprobs, lengths, width
+        c.c_int64, c.c_int32, c.c_void_p, c.c_void_p, c.c_void_p,  # B, D, draft_tokens, num_drafts, uniforms
+        c.c_uint64, c.c_uint64, c.c_int64,  # seed, step, row_offset
+    ] + outputs + [c.c_void_p]
     _lib = lib
     return lib
 
@@ -156,6 +193,22 @@ def _default_workspace(nbytes: int, device, stream):
         ws = allocate_workspace(nbytes, device)
         _workspaces[key] = ws
     return ws
+
+
+def _enter(device, stream):
+    """(stream, context): the stream to launch on (the current one when None) and what to allocate and launch
+    under, so that outputs belong to the stream that writes them. Nothing is switched where nothing differs."""
+    import contextlib
+
+    import torch
+
+    if stream is None and device.index == torch.cuda.current_device():
+        return torch.cuda.current_stream(device), contextlib.nullcontext()
+    context = contextlib.ExitStack()
+    context.enter_context(torch.cuda.device(device))
+    stream = torch.cuda.current_stream(device) if stream is None else stream
+    context.enter_context(torch.cuda.stream(stream))
+    return stream, context
 
 
 def _check_tensor(name, t, device, dtype, numel=None, shape=None):
@@ -312,9 +365,15 @@ class ReplayOutput(NamedTuple):
 def replay_logprob(logits, temperature, support_ids, lengths, tokens, support_logprobs: bool = False,
                    stream=None) -> ReplayOutput:
     """The sampled tokens' log-probabilities under ``logits`` [B, V] (bf16/f32 CUDA) renormalised over
-    captured supports ``support_ids`` [B, W] int32 with ``lengths`` [B] int32 (see include/sfc.h)."""
+    captured supports ``support_ids`` [B, W] int32 with ``lengths`` [B] int32 (see include/sfc.h).
+    Differentiable in ``logits`` (through ``replay_logprob_backward``): a row with status OVERFLOW or BADPARAM
+    passes no gradient on, nor does the token of an OUTSIDE row."""
     import torch
 
+    if torch.is_grad_enabled() and logits.requires_grad:
+        from .training import differentiable_replay
+
+        return differentiable_replay(logits, temperature, support_ids, lengths, tokens, support_logprobs, stream)
     lib = load_library()
     if logits.dim() != 2 or not logits.is_cuda or logits.stride(1) != 1:
         raise SfcError("logits must be a CUDA [B, V] tensor with contiguous rows")
@@ -373,3 +432,21 @@ def pack_supports_into(lengths, support_ids, support_logprobs, offsets, ids_out,
                                    B, W, _ptr(offsets), _ptr(ids_out), _ptr(lps_out), cap, int(stream.cuda_stream))
     if rc != SFC_OK:
         raise SfcError(f"sfc_pack_supports: {strerror(rc)} ({rc})")
+
+
+# The consumers of captured supports live in modules of their own, loaded on first use (they import torch).
+_MODULES = {
+    "training": ("DistillOutput", "DistillGradOutput", "distill_loss", "distill_loss_and_grad", "replay_logprob_backward"),
+    "speculative": ("VerifyOutput", "verify_drafts", "verify_supports", "verify_workspace_size"),
+}
+
+
+def __getattr__(name):
+    import importlib
+
+    for module, names in _MODULES.items():
+        if name in names:
+            value = getattr(importlib.import_module("." + module, __name__), name)
+            globals()[name] = value
+            return value
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

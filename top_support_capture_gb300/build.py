@@ -16,7 +16,7 @@ CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "libsfc.so")
 BUILD_DIR = os.path.join(HERE, "_build")
 SOURCES = ["sfc_api.cu", "sfc_launch_bf16.cu", "sfc_launch_f32.cu", "sfc_replay.cu", "sfc_pack.cu",
-           "sfc_noalloc.cu"]
+           "sfc_noalloc.cu", "sfc_replay_backward.cu", "sfc_distill.cu", "sfc_verify.cu", "sfc_verify_supports.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr"]
 # Shared cudart: when PyTorch is loaded first, its libcudart.so.13 is reused (one runtime instance,

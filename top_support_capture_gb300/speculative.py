@@ -1,0 +1,169 @@
+"""Verification of drafted tokens against the target's distributions: over full logit rows, and over captured
+supports (the filtered distributions that the decode step captured).
+
+Like the rest of the binding this only checks and marshals arguments (include/sfc.h has the rule).
+"""
+from __future__ import annotations
+
+from typing import NamedTuple
+
+import torch
+
+from . import (FLAG_GREEDY_T0, MAX_DRAFTS, MAX_PACKED_WIDTH, SFC_OK, SfcError, _check_tensor, _dtype_code, _enter, _ptr,
+               allocate_workspace, load_library, strerror)
+
+
+class VerifyOutput(NamedTuple):
+    accepted: "object"  # int32 [B]
+    tokens: "object"  # int32 [B, D + 1]: the accepted drafts, the drawn token, then -1
+    token_logprobs: "object"  # float32 [B, D + 1]
+    row_status: "object"  # int32 [B]
+
+
+# Workspaces the binding supplies when the caller passes none: one per (device, stream).
+_workspaces = {}
+
+
+def verify_workspace_size(B: int, D: int, V: int, dtype: int) -> int:
+    """Bytes of workspace that ``verify_drafts`` needs: zero-filled before its first use, one call at a time."""
+    return int(load_library().sfc_verify_workspace_size(B, D, V, dtype))
+
+
+def _workspace(nbytes, device, stream):
+    key = (device.index, int(stream.cuda_stream))
+    ws = _workspaces.get(key)
+    if ws is None or ws.numel() < nbytes:
+        if torch.cuda.is_current_stream_capturing():
+            raise SfcError("a CUDA graph is being captured and no workspace of this size exists for the stream: "
+                           "pass workspace= (allocate_workspace(verify_workspace_size(...))) or call once before capture")
+        ws = allocate_workspace(nbytes, device)
+        _workspaces[key] = ws
+    return ws
+
+
+def check_positions(name, t, B, positions):
+    """[B, positions, V] logits whose rows are contiguous (the rows may lie anywhere: they are only read);
+    returns (V, request stride, row stride)."""
+    if t.dim() != 3 or int(t.shape[0]) != B or int(t.shape[1]) != positions or t.shape[2] < 1:
+        raise SfcError(f"{name} must be [{B}, {positions}, V], got {tuple(t.shape)}")
+    _dtype_code(t)
+    if t.stride(2) != 1 and t.shape[2] > 1:
+        raise SfcError(f"{name} rows must be contiguous")
+    return int(t.shape[2]), int(t.stride(0)), int(t.stride(1))
+
+
+def check_drafts(draft_tokens, uniforms, num_drafts, device):
+    """[B, D] drafted tokens and uniforms, [B] counts; returns (B, D)."""
+    if draft_tokens.dim() != 2 or draft_tokens.shape[0] < 1:
+        raise SfcError("draft_tokens must be a non-empty [B, D] tensor")
+    B, D = int(draft_tokens.shape[0]), int(draft_tokens.shape[1])
+    if D < 1 or D > MAX_DRAFTS:
+        raise SfcError(f"draft_tokens must hold 1 to {MAX_DRAFTS} drafts a request, got {D}")
+    _check_tensor("draft_tokens", draft_tokens, device, torch.int32)
+    _check_tensor("uniforms", uniforms, device, torch.float32, shape=(B, D))
+    _check_tensor("num_drafts", num_drafts, device, torch.int32, numel=B)
+    return B, D
+
+
+def _outputs(B, D, dev):
+    return VerifyOutput(torch.empty(B, dtype=torch.int32, device=dev), torch.empty((B, D + 1), dtype=torch.int32, device=dev),
+                        torch.empty((B, D + 1), dtype=torch.float32, device=dev), torch.empty(B, dtype=torch.int32, device=dev))
+
+
+def _u64(x):
+    return int(x) & 0xFFFFFFFFFFFFFFFF
+
+
+def verify_drafts(target_logits, draft_logits, draft_tokens, uniforms, temperature, seed: int, step: int,
+                  draft_temperature=None, num_drafts=None, greedy_t0: bool = False, row_offset: int = 0, workspace=None,
+                  stream=None) -> VerifyOutput:
+    """Accept or refuse ``draft_tokens`` [B, D] int32 against ``target_logits`` [B, D + 1, V] (bf16/f32 CUDA) and
+    draw the token that follows. ``draft_logits`` [B, D, V] are the rows that the drafts were drawn from, None for
+    drafts that were not drawn (looked up); ``uniforms`` [B, D] f32 in [0, 1) decide; ``temperature`` [B] f32 (and
+    ``draft_temperature``, the same when omitted); ``num_drafts`` [B] int32 for requests with fewer than D drafts;
+    ``greedy_t0`` makes rows of temperature 0 greedy; ``seed``, ``step`` and ``row_offset`` key the draw's noise.
+    The workspace may be omitted: the binding then keeps one per device and stream. See include/sfc.h."""
+    if not target_logits.is_cuda:
+        raise SfcError(f"target_logits must be a CUDA tensor, got {target_logits.device}")
+    dev = target_logits.device
+    B, D, V, strides = check_verify_layout(target_logits, draft_logits, draft_tokens, uniforms, temperature, draft_temperature,
+                                           num_drafts)
+    dt = _dtype_code(target_logits)
+    lib = load_library()
+    stream, context = _enter(dev, stream)
+    with context:
+        if workspace is None:
+            workspace = _workspace(verify_workspace_size(B, D, V, dt), dev, stream)
+        _check_tensor("workspace", workspace, dev, workspace.dtype)
+        out = _outputs(B, D, dev)
+        rc = lib.sfc_verify_drafts(_ptr(target_logits), _ptr(draft_logits), dt, B, D, V, *strides, _ptr(temperature),
+                                   _ptr(draft_temperature), _ptr(draft_tokens), _ptr(num_drafts), _ptr(uniforms), _u64(seed),
+                                   _u64(step), int(row_offset), FLAG_GREEDY_T0 if greedy_t0 else 0, _ptr(out.accepted),
+                                   _ptr(out.tokens), _ptr(out.token_logprobs), _ptr(out.row_status), _ptr(workspace),
+                                   workspace.numel() * workspace.element_size(), int(stream.cuda_stream))
+    if rc != SFC_OK:
+        raise SfcError(f"sfc_verify_drafts: {strerror(rc)} ({rc})")
+    return out
+
+
+def check_verify_layout(target_logits, draft_logits, draft_tokens, uniforms, temperature, draft_temperature, num_drafts):
+    """The host-side checks of ``verify_drafts``; returns (B, D, V, the four strides)."""
+    dev = target_logits.device
+    B, D = check_drafts(draft_tokens, uniforms, num_drafts, dev)
+    V, request, row = check_positions("target_logits", target_logits, B, D + 1)
+    strides = [request, row, 0, 0]
+    if draft_logits is not None:
+        if draft_logits.device != dev or draft_logits.dtype != target_logits.dtype:
+            raise SfcError("draft_logits must have the target logits' device and dtype")
+        Vd, strides[2], strides[3] = check_positions("draft_logits", draft_logits, B, D)
+        if Vd != V:
+            raise SfcError(f"draft_logits must have the target's vocabulary of {V}, got {Vd}")
+    if temperature is None:
+        raise SfcError("temperature is required")
+    _check_tensor("temperature", temperature, dev, torch.float32, numel=B)
+    _check_tensor("draft_temperature", draft_temperature, dev, torch.float32, numel=B)
+    return B, D, V, strides
+
+
+def verify_supports(target_ids, target_logprobs, target_lengths, draft_ids, draft_logprobs, draft_lengths, draft_tokens,
+                    uniforms, seed: int, step: int, num_drafts=None, row_offset: int = 0, stream=None) -> VerifyOutput:
+    """``verify_drafts`` over captured supports: ``target_ids`` / ``target_logprobs`` [B, D + 1, W] and
+    ``target_lengths`` [B, D + 1] as the decode step wrote them for the target's rows, ``draft_*`` [B, D, Wd] and
+    [B, D] for the draft's (None, or a length of 0: a draft that was not drawn). See include/sfc.h."""
+    if not target_ids.is_cuda:
+        raise SfcError(f"target_ids must be a CUDA tensor, got {target_ids.device}")
+    dev = target_ids.device
+    B, D, W, Wd = check_supports_layout(target_ids, target_logprobs, target_lengths, draft_ids, draft_logprobs, draft_lengths,
+                                        draft_tokens, uniforms, num_drafts)
+    lib = load_library()
+    stream, context = _enter(dev, stream)
+    with context:
+        out = _outputs(B, D, dev)
+        rc = lib.sfc_verify_supports(_ptr(target_ids), _ptr(target_logprobs), _ptr(target_lengths), W, _ptr(draft_ids),
+                                     _ptr(draft_logprobs), _ptr(draft_lengths), Wd, B, D, _ptr(draft_tokens), _ptr(num_drafts),
+                                     _ptr(uniforms), _u64(seed), _u64(step), int(row_offset), _ptr(out.accepted),
+                                     _ptr(out.tokens), _ptr(out.token_logprobs), _ptr(out.row_status), int(stream.cuda_stream))
+    if rc != SFC_OK:
+        raise SfcError(f"sfc_verify_supports: {strerror(rc)} ({rc})")
+    return out
+
+
+def check_supports_layout(target_ids, target_logprobs, target_lengths, draft_ids, draft_logprobs, draft_lengths, draft_tokens,
+                          uniforms, num_drafts):
+    """The host-side checks of ``verify_supports``; returns (B, D, the target's width, the draft's or 0)."""
+    dev = target_ids.device
+    B, D = check_drafts(draft_tokens, uniforms, num_drafts, dev)
+
+    def rows(side, ids, lps, lengths, positions):
+        if ids.dim() != 3 or lps is None or lengths is None:
+            raise SfcError(f"{side} supports need ids and logprobs [B, positions, W] and lengths")
+        W = int(ids.shape[2])
+        if W < 1 or W > MAX_PACKED_WIDTH:
+            raise SfcError(f"{side}_ids must be 1 to {MAX_PACKED_WIDTH} wide, got {W}")
+        _check_tensor(f"{side}_ids", ids, dev, torch.int32, shape=(B, positions, W))
+        _check_tensor(f"{side}_logprobs", lps, dev, torch.float32, shape=(B, positions, W))
+        _check_tensor(f"{side}_lengths", lengths, dev, torch.int32, shape=(B, positions))
+        return W
+
+    W = rows("target", target_ids, target_logprobs, target_lengths, D + 1)
+    return B, D, W, 0 if draft_ids is None else rows("draft", draft_ids, draft_logprobs, draft_lengths, D)

@@ -1,0 +1,214 @@
+"""Training against captured supports: distillation from a teacher's top logits, and the replay's gradient.
+
+Like the rest of the binding this only checks and marshals arguments (include/sfc.h has the formulas). The
+functions ending in ``_backward`` / ``_and_grad`` take no part in autograd: a training step that is captured
+into a CUDA graph uses those. (Autograd's own bookkeeping is not made for a captured backward pass while an
+eager graph over the same leaves is alive.)
+"""
+from __future__ import annotations
+
+from typing import NamedTuple
+
+import torch
+
+from . import (FLAG_NORMALISE_TEACHER, MAX_PACKED_WIDTH, SFC_OK, ReplayOutput, SfcError, _check_tensor, _dtype_code, _enter, _ptr,
+               load_library, replay_logprob, strerror)
+
+
+class DistillOutput(NamedTuple):
+    loss: "object"  # float32 [B]
+    row_status: "object"  # int32 [B]
+
+
+class DistillGradOutput(NamedTuple):
+    loss: "object"  # float32 [B]
+    grad_logits: "object"  # [B, V], the logits' dtype
+    row_status: "object"  # int32 [B]
+
+
+def check_rows(name, t):
+    """[B, V] rows of a CUDA tensor, each contiguous."""
+    if not t.is_cuda:
+        raise SfcError(f"{name} must be a CUDA tensor, got {t.device}")
+    check_row_layout(name, t)
+
+
+def check_row_layout(name, t):
+    """A floating [B, V] tensor whose rows are contiguous and do not overlap; returns the row stride."""
+    if t.dim() != 2 or t.shape[0] < 1 or t.shape[1] < 1:
+        raise SfcError(f"{name} must be a non-empty [B, V] tensor")
+    _dtype_code(t)
+    if t.stride(1) != 1 and t.shape[1] > 1:
+        raise SfcError(f"{name} rows must be contiguous")
+    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+        raise SfcError(f"{name} rows must not overlap (an expanded tensor: make it contiguous)")
+    return int(t.stride(0)) if t.shape[0] > 1 else max(int(t.stride(0)), int(t.shape[1]))
+
+
+def check_packed(logits, temperature, ids, lengths, values=None, values_name="teacher_values", ids_name="teacher_ids"):
+    """The packed per-row arrays beside [B, V] logits, as the kernels assume them; returns W."""
+    dev, B = logits.device, int(logits.shape[0])
+    if ids.dim() != 2 or int(ids.shape[0]) != B:
+        raise SfcError(f"{ids_name} must be [B, W]")
+    W = int(ids.shape[1])
+    if W < 1 or W > MAX_PACKED_WIDTH:
+        raise SfcError(f"{ids_name} must be 1 to {MAX_PACKED_WIDTH} wide, got {W}")
+    _check_tensor(ids_name, ids, dev, torch.int32, shape=(B, W))
+    _check_tensor("temperature", temperature, dev, torch.float32, numel=B)
+    _check_tensor("lengths", lengths, dev, torch.int32, numel=B)
+    _check_tensor(values_name, values, dev, torch.float32, shape=(B, W))
+    return W
+
+
+def _raise(name, rc):
+    if rc != SFC_OK:
+        raise SfcError(f"{name}: {strerror(rc)} ({rc})")
+
+
+def _check_grad(grad, logits):
+    check_row_layout("grad", grad)
+    if grad.device != logits.device or grad.dtype != logits.dtype or grad.shape != logits.shape:
+        raise SfcError("grad must have the logits' device, dtype and shape")
+
+
+def _rows_args(logits, temperature):
+    B, V = int(logits.shape[0]), int(logits.shape[1])
+    return _ptr(logits), _dtype_code(logits), B, V, check_row_layout("logits", logits), _ptr(temperature)
+
+
+def _teacher_args(ids, values, lengths, normalise):
+    return _ptr(ids), _ptr(values), _ptr(lengths), int(ids.shape[1]), FLAG_NORMALISE_TEACHER if normalise else 0
+
+
+def _distill_forward(logits, temperature, ids, values, lengths, normalise, stream, keep_stats):
+    dev, B = logits.device, int(logits.shape[0])
+    stream, context = _enter(dev, stream)
+    with context:
+        loss = torch.empty(B, dtype=torch.float32, device=dev)
+        stats = torch.empty((B, 4), dtype=torch.float32, device=dev) if keep_stats else None
+        status = torch.empty(B, dtype=torch.int32, device=dev)
+        rc = load_library().sfc_distill_forward(*_rows_args(logits, temperature), *_teacher_args(ids, values, lengths, normalise),
+                                                _ptr(loss), _ptr(stats), _ptr(status), int(stream.cuda_stream))
+    _raise("sfc_distill_forward", rc)
+    return loss, stats, status
+
+
+class _Distill(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, temperature, ids, values, lengths, normalise):
+        loss, stats, status = _distill_forward(logits, temperature, ids, values, lengths, normalise, None, True)
+        ctx.save_for_backward(logits, temperature, ids, values, lengths, stats)
+        ctx.normalise = normalise
+        ctx.mark_non_differentiable(status)
+        return loss, status
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad_loss, _):
+        logits, temperature, ids, values, lengths, stats = ctx.saved_tensors
+        dev = logits.device
+        stream, context = _enter(dev, None)  # autograd runs a backward on its forward's stream
+        with context:
+            grad_loss = grad_loss.to(torch.float32).contiguous()
+            grad = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
+            rc = load_library().sfc_distill_backward(*_rows_args(logits, temperature),
+                                                     *_teacher_args(ids, values, lengths, ctx.normalise), _ptr(stats),
+                                                     _ptr(grad_loss), _ptr(grad), int(logits.shape[1]), int(stream.cuda_stream))
+        _raise("sfc_distill_backward", rc)
+        return grad, None, None, None, None, None
+
+
+def distill_loss(logits, temperature, teacher_ids, teacher_values, lengths, normalise: bool = False,
+                 stream=None) -> DistillOutput:
+    """Per-row distillation losses of a student's ``logits`` [B, V] (bf16/f32 CUDA) against packed teachers:
+    ``teacher_ids`` [B, W] int32 with ``teacher_values`` [B, W] f32, log-probabilities (a capture's
+    ``support_ids`` and ``support_logprobs``) or, with ``normalise``, raw top logits; ``lengths`` [B] int32 (0:
+    the row has no teacher). Differentiable in ``logits``. See include/sfc.h."""
+    check_rows("logits", logits)
+    check_packed(logits, temperature, teacher_ids, lengths, teacher_values)
+    if teacher_values is None:
+        raise SfcError("teacher_values is required")
+    if torch.is_grad_enabled() and logits.requires_grad:
+        stream, context = _enter(logits.device, stream)
+        with context:
+            return DistillOutput(*_Distill.apply(logits, temperature, teacher_ids, teacher_values, lengths, bool(normalise)))
+    loss, _, status = _distill_forward(logits, temperature, teacher_ids, teacher_values, lengths, normalise, stream, False)
+    return DistillOutput(loss, status)
+
+
+def distill_loss_and_grad(logits, temperature, teacher_ids, teacher_values, lengths, grad_loss, normalise: bool = False,
+                          grad=None, stream=None) -> DistillGradOutput:
+    """``distill_loss`` and its gradient in one call, for a known upstream gradient ``grad_loss`` [B] f32 (a mean
+    over the batch: 1 / B each): the logits are read once. ``grad`` may give the [B, V] tensor to write (not the
+    logits themselves). Outside autograd."""
+    check_rows("logits", logits)
+    check_packed(logits, temperature, teacher_ids, lengths, teacher_values)
+    if teacher_values is None:
+        raise SfcError("teacher_values is required")
+    dev, B = logits.device, int(logits.shape[0])
+    _check_tensor("grad_loss", grad_loss, dev, torch.float32, numel=B)
+    if grad is not None:
+        _check_grad(grad, logits)
+    stream, context = _enter(dev, stream)
+    with context:
+        loss = torch.empty(B, dtype=torch.float32, device=dev)
+        status = torch.empty(B, dtype=torch.int32, device=dev)
+        if grad is None:
+            grad = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
+        rc = load_library().sfc_distill_forward_backward(
+            *_rows_args(logits, temperature), *_teacher_args(teacher_ids, teacher_values, lengths, normalise), _ptr(grad_loss),
+            _ptr(loss), _ptr(status), _ptr(grad), check_row_layout("grad", grad), int(stream.cuda_stream))
+    _raise("sfc_distill_forward_backward", rc)
+    return DistillGradOutput(loss, grad, status)
+
+
+def replay_logprob_backward(logits, temperature, support_ids, lengths, tokens, grad_token_logprob,
+                            grad_support_logprobs=None, grad=None, stream=None):
+    """The gradient of ``replay_logprob`` with respect to ``logits`` [B, V], from the upstream gradients
+    ``grad_token_logprob`` [B] f32 and, where it is given, ``grad_support_logprobs`` [B, W] f32: a dense
+    [B, V] tensor of the logits' dtype, zero outside the supports (written into ``grad`` when that is given)."""
+    check_rows("logits", logits)
+    dev, B = logits.device, int(logits.shape[0])
+    W = check_packed(logits, temperature, support_ids, lengths, grad_support_logprobs, "grad_support_logprobs", "support_ids")
+    _check_tensor("tokens", tokens, dev, torch.int32, numel=B)
+    _check_tensor("grad_token_logprob", grad_token_logprob, dev, torch.float32, numel=B)
+    if grad is not None:
+        _check_grad(grad, logits)
+    stream, context = _enter(dev, stream)
+    with context:
+        if grad is None:
+            grad = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
+        rc = load_library().sfc_replay_backward(*_rows_args(logits, temperature), _ptr(support_ids), _ptr(lengths), W,
+                                                _ptr(tokens), _ptr(grad_token_logprob), _ptr(grad_support_logprobs),
+                                                _ptr(grad), check_row_layout("grad", grad), int(stream.cuda_stream))
+    _raise("sfc_replay_backward", rc)
+    return grad
+
+
+class _Replay(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, temperature, support_ids, lengths, tokens, support_logprobs):
+        out = replay_logprob(logits.detach(), temperature, support_ids, lengths, tokens, support_logprobs)
+        ctx.set_materialize_grads(False)
+        ctx.save_for_backward(logits, temperature, support_ids, lengths, tokens)
+        ctx.mark_non_differentiable(out.row_status)
+        return out.token_logprob, out.support_logprobs, out.row_status
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad_token, grad_entries, _):
+        logits, temperature, support_ids, lengths, tokens = ctx.saved_tensors
+        if grad_token is None and grad_entries is None:
+            return (None,) * 6
+        grad_token = torch.zeros_like(temperature) if grad_token is None else grad_token.to(torch.float32).contiguous()
+        if grad_entries is not None:
+            grad_entries = grad_entries.to(torch.float32).contiguous()
+        grad = replay_logprob_backward(logits.detach(), temperature, support_ids, lengths, tokens, grad_token, grad_entries)
+        return grad, None, None, None, None, None
+
+
+def differentiable_replay(logits, temperature, support_ids, lengths, tokens, support_logprobs, stream) -> ReplayOutput:
+    check_rows("logits", logits)
+    _, context = _enter(logits.device, stream)
+    with context:
+        return ReplayOutput(*_Replay.apply(logits, temperature, support_ids, lengths, tokens, support_logprobs))
