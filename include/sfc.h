@@ -276,8 +276,8 @@ int sfc_replay_backward(const void* logits, int dtype, int64_t B, int64_t V, int
  * temperature     [B] float32, finite and > 0.
  * teacher_ids     [B, W] int32, teacher_values [B, W] float32: entries j < lengths[r] are read; the ids must be
  *                 distinct — repeated ids give unspecified gradients.
- * lengths         [B] int32. 0: the row has no teacher (padding, a row that did not capture): its logits are not
- *                 read, its loss is 0 and its gradient 0. Above W: the first W entries are the teacher
+ * lengths         [B] int32. 0: the row has no teacher (padding, a row that did not capture): its logits do
+ *                 not matter, its loss is 0 and its gradient 0. Above W: the first W entries are the teacher
  *                 (a capture writes the largest first) and the status is SFC_ROW_OVERFLOW.
  * flags           0 or SFC_FLAG_NORMALISE_TEACHER; other bits: SFC_EINVAL.
  * loss            [B] float32 out; NaN on BADPARAM rows.

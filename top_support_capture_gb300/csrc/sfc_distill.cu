@@ -4,11 +4,19 @@
 //   z = x / T, ln p = z - ln sum_V exp z;  t_i = exp(y_i), or softmax over the row's entries of y_i / T
 //   loss = sum_i t_i (ln t_i - ln p_i),   dloss/dx_j = (tau p_j - t_j) / T,   tau = sum_i t_i
 //
-// One CTA per row: the statistics pass streams the row, the teacher's entries gather their logits, and the
-// gradient pass reads the row again (from L2 where it still lies there) and writes tau p_j g / T everywhere;
-// after a barrier the teacher's entries overwrite theirs with the whole gradient.
-#include <cuda_runtime.h>
-
+// A row is cut into slices of 16-byte vectors, one CTA each. In the calls that need the row's statistics the
+// slices of a row form a thread-block cluster: each CTA stores its share of the statistics into every CTA of the
+// cluster (distributed shared memory), and after the cluster's barrier each merges the shares in slice order, so
+// all hold the same bits. The teacher's mass is small work: every CTA sums it for itself.
+//
+// In the call that gives loss and gradient the slice stays in shared memory between its two uses, so the logits are
+// read from HBM once: each thread copies its own vectors there asynchronously (cp.async, no barrier needed) before
+// anything else. Rows longer than a cluster's shared memory are read again.
+//
+// The gradient's dense part tau p_j g / T is written first; after the CTA's barrier the teacher's entries that lie
+// in the slice overwrite theirs with the whole gradient, each rounded once, and add their part of the loss.
+#include <algorithm>
+#include <climits>
 #include <cstdint>
 
 #include "../../include/sfc.h"
@@ -32,12 +40,11 @@ struct DistillParams {
   int32_t* row_status;
   unsigned char* grad;
   int64_t grad_stride;
+  int32_t slices;
 };
 
-constexpr int kThreads = 512;
-
-// What the gradient needs of a row: its softmax (m, s) and its teacher's (y0, ty): t_i = exp((y_i - y0) a) / ty,
-// tau. m is NaN on rows that pass no gradient on (no teacher entry, bad parameters).
+// What the gradient needs of a row: its softmax (m, s) and its teacher's: t_i = exp((y_i - y0) / T_y) / ty, tau.
+// m is NaN on rows that pass no gradient on (no teacher entry, bad parameters).
 struct RowTerms {
   float m, s, tau, y0, ty;
 };
@@ -51,106 +58,226 @@ __device__ __forceinline__ RowTerms unpack_terms(const float4& v, bool normalise
   return normalise ? RowTerms{v.x, v.y, 1.f, v.z, v.w} : RowTerms{v.x, v.y, v.z, 0.f, 1.f};
 }
 
-template <int DT, bool FWD, bool BWD>
-__global__ void __launch_bounds__(kThreads) distill_kernel(const __grid_constant__ DistillParams p) {
-  constexpr int NW = kThreads / 32, VEC = Elem<DT>::kVec;
-  __shared__ float red[6 * NW];
-  const int tid = threadIdx.x;
-  const int64_t r = blockIdx.x;
+constexpr int kMaxSlices = 8;  // the portable cluster size
+constexpr int kGroups = 4;     // cp.async groups per thread: the statistics begin when the first has landed
+constexpr int kKeepBytes = 212992;  // shared memory of one SM that keeps logits: 13 vectors for each of 1024 threads
+constexpr int kPrefetch = 2;   // teacher entries per thread held from the start
+
+__device__ __forceinline__ void copy_async(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// KEEP: the slice's vectors lie in dynamic shared memory (16 bytes for each).
+template <int DT, int NT, int MINB, bool KEEP, bool FWD, bool BWD>
+__global__ void __launch_bounds__(NT, MINB) distill_kernel(const __grid_constant__ DistillParams p) {
+  constexpr int NW = NT / 32, VEC = Elem<DT>::kVec;
+  constexpr int kStream = BWD ? 4 : 8;  // vectors in flight per thread where they are not kept
+  extern __shared__ __align__(16) uint4 kept[];
+  __shared__ float2 red[2 * NW];
+  __shared__ float red_mass[NW], red_loss[NW];
+  __shared__ float2 table[kMaxSlices];  // (m, s) of the slices
+  __shared__ float losses[kMaxSlices];
+  const int tid = threadIdx.x, S = p.slices;
+  const int rank = static_cast<int>(blockIdx.x % static_cast<unsigned>(S));
+  const int64_t r = blockIdx.x / static_cast<unsigned>(S);
+  const RowSpan<DT> row(p.logits, r * p.row_stride, p.V);
+  const uint4* body = row.body();
+  const int nvec = static_cast<int>(row.nvec);
+  const int per = ((nvec + S - 1) / S + 7) & ~7;  // whole 128-byte lines
+  const int v0 = min(rank * per, nvec), v1 = min(v0 + per, nvec);
+  const bool scalar = rank == 0 && tid < row.scalars();
+  if (FWD && S > 1) cluster_arrive();  // its CTAs have started: waited for before the first store into another
+  const int quarter = (v1 - v0 + kGroups * NT - 1) / (kGroups * NT) * NT;  // vectors of one group
+  if (KEEP) {  // in flight while the row's parameters load
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) {
+      for (int k = g * quarter + tid; k < min((g + 1) * quarter, v1 - v0); k += NT) copy_async(kept + k, body + v0 + k);
+      copy_commit();
+    }
+  }
   const float T = p.temperature[r];
   const int len = p.lengths[r];
   const int n = min(max(len, 0), p.W);
   const int32_t* ids = p.ids + r * p.W;
   const float* values = p.values + r * p.W;
-  const RowSpan<DT> row(p.logits, r * p.row_stride, p.V);
-  const float c = exponent_scale(T);
-  const float ty_T = p.normalise ? T : 1.f;  // the teacher's temperature
-  RowTerms q;
-  bool live = true;  // the row has a teacher and passes its checks: uniform over the CTA
+  int32_t id[kPrefetch];
+  float y[kPrefetch];
+#pragma unroll
+  for (int e = 0; e < kPrefetch; ++e) {
+    const int j = tid + e * NT;
+    id[e] = j < n ? ids[j] : 0;
+    y[e] = j < n ? values[j] : -INFINITY;
+  }
+  const float c = exponent_scale(T), T_y = p.normalise ? T : 1.f;
+  RowTerms q{__int_as_float(0x7fc00000), 1.f, 0.f, 0.f, 1.f};
+  int status = SFC_ROW_OK;
+  bool live;  // the row has a teacher and passes its checks: uniform over its CTAs
   if (FWD) {
-    int status = len > p.W ? SFC_ROW_OVERFLOW : SFC_ROW_OK;
-    float loss = 0.f;
-    if (!temperature_valid(T) || len < 0) {
-      status = SFC_ROW_BADPARAM;
-    } else if (n > 0) {
-      SoftmaxAcc a = row_stats<DT, kThreads>(row, 0, row.nvec, true, c);
-      block_merge<kThreads>(a, c, red);
-      q = RowTerms{a.m, a.s, 0.f, 0.f, 1.f};
-      // the teacher's normaliser
-      int bad = !stats_valid(a.m, a.s);
-      if (p.normalise) {
-        SoftmaxAcc ta;
-        const float yc = exponent_scale(T);
-        for (int j = tid; j < n; j += kThreads) ta.add(values[j], yc);
-        block_merge<kThreads>(ta, yc, red + 2 * NW);
-        q.y0 = ta.m;
-        q.ty = ta.s;
-        bad |= !stats_valid(ta.m, ta.s);
-      }
-      const float ln_ty = logf(q.ty);
-      float sum[2] = {0.f, 0.f};  // tau, sum t (ln t - (x - m) / T)
-      for (int j = tid; j < n; j += kThreads) {
-        const int32_t id = ids[j];
-        const bool in = id >= 0 && id < p.V;
-        const float y = (values[j] - q.y0) / ty_T - ln_ty;
-        const float x = row.at(in ? id : 0);
-        bad |= !in || !(y < INFINITY);
-        const float t = expf(y);
-        sum[0] += t;
-        if (t > 0.f) sum[1] += t * (y - (x - a.m) / T);
-      }
-      bad = __syncthreads_or(bad);
-      block_sum<kThreads, 2>(sum, red + 4 * NW);
-      q.tau = p.normalise ? 1.f : sum[0];
-      loss = sum[1] + q.tau * logf(a.s);
-      if (bad) status = SFC_ROW_BADPARAM;
-    }
+    if (len > p.W) status = SFC_ROW_OVERFLOW;
+    if (!temperature_valid(T) || len < 0) status = SFC_ROW_BADPARAM;
     live = status != SFC_ROW_BADPARAM && n > 0;
-    if (!live) q.m = __int_as_float(0x7fc00000);
-    if (tid == 0) {
-      p.loss[r] = status == SFC_ROW_BADPARAM ? __int_as_float(0x7fc00000) : loss;
-      if (p.row_status) p.row_status[r] = status;
-      if (p.stats) p.stats[r] = pack_terms(q, p.normalise);
+    if (live) {
+      // the teacher: its mass, or its maximum and normaliser; an id outside the row makes it NaN
+      SoftmaxAcc a, t;
+      float mass = 0.f;
+      auto entry = [&](int32_t i, float v) {
+        if (i < 0 || i >= p.V) v = __int_as_float(0x7fc00000);
+        if (p.normalise) t.add(v, c);
+        else mass += expf(v);
+      };
+#pragma unroll
+      for (int e = 0; e < kPrefetch; ++e) entry(id[e], y[e]);
+      for (int j = tid + kPrefetch * NT; j < n; j += NT) entry(ids[j], values[j]);
+      auto fold = [&](const uint4& w) {
+        float x[VEC];
+        Elem<DT>::unpack(w, x);
+        a.add(x, Elem<DT>::vmax(w), c);
+      };
+      if (KEEP) {
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) {
+          if (g == 0) copy_wait<3>();
+          if (g == 1) copy_wait<2>();
+          if (g == 2) copy_wait<1>();
+          if (g == 3) copy_wait<0>();
+#pragma unroll 2
+          for (int k = g * quarter + tid; k < min((g + 1) * quarter, v1 - v0); k += NT) fold(kept[k]);
+        }
+      } else {
+        for (int k0 = v0 + tid; k0 < v1; k0 += NT * kStream) {
+          uint4 w[kStream];
+#pragma unroll
+          for (int u = 0; u < kStream; ++u) w[u] = k0 + u * NT < v1 ? ld_once(body + k0 + u * NT) : Elem<DT>::neg_inf_vec();
+#pragma unroll
+          for (int u = 0; u < kStream; ++u) fold(w[u]);
+        }
+      }
+      if (scalar) a.add(row.at(row.scalar_index(tid)), c);
+      const int lane = tid & 31, wp = tid >> 5;
+      const SoftmaxStats w = warp_stats(a, c);
+      if (lane == 0) red[wp] = make_float2(w.m, w.s);
+      if (p.normalise) {
+        const SoftmaxStats wt = warp_stats(t, c);
+        if (lane == 0) red[NW + wp] = make_float2(wt.m, wt.s);
+      } else {
+        mass = warp_total(mass);
+        if (lane == 0) red_mass[wp] = mass;
+      }
+      __syncthreads();
+      SoftmaxStats all = merge_warps<NT>(red, c);
+      if (S > 1) {
+        cluster_wait();
+        if (tid < S) dsmem_st64(dsmem_addr(&table[rank], tid), pack_f2(all.m, all.s));
+        cluster_sync_all();
+        all = SoftmaxStats{table[0].x, table[0].y};
+        for (int i = 1; i < S; ++i) all.merge(table[i].x, table[i].y, c);
+      }
+      q = RowTerms{all.m, all.s, 1.f, 0.f, 1.f};
+      live = stats_valid(all.m, all.s);
+      if (p.normalise) {
+        const SoftmaxStats teacher = merge_warps<NT>(red + NW, c);
+        q.y0 = teacher.m;
+        q.ty = teacher.s;
+        live = live && stats_valid(teacher.m, teacher.s);
+      } else {
+        q.tau = warp_total(lane < NW ? red_mass[lane] : 0.f);
+        live = live && q.tau < INFINITY;
+      }
+      if (!live) {
+        status = SFC_ROW_BADPARAM;
+        q.m = __int_as_float(0x7fc00000);
+      }
+    } else {
+      if (KEEP) copy_wait<0>();
+      if (S > 1) {
+        cluster_wait();
+        cluster_sync_all();
+      }
     }
   } else {
     q = unpack_terms(p.stats[r], p.normalise);
     live = q.m == q.m;
   }
-  if (!BWD) return;
-  unsigned char* grad = p.grad + r * p.grad_stride * Elem<DT>::kBytes;
-  const float g = live ? p.grad_loss[r] / T : 0.f;
-  const float k = live ? g * q.tau / q.s : 0.f;
-  const float m = live ? q.m : 0.f;
-  const bool same = ((reinterpret_cast<uintptr_t>(grad) ^ reinterpret_cast<uintptr_t>(row.row)) & 15) == 0;
-  if (!live) {
-    for (int64_t i = tid; i < p.V; i += kThreads) Out<DT>::store1(grad, i, 0.f);
-    return;
-  }
-  const uint4* body = row.body();
-  uint4* out = reinterpret_cast<uint4*>(grad + static_cast<int64_t>(row.head) * Elem<DT>::kBytes);
-  for (int64_t v = tid; v < row.nvec; v += kThreads) {
-    float x[VEC];
-    Elem<DT>::unpack(__ldg(body + v), x);
+  const float g = BWD && live ? p.grad_loss[r] / T : 0.f;
+  const float k = live ? g * q.tau / q.s : 0.f, m = q.m;
+  unsigned char* grad = BWD ? p.grad + r * p.grad_stride * Elem<DT>::kBytes : nullptr;
+  if (BWD) {
+    const bool same = ((reinterpret_cast<uintptr_t>(grad) ^ reinterpret_cast<uintptr_t>(row.row)) & 15) == 0;
+    uint4* out = reinterpret_cast<uint4*>(grad + static_cast<int64_t>(row.head) * Elem<DT>::kBytes);
+    const uint64_t minus_m2 = pack_f2(-m, -m), c2 = pack_f2(c, c), k2 = pack_f2(k, k);
+    auto put = [&](int at, const uint4& w) {
+      float x[VEC];
+      Elem<DT>::unpack(w, x);
+      uint64_t e2[VEC / 2];
+      exponentials(x, minus_m2, c2, e2);
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) x[e] = k * ex2_approx((x[e] - m) * c);
-    if (same) {
-      out[v] = Out<DT>::pack(x);
+      for (int e = 0; e < VEC / 2; ++e) unpack_f2(fmul_f2(e2[e], k2), x[2 * e], x[2 * e + 1]);
+      if (!live) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) x[e] = 0.f;
+      }
+      if (same) {
+        out[at] = Out<DT>::pack(x);
+      } else {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) Out<DT>::store1(grad, row.head + static_cast<int64_t>(at) * VEC + e, x[e]);
+      }
+    };
+    if (KEEP) {
+#pragma unroll 2
+      for (int i = tid; i < v1 - v0; i += NT) put(v0 + i, kept[i]);
     } else {
+      for (int k0 = v0 + tid; k0 < v1; k0 += NT * kStream) {
+        uint4 w[kStream];
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) Out<DT>::store1(grad, row.head + v * VEC + e, x[e]);
+        for (int u = 0; u < kStream; ++u)
+          if (k0 + u * NT < v1) w[u] = ld_once(body + k0 + u * NT);
+#pragma unroll
+        for (int u = 0; u < kStream; ++u)
+          if (k0 + u * NT < v1) put(k0 + u * NT, w[u]);
+      }
     }
+    if (scalar) {
+      const int64_t i = row.scalar_index(tid);
+      Out<DT>::store1(grad, i, live ? k * ex2_approx((row.at(i) - m) * c) : 0.f);
+    }
+    if (live) __syncthreads();  // the dense values are written before the teacher's entries overwrite theirs
   }
-  if (tid < row.scalars()) {
-    const int64_t i = row.scalar_index(tid);
-    Out<DT>::store1(grad, i, k * ex2_approx((row.at(i) - m) * c));
+  float loss = 0.f;
+  if (live) {
+    const float ln_ty = logf(q.ty);
+    const int64_t lo = row.head + static_cast<int64_t>(v0) * VEC, hi = row.head + static_cast<int64_t>(v1) * VEC;
+    auto entry = [&](int32_t i, float v) {
+      const bool body_entry = i >= lo && i < hi;
+      if (!body_entry && !(rank == 0 && (i < row.head || i >= row.tail()))) return;
+      const float ln_t = (v - q.y0) / T_y - ln_ty, e = expf(ln_t);
+      const float x = KEEP && body_entry ? Elem<DT>::load1(reinterpret_cast<const unsigned char*>(kept), i - lo) : row.at(i);
+      if (FWD && e > 0.f) loss += e * (ln_t - (x - m) / T);
+      if (BWD) Out<DT>::store1(grad, i, k * ex2_approx((x - m) * c) - e * g);
+    };
+#pragma unroll
+    for (int e = 0; e < kPrefetch; ++e)
+      if (tid + e * NT < n) entry(id[e], y[e]);
+    for (int j = tid + kPrefetch * NT; j < n; j += NT) entry(ids[j], values[j]);
   }
-  __syncthreads();  // the dense values are written before the teacher's entries overwrite theirs
-  const float ln_ty = logf(q.ty);
-  for (int j = tid; j < n; j += kThreads) {
-    const int32_t id = ids[j];
-    if (id < 0 || id >= p.V) continue;
-    const float t = expf((values[j] - q.y0) / ty_T - ln_ty);
-    Out<DT>::store1(grad, id, k * ex2_approx((row.at(id) - m) * c) - t * g);
+  if (!FWD) return;
+  loss = block_total<NT>(loss, red_loss);
+  if (S > 1) {
+    if (tid == 0) dsmem_st32(dsmem_addr(&losses[rank], 0), __float_as_uint(loss));
+    cluster_sync_all();
+    if (rank != 0) return;
+    loss = losses[0];
+    for (int i = 1; i < S; ++i) loss += losses[i];
+  }
+  if (tid == 0) {
+    p.loss[r] = live ? loss + q.tau * logf(q.s) : (status == SFC_ROW_BADPARAM ? __int_as_float(0x7fc00000) : 0.f);
+    p.row_status[r] = status;
+    if (p.stats) p.stats[r] = pack_terms(q, p.normalise);
   }
 }
 
@@ -176,15 +303,54 @@ int check_grad(const void* logits, int dtype, int64_t B, int64_t V, int64_t row_
   return g < l_end && l < g_end ? SFC_EINVAL : SFC_OK;
 }
 
+template <int DT, int NT, int MINB, bool KEEP, bool FWD, bool BWD>
+cudaError_t start(const DistillParams& p, int64_t B, cudaStream_t stream) {
+  auto kern = distill_kernel<DT, NT, MINB, KEEP, FWD, BWD>;
+  cudaLaunchConfig_t cfg = {};
+  if (KEEP) {
+    const int64_t vectors = p.V / Elem<DT>::kVec;
+    cfg.dynamicSmemBytes = static_cast<size_t>(((vectors + p.slices - 1) / p.slices + 7) & ~int64_t{7}) * 16;
+    const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kKeepBytes / MINB);
+    if (err != cudaSuccess) return err;
+  }
+  cfg.gridDim = dim3(static_cast<unsigned>(B * p.slices));
+  cfg.blockDim = dim3(NT);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim = {static_cast<unsigned>(p.slices), 1, 1};
+  cfg.attrs = attr;
+  cfg.numAttrs = FWD && p.slices > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+template <int DT, bool FWD, bool BWD>
+cudaError_t choose(DistillParams& p, int64_t B, cudaStream_t stream) {
+  const int64_t vectors = p.V / Elem<DT>::kVec;
+  auto cut = [&](int64_t per) { return std::max<int64_t>(1, (vectors + per - 1) / per); };
+  auto fits = [&](int64_t S) {
+    p.slices = static_cast<int32_t>(S);
+    return S <= kMaxSlices && B * S <= INT32_MAX;
+  };
+  // few rows: enough slices to fill the GPU's 304 CTA slots, of at least two vectors per thread
+  const int64_t fill = std::min<int64_t>({kMaxSlices, cut(1024), (304 + B - 1) / B});
+  if constexpr (FWD && BWD) {  // a slice, in whole 128-byte lines, within its CTA's shared memory
+    if (fits(std::max(fill, cut(kKeepBytes / 2 / 16 - 8)))) return start<DT, 512, 2, true, true, true>(p, B, stream);
+    if (fits(cut(kKeepBytes / 16 - 8))) return start<DT, 1024, 1, true, true, true>(p, B, stream);
+  }
+  if (!fits(FWD ? fill : std::max(fill, std::min<int64_t>(kMaxSlices, cut(8192))))) p.slices = 1;
+  return start<DT, 512, 2, false, FWD, BWD>(p, B, stream);
+}
+
 template <bool FWD, bool BWD>
-int launch(const DistillParams& p, int dtype, int64_t B, void* stream) {
+int launch(DistillParams p, int dtype, int64_t B, void* stream) {
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const unsigned grid = static_cast<unsigned>(B);
-  if (dtype == SFC_BF16)
-    distill_kernel<0, FWD, BWD><<<grid, kThreads, 0, st>>>(p);
-  else
-    distill_kernel<1, FWD, BWD><<<grid, kThreads, 0, st>>>(p);
-  return cudaGetLastError() == cudaSuccess ? SFC_OK : SFC_ECUDA;
+  const cudaError_t err = dtype == SFC_BF16 ? choose<0, FWD, BWD>(p, B, st) : choose<1, FWD, BWD>(p, B, st);
+  if (err != cudaSuccess) {
+    (void)cudaGetLastError();
+    return SFC_ECUDA;
+  }
+  return SFC_OK;
 }
 
 }  // namespace
@@ -200,7 +366,7 @@ extern "C" int sfc_distill_forward(const void* logits, int dtype, int64_t B, int
   if (!loss || !row_status || reinterpret_cast<uintptr_t>(row_stats) % 16) return SFC_EINVAL;
   const sfc::DistillParams p{logits, row_stride, V, packed_width, (flags & SFC_FLAG_NORMALISE_TEACHER) != 0,
                              temperature, teacher_ids, teacher_values, lengths, nullptr, loss,
-                             reinterpret_cast<float4*>(row_stats), row_status, nullptr, 0};
+                             reinterpret_cast<float4*>(row_stats), row_status, nullptr, 0, 1};
   return sfc::launch<true, false>(p, dtype, B, stream);
 }
 
@@ -217,7 +383,7 @@ extern "C" int sfc_distill_backward(const void* logits, int dtype, int64_t B, in
   const sfc::DistillParams p{logits, row_stride, V, packed_width, (flags & SFC_FLAG_NORMALISE_TEACHER) != 0,
                              temperature, teacher_ids, teacher_values, lengths, grad_loss, nullptr,
                              const_cast<float4*>(reinterpret_cast<const float4*>(row_stats)), nullptr,
-                             static_cast<unsigned char*>(grad_logits), grad_stride};
+                             static_cast<unsigned char*>(grad_logits), grad_stride, 1};
   return sfc::launch<false, true>(p, dtype, B, stream);
 }
 
@@ -234,6 +400,6 @@ extern "C" int sfc_distill_forward_backward(const void* logits, int dtype, int64
   if (!loss || !row_status) return SFC_EINVAL;
   const sfc::DistillParams p{logits, row_stride, V, packed_width, (flags & SFC_FLAG_NORMALISE_TEACHER) != 0,
                              temperature, teacher_ids, teacher_values, lengths, grad_loss, loss, nullptr, row_status,
-                             static_cast<unsigned char*>(grad_logits), grad_stride};
+                             static_cast<unsigned char*>(grad_logits), grad_stride, 1};
   return sfc::launch<true, true>(p, dtype, B, stream);
 }

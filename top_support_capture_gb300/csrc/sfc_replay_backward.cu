@@ -34,7 +34,8 @@ constexpr int kThreads = 256;
 template <int DT>
 __global__ void __launch_bounds__(kThreads) replay_backward_kernel(const __grid_constant__ ReplayBackwardParams p) {
   constexpr int NW = kThreads / 32;
-  __shared__ float red[3 * NW];
+  __shared__ float2 red[NW];
+  __shared__ float red_sum[NW];
   const int tid = threadIdx.x;
   const int64_t r = blockIdx.x;
   const float T = p.temperature[r];
@@ -52,23 +53,23 @@ __global__ void __launch_bounds__(kThreads) replay_backward_kernel(const __grid_
   if (!temperature_valid(T) || n < 1 || n > p.W) return;
   const float c = exponent_scale(T), g = p.grad_token[r];
   SoftmaxAcc a;
-  float sum[1] = {0.f};
+  float sum = 0.f;
   int bad = 0;
   for (int j = tid; j < n; j += kThreads) {
     const int32_t id = ids[j];
     const bool in = id >= 0 && id < p.V;
     bad |= !in;
     a.add(Elem<DT>::load1(row, in ? id : 0), c);
-    sum[0] += (G ? G[j] : 0.f) + (id == tok ? g : 0.f);
+    sum += (G ? G[j] : 0.f) + (id == tok ? g : 0.f);
   }
-  block_merge<kThreads>(a, c, red);
-  block_sum<kThreads, 1>(sum, red + 2 * NW);
-  if (__syncthreads_or(bad) || !stats_valid(a.m, a.s)) return;  // the barrier also orders the zeros before the values
-  const float k = sum[0] / a.s;
+  const SoftmaxStats st = block_stats<kThreads>(a, c, red);
+  const float total = block_total<kThreads>(sum, red_sum);
+  if (__syncthreads_or(bad) || !stats_valid(st.m, st.s)) return;  // the barrier also orders the zeros before the values
+  const float k = total / st.s;
   for (int j = tid; j < n; j += kThreads) {
     const int32_t id = ids[j];
     const float u = (G ? G[j] : 0.f) + (id == tok ? g : 0.f);
-    Out<DT>::store1(grad, id, (u - k * ex2_approx((Elem<DT>::load1(row, id) - a.m) * c)) / T);
+    Out<DT>::store1(grad, id, (u - k * ex2_approx((Elem<DT>::load1(row, id) - st.m) * c)) / T);
   }
 }
 

@@ -46,32 +46,69 @@ struct RowSpan {
   __device__ __forceinline__ float at(int64_t i) const { return Elem<DT>::load1(row, i); }
 };
 
-struct SoftmaxAcc {
-  float m = -FLT_MAX, s = 0.f;
+__device__ __forceinline__ uint64_t fmul_f2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
 
-  __device__ __forceinline__ void add(float x, float c) {
+__device__ __forceinline__ float warp_max(float x) {  // one instruction (NaN only where all are)
+  float y;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// 2^((x - m) c) of a vector's elements, two lanes of a packed instruction at a time: the pass over a row is bound by
+// its instruction issue as much as by HBM. minus_m and c hold their value in both lanes.
+template <int N>
+__device__ __forceinline__ void exponentials(const float (&x)[N], uint64_t minus_m, uint64_t c, uint64_t (&e)[N / 2]) {
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) {
+    float a, b;
+    unpack_f2(fmul_f2(fadd_f2(pack_f2(x[2 * i], x[2 * i + 1]), minus_m), c), a, b);
+    e[i] = pack_f2(ex2_approx(a), ex2_approx(b));
+  }
+}
+
+// The statistics of what one thread has seen. The sum is held in two lanes.
+struct SoftmaxAcc {
+  float m = -FLT_MAX;
+  uint64_t s2 = 0;  // (0.f, 0.f)
+
+  __device__ __forceinline__ void raise(float x, float c) {
     if (x > m) {
-      s *= ex2_approx((m - x) * c);
+      const float f = ex2_approx((m - x) * c);
+      s2 = fmul_f2(s2, pack_f2(f, f));
       m = x;
     }
-    s += ex2_approx((x - m) * c);
+  }
+  __device__ __forceinline__ void add(float x, float c) {
+    raise(x, c);
+    s2 = fadd_f2(s2, pack_f2(ex2_approx((x - m) * c), 0.f));
   }
   // One vector: a rescale only when its maximum is a new one.
   template <int N>
   __device__ __forceinline__ void add(const float (&x)[N], float vmax, float c) {
-    if (vmax > m) {
-      s *= ex2_approx((m - vmax) * c);
-      m = vmax;
-    }
-    float e[N];
+    raise(vmax, c);
+    uint64_t e[N / 2];
+    exponentials(x, pack_f2(-m, -m), pack_f2(c, c), e);
 #pragma unroll
-    for (int i = 0; i < N; ++i) e[i] = ex2_approx((x[i] - m) * c);
+    for (int w = N / 4; w > 0; w /= 2)  // a fixed tree
 #pragma unroll
-    for (int w = N / 2; w > 0; w /= 2)  // a fixed tree
-#pragma unroll
-      for (int i = 0; i < w; ++i) e[i] += e[i + w];
-    s += e[0];
+      for (int i = 0; i < w; ++i) e[i] = fadd_f2(e[i], e[i + w]);
+    s2 = fadd_f2(s2, e[0]);
   }
+  __device__ __forceinline__ float sum() const {
+    float a, b;
+    unpack_f2(s2, a, b);
+    return a + b;
+  }
+};
+
+// Merged statistics: of a warp, a CTA, a row.
+struct SoftmaxStats {
+  float m, s;
+
   __device__ __forceinline__ void merge(float m2, float s2, float c) {
     const float mn = fmaxf(m, m2);
     s = s * ex2_approx((m - mn) * c) + s2 * ex2_approx((m2 - mn) * c);
@@ -82,46 +119,44 @@ struct SoftmaxAcc {
 // A finite maximum and a mass: false for rows with NaN or +inf logits (s is NaN) or without a finite one.
 __device__ __forceinline__ bool stats_valid(float m, float s) { return s > 0.f && s < INFINITY && m < INFINITY; }
 
-// The accumulators of the CTA's NT threads as one, the same bits in every thread: warp butterflies (each
-// step is symmetric in its two operands), then the warps in order. `red` holds 2 NT / 32 floats; a barrier
-// must separate two uses of it.
-template <int NT>
-__device__ __forceinline__ void block_merge(SoftmaxAcc& a, float c, float* red) {
-  constexpr int NW = NT / 32;
+__device__ __forceinline__ float warp_total(float x) {  // butterflies: the same bits in every lane
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const float m2 = __shfl_xor_sync(kFull, a.m, o), s2 = __shfl_xor_sync(kFull, a.s, o);
-    a.merge(m2, s2, c);
-  }
-  if ((threadIdx.x & 31) == 0) {
-    red[threadIdx.x >> 5] = a.m;
-    red[NW + (threadIdx.x >> 5)] = a.s;
-  }
-  __syncthreads();
-  float m = red[0];
-  for (int w = 1; w < NW; ++w) m = fmaxf(m, red[w]);
-  float s = 0.f;
-  for (int w = 0; w < NW; ++w) s += red[NW + w] * ex2_approx((red[w] - m) * c);
-  a.m = m;
-  a.s = s;
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(kFull, x, o);
+  return x;
 }
 
-// Sums over the CTA in a fixed order, the same bits in every thread. `red` holds K NT / 32 floats.
-template <int NT, int K>
-__device__ __forceinline__ void block_sum(float (&v)[K], float* red) {
-  constexpr int NW = NT / 32;
-#pragma unroll
-  for (int k = 0; k < K; ++k) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v[k] += __shfl_xor_sync(kFull, v[k], o);
-    if ((threadIdx.x & 31) == 0) red[k * NW + (threadIdx.x >> 5)] = v[k];
-  }
+// The warp's statistics: its maximum first, then each thread's sum rescaled once.
+__device__ __forceinline__ SoftmaxStats warp_stats(const SoftmaxAcc& a, float c) {
+  const float m = warp_max(a.m);
+  return SoftmaxStats{m, warp_total(a.sum() * ex2_approx((a.m - m) * c))};
+}
+// Those of the CTA's warps, one in each lane (the lanes past them repeat the first with no mass).
+template <int NT>
+__device__ __forceinline__ SoftmaxStats merge_warps(const float2* red, float c) {
+  const int lane = threadIdx.x & 31;
+  const float2 v = red[lane < NT / 32 ? lane : 0];
+  const float m = warp_max(v.x);
+  return SoftmaxStats{m, warp_total(lane < NT / 32 ? v.y * ex2_approx((v.x - m) * c) : 0.f)};
+}
+
+// The accumulators of the CTA's NT threads as one, in a fixed order, the same bits in every thread. `red` holds
+// NT / 32 entries; a barrier must separate two uses of it.
+template <int NT>
+__device__ __forceinline__ SoftmaxStats block_stats(const SoftmaxAcc& a, float c, float2* red) {
+  const SoftmaxStats w = warp_stats(a, c);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = make_float2(w.m, w.s);
   __syncthreads();
-#pragma unroll
-  for (int k = 0; k < K; ++k) {
-    v[k] = red[k * NW];
-    for (int w = 1; w < NW; ++w) v[k] += red[k * NW + w];
-  }
+  return merge_warps<NT>(red, c);
+}
+
+// A sum over the CTA in a fixed order, the same bits in every thread. `red` holds NT / 32 floats.
+template <int NT>
+__device__ __forceinline__ float block_total(float v, float* red) {
+  const float w = warp_total(v);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = w;
+  __syncthreads();
+  const int lane = threadIdx.x & 31;
+  return warp_total(lane < NT / 32 ? red[lane] : 0.f);
 }
 
 // This thread's share (vectors t, t + NT, ...) of the row's statistics.

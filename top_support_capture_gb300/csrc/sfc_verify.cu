@@ -63,7 +63,7 @@ constexpr int kThreads = 512;
 template <int DT>
 __global__ void __launch_bounds__(kThreads) verify_stats_kernel(const __grid_constant__ VerifyParams p) {
   constexpr int NW = kThreads / 32;
-  __shared__ float red[2 * NW];
+  __shared__ float2 red[NW];
   __shared__ int lowest;
   const int rows = p.draft ? 2 * p.D + 1 : p.D + 1;
   const int64_t b = blockIdx.x / rows;
@@ -74,8 +74,7 @@ __global__ void __launch_bounds__(kThreads) verify_stats_kernel(const __grid_con
   if (n < 0 || n > p.D || j > n || (!of_target && j == n) || !p.usable(T)) return;  // not part of the request
   const RowSpan<DT> row = of_target ? target_row<DT>(p, b, j) : draft_row<DT>(p, b, j);
   const float c = T == 0.f ? kLog2e : exponent_scale(T);
-  SoftmaxAcc a = row_stats<DT, kThreads>(row, 0, row.nvec, true, c);
-  block_merge<kThreads>(a, c, red);
+  const SoftmaxStats a = block_stats<kThreads>(row_stats<DT, kThreads>(row, 0, row.nvec, true, c), c, red);
   int arg = 0;
   if (T == 0.f) {
     if (threadIdx.x == 0) lowest = INT32_MAX;
