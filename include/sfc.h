@@ -346,10 +346,9 @@ int sfc_distill_forward_backward(const void* logits, int dtype, int64_t B, int64
  *                 when a temperature or num_drafts is out of range, or when, at a position up to a, a row has a
  *                 NaN or +inf logit or no finite one, or the drafted token is outside [0, V). Rows past the
  *                 position of the first refusal do not matter.
- * workspace       device scratch of sfc_verify_workspace_size bytes, 16-byte aligned, with a contract like
- *                 sfc_workspace_size's: ZERO-FILLED before its first use, left ready for the next verification
- *                 call (of any size that it holds), used by one call at a time. Not to be shared with
- *                 sfc_sample_filter_capture.
+ * workspace       device scratch of sfc_verify_workspace_size bytes, with the contract of sfc_workspace_size
+ *                 (16-byte aligned, ZERO-FILLED before its first use, returned to zero by every call, used by one
+ *                 call at a time).
  * Returns SFC_OK or a negative code (nothing enqueued).
  */
 size_t sfc_verify_workspace_size(int64_t B, int32_t D, int64_t V, int dtype);
