@@ -159,26 +159,36 @@ __device__ __forceinline__ float block_total(float v, float* red) {
   return warp_total(lane < NT / 32 ? red[lane] : 0.f);
 }
 
-// This thread's share (vectors t, t + NT, ...) of the row's statistics.
-template <int DT, int NT>
-__device__ __forceinline__ SoftmaxAcc row_stats(const RowSpan<DT>& r, int64_t v0, int64_t v1, bool scalars, float c) {
-  constexpr int VEC = Elem<DT>::kVec, U = 4;
-  SoftmaxAcc a;
-  const uint4* body = r.body();
-  for (int64_t k0 = v0 + threadIdx.x; k0 < v1; k0 += NT * U) {
-    uint4 v[U];
+// This thread's vectors of [v0, v1) of a row, every NT-th, U of them at a time. The first batch can be on its way
+// before anything else of the row is known, and each later one is while the one before it is used.
+template <int DT, int NT, int U>
+struct RowStream {
+  const uint4* body;
+  int k, v1;
+  uint4 v[U];
+
+  __device__ __forceinline__ RowStream(const RowSpan<DT>& r, int v0, int v1_)
+      : body(r.body()), k(v0 + static_cast<int>(threadIdx.x)), v1(v1_) {
+    load(v, k);
+  }
+  __device__ __forceinline__ void load(uint4 (&w)[U], int at) const {
 #pragma unroll
-    for (int u = 0; u < U; ++u) v[u] = k0 + u * NT < v1 ? __ldg(body + k0 + u * NT) : Elem<DT>::neg_inf_vec();
+    for (int u = 0; u < U; ++u) w[u] = at + u * NT < v1 ? ld_once(body + at + u * NT) : Elem<DT>::neg_inf_vec();
+  }
+  // use(vector, its index), in order; padding vectors (-inf) have an index >= v1.
+  template <class F>
+  __device__ __forceinline__ void each(F use) {
+    while (k < v1) {
+      uint4 next[U];
+      load(next, k + NT * U);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      float x[VEC];
-      Elem<DT>::unpack(v[u], x);
-      a.add(x, Elem<DT>::vmax(v[u]), c);
+      for (int u = 0; u < U; ++u) use(v[u], k + u * NT);
+#pragma unroll
+      for (int u = 0; u < U; ++u) v[u] = next[u];
+      k += NT * U;
     }
   }
-  if (scalars && static_cast<int>(threadIdx.x) < r.scalars()) a.add(r.at(r.scalar_index(threadIdx.x)), c);
-  return a;
-}
+};
 
 // Round once to the element type.
 template <int DT>

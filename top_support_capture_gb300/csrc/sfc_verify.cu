@@ -29,8 +29,9 @@
 namespace sfc {
 namespace {
 
-constexpr int kStatThreads = 512, kDrawThreads = 256;
-constexpr int64_t kStatCtas = 1216, kDrawCtas = 608;  // CTAs wanted: two waves of four a SM; one wave
+constexpr int kStatThreads = 512, kStatUnroll = 2, kDrawThreads = 256;
+constexpr int64_t kSlots = 456;  // CTAs of statistics that a GB300 runs at once: three a SM
+constexpr int64_t kStatCtas = 1216, kDrawCtas = 608;  // CTAs wanted
 
 struct RowStats {  // 16 bytes
   float m, s;
@@ -58,7 +59,9 @@ static_assert(sizeof(Decision) % 16 == 0 && sizeof(BlockHeader) % 16 == 0, "bloc
 // How the work is cut, by sizes alone. At least `kMinVectors` 16-byte vectors a slice.
 constexpr int kMaxStatSlices = 16, kMaxDrawSlices = 128, kMinVectors = 512;
 struct Cut {
-  int stat, draw;                                   // slices per row, per request
+  int stat, draw;                                     // slices per row, per request
+  bool waves;                                         // more CTAs of statistics than run at once
+  int32_t stat_per, draw_per;                         // vectors of a slice, groups of 8 elements of a slice
   int32_t rec_at, decision_at, best_at, block_bytes;  // a request's block: header, [2D+1][stat], [D+1], [draw]
 };
 Cut cut_of(int64_t B, int D, int64_t V, int elt) {
@@ -68,7 +71,10 @@ Cut cut_of(int64_t B, int D, int64_t V, int elt) {
   };
   Cut c;
   c.stat = slices((kStatCtas + rows - 1) / rows, kMaxStatSlices, kMinVectors);
-  c.draw = slices((kDrawCtas + B - 1) / B, kMaxDrawSlices, 128);
+  c.draw = slices(kDrawCtas / B, kMaxDrawSlices, 128);
+  c.waves = rows * c.stat > kSlots;
+  c.stat_per = static_cast<int32_t>((vectors + c.stat - 1) / c.stat);
+  c.draw_per = static_cast<int32_t>(((V + 7) / 8 + c.draw - 1) / c.draw);
   c.rec_at = sizeof(BlockHeader);
   c.decision_at = c.rec_at + (2 * D + 1) * c.stat * static_cast<int>(sizeof(RowStats));
   c.best_at = c.decision_at + (D + 1) * static_cast<int>(sizeof(Decision));
@@ -120,11 +126,23 @@ __device__ __forceinline__ RowSpan<DT> draft_row(const VerifyParams& p, int64_t 
   return RowSpan<DT>(p.draft, b * p.draft_request + j * p.draft_row, p.V);
 }
 
-// ln of the probability of token t, and the probability, in 64 bits: it is compared with a number next to it.
-template <int DT>
-__device__ __forceinline__ double log_prob(const RowSpan<DT>& row, const RowStats& st, float T, int32_t t) {
+// ln of the probability of token t from its logit x: in 32 bits, and where that has to decide against a number next
+// to it, in 64.
+__device__ __forceinline__ float log_prob(float x, const RowStats& st, float T, int32_t t) {
+  if (T == 0.f) return t == st.argmax ? 0.f : -INFINITY;
+  return (x - st.m) / T - logf(st.s);
+}
+__device__ __noinline__ double log_prob_exact(float x, const RowStats& st, float T, int32_t t) {
   if (T == 0.f) return t == st.argmax ? 0.0 : -INFINITY;
-  return (static_cast<double>(row.at(t)) - st.m) / T - log(static_cast<double>(st.s));
+  return (static_cast<double>(x) - st.m) / T - log(static_cast<double>(st.s));
+}
+
+// u q < p.
+__device__ __forceinline__ bool accepts(float u, float x, const RowStats& st, float T, float y, const RowStats& sd,
+                                        float Td, bool certain, int32_t t) {
+  const float left = certain ? u : u * expf(log_prob(y, sd, Td, t)), right = expf(log_prob(x, st, T, t));
+  if (fabsf(left - right) > 0x1p-14f * fmaxf(left, right) && right > 0x1p-100f) return left < right;
+  return u * (certain ? 1.0 : exp(log_prob_exact(y, sd, Td, t))) < exp(log_prob_exact(x, st, T, t));
 }
 
 // A row's statistics from its slice records, by one warp (lane k: slice k).
@@ -141,40 +159,57 @@ __device__ __forceinline__ RowStats merge_records(const RowStats* rec, int slice
   return RowStats{m, s, arg, 0};
 }
 
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_primary() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 __device__ __forceinline__ float stat_scale(float T) { return T == 0.f ? kLog2e : exponent_scale(T); }
 
 template <int DT>
-__global__ void __launch_bounds__(kStatThreads) verify_stats_kernel(const __grid_constant__ VerifyParams p) {
+__global__ void __launch_bounds__(kStatThreads, 3) verify_stats_kernel(const __grid_constant__ VerifyParams p) {
+  constexpr int VEC = Elem<DT>::kVec;
   __shared__ float2 red[kStatThreads / 32];
   __shared__ int lowest;
   __shared__ bool last;
-  // block index: position, side, request, slice (the earliest positions first)
-  const int S = p.cut.stat, sides = p.draft ? 2 : 1;
-  unsigned i = blockIdx.x;
-  const int slice = static_cast<int>(i % S);
-  i /= S;
-  const int64_t b = i % static_cast<unsigned>(p.B);
-  i /= static_cast<unsigned>(p.B);
-  const bool of_target = sides == 1 || i % 2 == 0;
-  const int j = static_cast<int>(i / sides), n = p.drafts(b);
+  // grid: request, slice, position and side (the earliest positions first)
+  const int S = p.cut.stat, slice = blockIdx.y;
+  const int64_t b = blockIdx.x;
+  const bool of_target = !p.draft || (blockIdx.z & 1) == 0;
+  const int j = p.draft ? blockIdx.z >> 1 : blockIdx.z, n = p.drafts(b);
   BlockHeader* head = p.header(b);
+  if (!p.cut.waves) launch_dependents();
+  const RowSpan<DT> row = of_target ? target_row<DT>(p, b, j) : draft_row<DT>(p, b, j < p.D ? j : 0);
+  const int nvec = static_cast<int>(row.nvec), v0 = min(slice * p.cut.stat_per, nvec), v1 = min(v0 + p.cut.stat_per, nvec);
+  RowStream<DT, kStatThreads, kStatUnroll> stream(row, v0, v1);  // on its way while the parameters load
   if (!p.sound(b, n) || j > n || (!of_target && j == n)) return;  // not part of the request
-  const uint32_t stop = *reinterpret_cast<volatile uint32_t*>(&head->stop);
-  // past a refusal (one vote: the mark may rise while the CTA's threads read it)
-  if (__syncthreads_or(stop != 0 && static_cast<int>(kStopBase - stop) < j)) return;
+  if (p.cut.waves) {
+    // past a refusal (one vote: the mark may rise while the CTA's threads read it)
+    const uint32_t stop = *reinterpret_cast<volatile uint32_t*>(&head->stop);
+    if (__syncthreads_or(stop != 0 && static_cast<int>(kStopBase - stop) < j)) return;
+  }
   const float T = of_target ? p.temperature[b] : p.draft_temperature[b], c = stat_scale(T);
-  const RowSpan<DT> row = of_target ? target_row<DT>(p, b, j) : draft_row<DT>(p, b, j);
-  const int64_t per = (row.nvec + S - 1) / S, v0 = min(slice * per, row.nvec), v1 = min(v0 + per, row.nvec);
-  const SoftmaxStats a = block_stats<kStatThreads>(row_stats<DT, kStatThreads>(row, v0, v1, slice == 0, c), c, red);
+  const bool scalar = slice == 0 && static_cast<int>(threadIdx.x) < row.scalars();
+  SoftmaxAcc acc;
+  stream.each([&](const uint4& v, int) {
+    float x[VEC];
+    Elem<DT>::unpack(v, x);
+    acc.add(x, Elem<DT>::vmax(v), c);
+  });
+  if (scalar) acc.add(row.at(row.scalar_index(threadIdx.x)), c);
+  const SoftmaxStats a = block_stats<kStatThreads>(acc, c, red);
   int arg = 0;
-  if (T == 0.f) {  // the slice's elements once more, for the lowest id of its maximum
+  if (T == 0.f) {  // the slice once more, for the lowest id of its maximum
     if (threadIdx.x == 0) lowest = INT32_MAX;
     __syncthreads();
     int mine = INT32_MAX;
-    const int64_t e0 = row.head + v0 * Elem<DT>::kVec, e1 = row.head + v1 * Elem<DT>::kVec;
-    for (int64_t k = e0 + threadIdx.x; k < e1 && mine == INT32_MAX; k += kStatThreads)
-      if (row.at(k) == a.m) mine = static_cast<int>(k);
-    if (slice == 0 && static_cast<int>(threadIdx.x) < row.scalars()) {
+    RowStream<DT, kStatThreads, kStatUnroll> again(row, v0, v1);
+    again.each([&](const uint4& v, int at) {
+      float x[VEC];
+      Elem<DT>::unpack(v, x);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e)
+        if (x[e] == a.m && at < v1) mine = min(mine, row.head + at * VEC + e);
+    });
+    if (scalar) {
       const int64_t k = row.scalar_index(threadIdx.x);
       if (row.at(k) == a.m) mine = min(mine, static_cast<int>(k));
     }
@@ -192,52 +227,87 @@ __global__ void __launch_bounds__(kStatThreads) verify_stats_kernel(const __grid
   if (!last || threadIdx.x >= 32) return;
   __threadfence();
   Decision d{};
-  const float Tt = p.temperature[b];
+  const bool drafted = j < n, certain = !p.draft;
+  const float Tt = p.temperature[b], Td = certain ? 0.f : p.draft_temperature[b];
+  // the draft's token and logits travel while the records merge
+  const int32_t t = drafted ? p.draft_tokens[b * p.D + j] : 0;
+  const bool in = t >= 0 && t < p.V;
+  const float u = drafted ? p.uniforms[b * p.D + j] : 0.f;
+  const float x = target_row<DT>(p, b, j).at(in ? t : 0);
+  const float y = drafted && !certain ? draft_row<DT>(p, b, j).at(in ? t : 0) : 0.f;
   d.target = merge_records(p.records(b, true, j), S, stat_scale(Tt));
   d.draft = RowStats{0.f, 1.f, INT32_MAX, 0};
-  const bool drafted = j < n;
-  if (drafted && p.draft) d.draft = merge_records(p.records(b, false, j), S, stat_scale(p.draft_temperature[b]));
+  if (drafted && !certain) d.draft = merge_records(p.records(b, false, j), S, stat_scale(Td));
   if (threadIdx.x != 0) return;
   d.code = kStopped;
-  if (!stats_valid(d.target.m, d.target.s) || !stats_valid(d.draft.m, d.draft.s)) d.code = kBad;
-  if (drafted && d.code != kBad) {
-    const int32_t t = p.draft_tokens[b * p.D + j];
-    if (t < 0 || t >= p.V) {
-      d.code = kBad;
-    } else {
-      const double lp = log_prob<DT>(target_row<DT>(p, b, j), d.target, Tt, t);
-      const double q = p.draft ? exp(log_prob<DT>(draft_row<DT>(p, b, j), d.draft, p.draft_temperature[b], t)) : 1.0;
-      if (p.uniforms[b * p.D + j] * q < exp(lp)) d.code = kAccepted;
-      d.lp = static_cast<float>(lp);
-    }
+  if (!in || !stats_valid(d.target.m, d.target.s) || !stats_valid(d.draft.m, d.draft.s)) {
+    d.code = kBad;
+  } else if (drafted) {
+    if (accepts(u, x, d.target, Tt, y, d.draft, Td, certain, t)) d.code = kAccepted;
+    d.lp = log_prob(x, d.target, Tt, t);
   }
   *p.decision(b, j) = d;
   if (d.code != kAccepted) atomicMax(&head->stop, kStopBase - static_cast<uint32_t>(j));
 }
 
-// Elements 8 g .. 8 g + 7 of a row; past its end: -inf.
+// Elements 8 g .. 8 g + 7 of a row as they lie in memory (16-byte loads where the row allows, else one by one);
+// past its end: -inf.
 template <int DT>
-__device__ __forceinline__ void load8(const RowSpan<DT>& row, int64_t g, bool aligned, float (&x)[8]) {
-  const int64_t i0 = 8 * g;
-  if (aligned && i0 + 8 <= row.V) {
-    const uint4* at = reinterpret_cast<const uint4*>(row.row + i0 * Elem<DT>::kBytes);
+struct Eight {
+  static constexpr int N = DT == 0 ? 1 : 2;
+  uint4 v[N];
+
+  __device__ __forceinline__ void load(const RowSpan<DT>& row, int64_t g, bool aligned) {
+    const int64_t i0 = 8 * g;
+    if (aligned && i0 + 8 <= row.V) {
+      const uint4* at = reinterpret_cast<const uint4*>(row.row + i0 * Elem<DT>::kBytes);
+#pragma unroll
+      for (int k = 0; k < N; ++k) v[k] = ld_once(at + k);
+    } else {
+      uint32_t w[4 * N];
+#pragma unroll
+      for (int k = 0; k < 4 * N; ++k) {
+        if constexpr (DT == 0) {
+          const uint32_t lo = i0 + 2 * k < row.V ? __float_as_uint(row.at(i0 + 2 * k)) : 0xFF800000u;
+          const uint32_t hi = i0 + 2 * k + 1 < row.V ? __float_as_uint(row.at(i0 + 2 * k + 1)) : 0xFF800000u;
+          w[k] = (lo >> 16) | hi;
+        } else {
+          w[k] = i0 + k < row.V ? __float_as_uint(row.at(i0 + k)) : 0xFF800000u;
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < N; ++k) v[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+    }
+  }
+  __device__ __forceinline__ void values(float (&x)[8]) const {
     if constexpr (DT == 0) {
-      Elem<0>::unpack(__ldg(at), x);
+      Elem<0>::unpack(v[0], x);
     } else {
       float lo[4], hi[4];
-      Elem<1>::unpack(__ldg(at), lo);
-      Elem<1>::unpack(__ldg(at + 1), hi);
+      Elem<1>::unpack(v[0], lo);
+      Elem<1>::unpack(v[1], hi);
 #pragma unroll
       for (int e = 0; e < 4; ++e) x[e] = lo[e], x[4 + e] = hi[e];
     }
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = i0 + e < row.V ? row.at(i0 + e) : -INFINITY;
   }
+};
+
+__device__ __forceinline__ float lg2_approx(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
-// The race over elements [8 g0, 8 g1). -ln u is estimated first (lg2, absolute error below 2^-22 times ln 2): only
-// a weight that could beat the warp's best so far takes the exact logarithm and the division.
+// The race over elements [8 g0, 8 g1). E = -ln u is estimated from lg2 (absolute error below 2^-22); an element
+// takes the exact logarithm and the division only if its weight, over the least E that the estimate allows, reaches
+// the warp's bar. The bar is the best ratio so far, at first the largest that the estimates guarantee: about one
+// element of a warp's first 256 passes, and ever fewer later. What is left is the noise itself: ten rounds for four
+// elements.
 template <int DT, bool RESIDUAL>
 __device__ __forceinline__ RaceBest race(const VerifyParams& p, const RowSpan<DT>& row, const RowSpan<DT>& qrow,
                                          const RowStats& st, const RowStats& sd, float c, float cd, int32_t certain,
@@ -245,83 +315,120 @@ __device__ __forceinline__ RaceBest race(const VerifyParams& p, const RowSpan<DT
   RaceBest best;
   float bar = 0.f;  // of the warp
   const float inv = 1.f / st.s, invd = 1.f / sd.s;
+  const uint64_t m2 = pack_f2(-st.m, -st.m), c2 = pack_f2(c, c), inv2 = pack_f2(inv, inv);
+  const uint64_t md2 = pack_f2(-sd.m, -sd.m), cd2 = pack_f2(cd, cd), invd2 = pack_f2(-invd, -invd);
   const bool aligned = (reinterpret_cast<uintptr_t>(row.row) & 15) == 0;
   const bool qaligned = (reinterpret_cast<uintptr_t>(qrow.row) & 15) == 0;
+  const bool two = RESIDUAL && certain < 0 && cd != 0.f;
   const int lane = threadIdx.x & 31;
+  Eight<DT> tx, qx;  // of the coming group
+  if (g0 + threadIdx.x < g1) {
+    tx.load(row, g0 + threadIdx.x, aligned);
+    if (two) qx.load(qrow, g0 + threadIdx.x, qaligned);
+  }
   for (int64_t base = g0 + (threadIdx.x & ~31); base < g1; base += kDrawThreads) {  // uniform over the warp
     const int64_t g = base + lane;
-    float w[8];
+    float w[8], u[8];
+    float most[2] = {0.f, 0.f};  // of each four
     if (g < g1) {
-      load8(row, g, aligned, w);
+      float x[8];
+      uint64_t e2[4];
+      tx.values(x);
+      exponentials(x, m2, c2, e2);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) w[e] = ex2_approx((w[e] - st.m) * c) * inv;
-      if (RESIDUAL) {
-        if (certain >= 0) {
-          const int64_t off = certain - 8 * g;
+      for (int i = 0; i < 4; ++i) e2[i] = fmul_f2(e2[i], inv2);
+      if (two) {
+        uint64_t q2[4];
+        qx.values(x);
+        exponentials(x, md2, cd2, q2);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) w[e] = off == e ? 0.f : w[e];
-        } else if (cd == 0.f) {  // a greedy draft
-          const int64_t off = sd.argmax - 8 * g;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) w[e] = off == e ? fmaxf(w[e] - 1.f, 0.f) : w[e];
-        } else {
-          float q[8];
-          load8(qrow, g, qaligned, q);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) w[e] = fmaxf(w[e] - ex2_approx((q[e] - sd.m) * cd) * invd, 0.f);
-        }
+        for (int i = 0; i < 4; ++i) e2[i] = fadd_f2(e2[i], fmul_f2(q2[i], invd2));  // (fused, equal p and q would leave a rounding)
       }
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float most = fmaxf(fmaxf(w[4 * h], w[4 * h + 1]), fmaxf(w[4 * h + 2], w[4 * h + 3]));
-        if (!(most > bar * 0x1p-25f)) continue;  // E >= -ln(1 - 2^-24): no word can make it win
-        const uint4 block = race_block(p.key, counter_row, static_cast<uint32_t>(2 * g + h));
-        const uint32_t words[4] = {block.x, block.y, block.z, block.w};
+      for (int i = 0; i < 4; ++i) unpack_f2(e2[i], w[2 * i], w[2 * i + 1]);
+      if (g + kDrawThreads < g1) {
+        tx.load(row, g + kDrawThreads, aligned);
+        if (two) qx.load(qrow, g + kDrawThreads, qaligned);
+      }
+      if (RESIDUAL && !two) {  // all of the draft's mass on one token
+        const int64_t off = (certain >= 0 ? certain : sd.argmax) - 8 * g;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float u = static_cast<float>(2u * (words[e] >> 9) + 1u) * 0x1p-24f;
-          const float estimate = fmaf(__log2f(u), -0.693147f, -4e-7f) * 0.99999f;  // at most E
-          if (w[4 * h + e] > bar * estimate) best.offer(w[4 * h + e] / -logf(u), static_cast<int32_t>(8 * g + 4 * h + e));
-        }
+        for (int e = 0; e < 8; ++e) w[e] = off == e ? w[e] - 1.f : w[e];
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) most[h] = fmaxf(fmaxf(w[4 * h], w[4 * h + 1]), fmaxf(w[4 * h + 2], w[4 * h + 3]));
+    }
+    bool pass = false;
+    float reach = 0.f;  // the largest ratio that is certain
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (!(most[h] > bar * 0x1p-25f)) continue;  // nothing here, or E >= -ln(1 - 2^-24) and no word can make one win
+      const uint4 block = race_block(p.key, counter_row, static_cast<uint32_t>(2 * g + h));
+      const uint32_t words[4] = {block.x, block.y, block.z, block.w};
+#pragma unroll
+      for (int e = 4 * h; e < 4 * h + 4; ++e) {
+        u[e] = race_unit(words[e - 4 * h]);
+        const float l = lg2_approx(u[e]);
+        pass |= w[e] > 0.f && w[e] >= bar * fmaf(l, -0.69314f, -4e-7f);
+        if (bar == 0.f) reach = fmaxf(reach, w[e] * rcp_approx(fmaf(l, -0.69316f, 4e-7f)));
       }
     }
-    bar = warp_max(fmaxf(bar, best.ratio));
+    if (!__any_sync(kFull, pass)) continue;
+    if (bar == 0.f) bar = warp_max(reach) * 0.99999f;
+    if (pass) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        if (!(most[e / 4] > 0.f) || !(w[e] > 0.f)) continue;
+        if (most[e / 4] > bar * 0x1p-25f && w[e] >= bar * fmaf(lg2_approx(u[e]), -0.69314f, -4e-7f))
+          best.offer(w[e] / -logf(u[e]), static_cast<int32_t>(8 * g + e));
+      }
+    }
+    bar = fmaxf(bar, warp_max(best.ratio));
   }
   return best;
 }
 
 template <int DT>
-__global__ void __launch_bounds__(kDrawThreads) verify_draw_kernel(const __grid_constant__ VerifyParams p) {
+__global__ void __launch_bounds__(kDrawThreads, 4) verify_draw_kernel(const __grid_constant__ VerifyParams p) {
   constexpr int NW = kDrawThreads / 32;
   __shared__ float ratios[NW];
   __shared__ int32_t best_ids[NW];
   __shared__ bool last;
   const int tid = threadIdx.x, lane = tid & 31, S = p.cut.draw;
-  const int slice = static_cast<int>(blockIdx.x % static_cast<unsigned>(S));
-  const int64_t b = blockIdx.x / static_cast<unsigned>(S);
+  const int slice = blockIdx.y;
+  const int64_t b = blockIdx.x;
   const int n = p.drafts(b);
   const bool sound = p.sound(b, n);
   int a = 0, code = kBad;
-  if (sound) {  // the first position that was not accepted
+  RowStats st{}, sd{};
+  wait_for_primary();
+  if (sound) {  // the first position that was not accepted, one position a lane
     for (int j0 = 0; j0 <= n; j0 += 32) {
-      const int mine = j0 + lane <= n ? __ldcg(&p.decision(b, j0 + lane)->code) : kBad;
+      const uint4* at = reinterpret_cast<const uint4*>(p.decision(b, min(j0 + lane, n)));
+      const uint4 w0 = __ldcg(at), w1 = __ldcg(at + 1), w2 = __ldcg(at + 2);
+      const int mine = j0 + lane <= n ? static_cast<int>(w2.x) : kBad;
       const unsigned open = __ballot_sync(kFull, mine != kAccepted);
       if (open) {
-        a = j0 + __ffs(static_cast<int>(open)) - 1;
-        code = __shfl_sync(kFull, mine, __ffs(static_cast<int>(open)) - 1);
+        const int k = __ffs(static_cast<int>(open)) - 1;
+        a = j0 + k;
+        code = __shfl_sync(kFull, mine, k);
+        auto take = [&](const uint4& w) {
+          return RowStats{__uint_as_float(__shfl_sync(kFull, w.x, k)), __uint_as_float(__shfl_sync(kFull, w.y, k)),
+                          static_cast<int32_t>(__shfl_sync(kFull, w.z, k)), 0};
+        };
+        st = take(w0);
+        sd = take(w1);
         break;
       }
     }
   }
   const bool refused = a < n;
   const float T = p.temperature[b];
-  const Decision* d = p.decision(b, a);
-  const RowStats st = d->target, sd = d->draft;
   const RowSpan<DT> row = target_row<DT>(p, b, a);
   RaceBest best;
   if (code == kStopped && T != 0.f) {
-    const int64_t groups = (p.V + 7) / 8, per = (groups + S - 1) / S;
-    const int64_t g0 = min(slice * per, groups), g1 = min(g0 + per, groups);
+    const int64_t groups = (p.V + 7) / 8;
+    const int64_t g0 = min(static_cast<int64_t>(slice) * p.cut.draw_per, groups), g1 = min(g0 + p.cut.draw_per, groups);
     const float c = exponent_scale(T), Td = p.draft ? p.draft_temperature[b] : 0.f;
     const float cd = Td == 0.f ? 0.f : exponent_scale(Td);
     const uint32_t counter_row = p.row_offset + static_cast<uint32_t>(b);
@@ -363,7 +470,7 @@ __global__ void __launch_bounds__(kDrawThreads) verify_draw_kernel(const __grid_
       p.out.refuse(b, p.D, j, SFC_ROW_BADPARAM);
     } else if (j == a) {
       tokens[a] = token;
-      lps[a] = static_cast<float>(log_prob<DT>(row, st, T, token));
+      lps[a] = log_prob(row.at(token), st, T, token);
     } else {
       tokens[j] = j < a ? p.draft_tokens[b * p.D + j] : -1;
       lps[j] = j < a ? p.decision(b, j)->lp : 0.f;
@@ -376,6 +483,26 @@ __global__ void __launch_bounds__(kDrawThreads) verify_draw_kernel(const __grid_
   __syncthreads();  // the block has been read
   uint4* words = reinterpret_cast<uint4*>(p.block(b));
   for (int k = tid; k < p.cut.block_bytes / 16; k += kDrawThreads) words[k] = make_uint4(0u, 0u, 0u, 0u);
+}
+
+// Where all CTAs of the statistics run at once, the draw's start while they end (programmatic dependent launch) and
+// wait for them before they read the workspace. (With more of them, the waiting CTAs took their places: 10 us slower
+// at 64 x 4 x 151936.)
+template <int DT>
+cudaError_t start(const VerifyParams& p, dim3 stat, dim3 draw, cudaStream_t stream) {
+  verify_stats_kernel<DT><<<stat, kStatThreads, 0, stream>>>(p);
+  const cudaError_t err = cudaGetLastError();
+  if (err != cudaSuccess) return err;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = draw;
+  cfg.blockDim = dim3(kDrawThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = p.cut.waves ? 0 : 1;
+  return cudaLaunchKernelEx(&cfg, verify_draw_kernel<DT>, p);
 }
 
 }  // namespace
@@ -402,7 +529,6 @@ extern "C" int sfc_verify_drafts(const void* target_logits, const void* draft_lo
   if (dtype != SFC_BF16 && dtype != SFC_F32) return SFC_EINVAL;
   if (B < 1 || B > INT32_MAX || V < 1 || V > INT32_MAX || D < 1 || D > SFC_MAX_DRAFTS) return SFC_EINVAL;
   const sfc::Cut cut = sfc::cut_of(B, D, V, dtype == SFC_BF16 ? 2 : 4);
-  if (B * (2 * D + 2) * cut.stat > INT32_MAX || B * cut.draw > INT32_MAX) return SFC_EINVAL;  // the grids
   if (target_request_stride < 0 || target_row_stride < 0 || draft_request_stride < 0 || draft_row_stride < 0) return SFC_EINVAL;
   if (row_offset < 0 || row_offset + B > (int64_t{1} << 32)) return SFC_EINVAL;
   if (flags & ~static_cast<uint32_t>(SFC_FLAG_GREEDY_T0)) return SFC_EINVAL;
@@ -420,14 +546,12 @@ extern "C" int sfc_verify_drafts(const void* target_logits, const void* draft_lo
                             static_cast<uint32_t>(row_offset), static_cast<unsigned char*>(workspace), cut,
                             sfc::VerifyOutputs{accepted, tokens, token_logprobs, row_status}};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const unsigned stat = static_cast<unsigned>(B * (D + 1) * (draft_logits ? 2 : 1) * cut.stat);
-  const unsigned draw = static_cast<unsigned>(B * cut.draw);
-  if (dtype == SFC_BF16) {
-    sfc::verify_stats_kernel<0><<<stat, sfc::kStatThreads, 0, st>>>(p);
-    sfc::verify_draw_kernel<0><<<draw, sfc::kDrawThreads, 0, st>>>(p);
-  } else {
-    sfc::verify_stats_kernel<1><<<stat, sfc::kStatThreads, 0, st>>>(p);
-    sfc::verify_draw_kernel<1><<<draw, sfc::kDrawThreads, 0, st>>>(p);
+  const dim3 stat(static_cast<unsigned>(B), static_cast<unsigned>(cut.stat), static_cast<unsigned>((D + 1) * (draft_logits ? 2 : 1)));
+  const dim3 draw(static_cast<unsigned>(B), static_cast<unsigned>(cut.draw));
+  const cudaError_t err = dtype == SFC_BF16 ? sfc::start<0>(p, stat, draw, st) : sfc::start<1>(p, stat, draw, st);
+  if (err != cudaSuccess) {
+    (void)cudaGetLastError();
+    return SFC_ECUDA;
   }
-  return cudaGetLastError() == cudaSuccess ? SFC_OK : SFC_ECUDA;
+  return SFC_OK;
 }

@@ -25,22 +25,23 @@ __device__ __forceinline__ uint4 race_block(const RaceKey& key, uint32_t row, ui
   uint32_t k0 = key.seed_lo, k1 = key.seed_hi;
 #pragma unroll
   for (int r = 0; r < 10; ++r) {
-    const uint32_t lo0 = 0xD2511F53u * c0, hi0 = __umulhi(0xD2511F53u, c0);
-    const uint32_t lo1 = 0xCD9E8D57u * c2, hi1 = __umulhi(0xCD9E8D57u, c2);
-    c0 = hi1 ^ c1 ^ k0;
-    c1 = lo1;
-    c2 = hi0 ^ c3 ^ k1;
-    c3 = lo0;
+    const uint64_t p0 = static_cast<uint64_t>(0xD2511F53u) * c0, p1 = static_cast<uint64_t>(0xCD9E8D57u) * c2;
+    c0 = static_cast<uint32_t>(p1 >> 32) ^ c1 ^ k0;
+    c1 = static_cast<uint32_t>(p1);
+    c2 = static_cast<uint32_t>(p0 >> 32) ^ c3 ^ k1;
+    c3 = static_cast<uint32_t>(p0);
     k0 += 0x9E3779B9u;
     k1 += 0xBB67AE85u;
   }
   return make_uint4(c0, c1, c2, c3);
 }
 
-// E = -ln u of one word, u = (2 (w >> 9) + 1) 2^-24, exact in float32 and never 0 or 1.
-__device__ __forceinline__ float race_wait(uint32_t w) {
-  return -logf(static_cast<float>(2u * (w >> 9) + 1u) * 0x1p-24f);
-}
+// u = (2 (w >> 9) + 1) 2^-24, exact in float32 and never 0 or 1: the 23 bits as the fraction of a number in [1, 2),
+// less 1 - 2^-24.
+__device__ __forceinline__ float race_unit(uint32_t w) { return __uint_as_float(0x3F800000u | (w >> 9)) - 0x1.fffffep-1f; }
+
+// E = -ln u of one word.
+__device__ __forceinline__ float race_wait(uint32_t w) { return -logf(race_unit(w)); }
 
 // The winner so far: the largest w / E, ties to the lowest id. No winner: ratio 0.
 struct RaceBest {
