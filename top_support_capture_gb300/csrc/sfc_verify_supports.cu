@@ -2,12 +2,14 @@
 // packed (id, log-probability) entries, as the decode step captures them. The rule is that of sfc_verify.cu with
 // p_j and q_j zero outside the supports; a draft row of length 0 is a certain draft.
 //
-// One CTA per request. Its warps look the drafted tokens up in both supports, all positions at once; thread 0
-// walks the decisions; then the CTA draws over the target's support at the position it stopped at. What the draft
-// gives a member is found through a hash table in shared memory (open addressing, 16-bit entry indices, at most
-// half full), built from the draft's support of that position.
+// One CTA per request, every step as wide as the CTA: its warps look the drafted tokens up in both supports, all
+// positions at once, in 16-byte loads; each warp then has every decision (a lane a position); and the CTA draws over
+// the target's support at the position it stopped at. What the draft gives a member is found through a hash table in
+// shared memory (open addressing, 16-bit entry indices, at most half full). Latency bounds it: about ten dependent
+// steps whatever the sizes.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 
 #include "../../include/sfc.h"
@@ -34,32 +36,61 @@ struct VerifySupportsParams {
   VerifyOutputs out;
 };
 
-constexpr int kThreads = 256;
 constexpr uint16_t kEmpty = 0xFFFFu;
 
 __device__ __forceinline__ uint32_t slot_of(int32_t id, uint32_t mask) {
   return (static_cast<uint32_t>(id) * 0x9E3779B1u >> 15) & mask;  // Knuth's multiplicative hash
 }
 
-// The log-probability of token t in a row of n entries (each lane's share of them, then the warp's): -inf where it
-// is not a member.
-__device__ __forceinline__ float find(const int32_t* ids, const float* lps, int n, int32_t t) {
+// The warp's search of ids[k0, k1) for t (k0 a multiple of 4): the lane that finds it leaves its log-probability.
+__device__ __forceinline__ void find(const int32_t* ids, const float* lps, int k0, int k1, int32_t t, float* found) {
   const int lane = threadIdx.x & 31;
   int at = -1;
-  for (int k = lane; k < n; k += 32)
-    if (ids[k] == t) at = k;
-  at = __reduce_max_sync(kFull, at);
-  return at < 0 ? -INFINITY : lps[at];
+  if ((reinterpret_cast<uintptr_t>(ids) & 15) == 0) {
+    const int4* four = reinterpret_cast<const int4*>(ids);
+#pragma unroll 2
+    for (int k = k0 + 4 * lane; k < k1; k += 128) {
+      int4 v = make_int4(-1, -1, -1, -1);
+      if (k + 4 <= k1) v = __ldg(four + k / 4);
+      else {
+        v.x = ids[k];
+        if (k + 1 < k1) v.y = ids[k + 1];
+        if (k + 2 < k1) v.z = ids[k + 2];
+      }
+      if (v.x == t) at = k;
+      if (v.y == t) at = k + 1;
+      if (v.z == t) at = k + 2;
+      if (v.w == t) at = k + 3;
+    }
+  } else {
+#pragma unroll 8
+    for (int k = k0 + lane; k < k1; k += 32)
+      if (ids[k] == t) at = k;
+  }
+  if (t >= 0 && at >= 0) *found = lps[at];
 }
 
-__global__ void __launch_bounds__(kThreads) verify_supports_kernel(const __grid_constant__ VerifySupportsParams p) {
-  constexpr int NW = kThreads / 32;
+// The winner with its place in the row.
+struct Drawn {
+  RaceBest best;
+  int at = 0;
+
+  __device__ __forceinline__ void offer(float ratio, int32_t id, int k) {
+    const float r = best.ratio;
+    const int32_t i = best.id;
+    best.offer(ratio, id);
+    if (best.ratio != r || best.id != i) at = k;
+  }
+};
+
+template <int NT>
+__global__ void __launch_bounds__(NT) verify_supports_kernel(const __grid_constant__ VerifySupportsParams p) {
+  constexpr int NW = NT / 32;
   extern __shared__ uint16_t table[];
-  __shared__ float lp_target[SFC_MAX_DRAFTS], lp_draft[SFC_MAX_DRAFTS];
+  __shared__ float lp_of[2][SFC_MAX_DRAFTS];  // of the drafted tokens: the target's, the draft's
   __shared__ float ratios[NW];
-  __shared__ int32_t best_ids[NW];
-  __shared__ int sh_a, sh_status;
-  const int tid = threadIdx.x, wp = tid >> 5, D = p.D;
+  __shared__ int32_t best_ids[NW], best_at[NW];
+  const int tid = threadIdx.x, lane = tid & 31, wp = tid >> 5, D = p.D;
   const int64_t b = blockIdx.x;
   const int n = p.num_drafts ? p.num_drafts[b] : D;
   const int32_t* drafted = p.draft_tokens + b * D;
@@ -67,44 +98,63 @@ __global__ void __launch_bounds__(kThreads) verify_supports_kernel(const __grid_
   const int32_t* dlen = p.draft.ids ? p.draft.lengths + b * D : nullptr;
   float* lps = p.out.token_logprobs + b * (D + 1);
   int32_t* tokens = p.out.tokens + b * (D + 1);
-  const int looked = min(max(n, 0), D);
-  for (int i = wp; i < 2 * looked; i += NW) {  // even: the target's rows, odd: the draft's
-    const int j = i >> 1;
-    const SupportRows& rows = (i & 1) ? p.draft : p.target;
-    const int len = (i & 1) ? (dlen ? dlen[j] : 0) : tlen[j];
-    const int64_t at = ((i & 1) ? b * D + j : b * (D + 1) + j) * rows.W;
-    float lp = 0.f;  // a certain draft
-    if (!(i & 1) || len > 0) lp = find(rows.ids + at, rows.lps + at, min(max(len, 0), rows.W), drafted[j]);
-    if ((tid & 31) == 0) ((i & 1) ? lp_draft : lp_target)[j] = lp;
+  const uint32_t mask = static_cast<uint32_t>(p.table) - 1;
+  for (int k = tid; k < 2 * SFC_MAX_DRAFTS; k += NT) (&lp_of[0][0])[k] = -INFINITY;
+  if (p.draft.ids)
+    for (int k = tid; k < p.table / 2; k += NT) reinterpret_cast<uint32_t*>(table)[k] = 0xFFFFFFFFu;
+  __syncthreads();
+  // the look-ups: each row cut over `parts` warps
+  const int looked = min(max(n, 0), D), rows = looked * (dlen ? 2 : 1);
+  const int parts = max(1, NW / max(rows, 1));
+  for (int i = wp; i < rows * parts; i += NW) {
+    const int part = i / max(rows, 1), row = i - part * rows, side = row >= looked, j = row - side * looked;
+    const SupportRows& of = side ? p.draft : p.target;
+    const int len = min(max(side ? dlen[j] : tlen[j], 0), of.W);
+    const int per = ((len + parts - 1) / parts + 127) & ~127, k0 = min(part * per, len), k1 = min(k0 + per, len);
+    const int64_t at = (b * (side ? D : D + 1) + j) * of.W;
+    find(of.ids + at, of.lps + at, k0, k1, drafted[j], &lp_of[side][j]);
   }
   __syncthreads();
-  if (tid == 0) {
-    int a = 0, status = n < 0 || n > D ? SFC_ROW_BADPARAM : SFC_ROW_OK;
-    while (status == SFC_ROW_OK) {
-      if (tlen[a] < 1) status = SFC_ROW_BADPARAM;
-      if (tlen[a] > p.target.W) status = SFC_ROW_OVERFLOW;
-      if (a == n || status != SFC_ROW_OK) break;
-      const float lp = lp_target[a], lq = lp_draft[a];
-      if (drafted[a] < 0 || (dlen && dlen[a] < 0))
-        status = SFC_ROW_BADPARAM;
-      else if (dlen && dlen[a] > p.draft.W)
-        status = SFC_ROW_OVERFLOW;
-      else if (!(lp < INFINITY) || !(lq < INFINITY))
-        status = SFC_ROW_BADPARAM;
-      if (status != SFC_ROW_OK) break;
-      // in 64 bits: compared with a number next to it
-      if (!(p.uniforms[b * D + a] * exp(static_cast<double>(lq)) < exp(static_cast<double>(lp)))) break;
-      tokens[a] = drafted[a];
-      lps[a] = lp;
-      ++a;
+  // the decisions, every warp for itself: code 0 goes on, kStop draws here, else the status plus kStatus
+  constexpr int kStop = 1, kStatus = 16;
+  int a = 0, code = kStatus + SFC_ROW_BADPARAM;
+  if (n >= 0 && n <= D) {
+    for (int j0 = 0; j0 <= n; j0 += 32) {
+      const int j = j0 + lane;
+      int mine = kStop;
+      if (j <= n) {
+        const int nt = tlen[j];
+        if (nt < 1 || nt > p.target.W) {
+          mine = kStatus + (nt < 1 ? SFC_ROW_BADPARAM : SFC_ROW_OVERFLOW);
+        } else if (j < n) {
+          const int nd = dlen ? dlen[j] : 0;
+          const float lp = lp_of[0][j], lq = nd > 0 ? lp_of[1][j] : 0.f;  // no row: a certain draft
+          if (drafted[j] < 0 || nd < 0) {
+            mine = kStatus + SFC_ROW_BADPARAM;
+          } else if (nd > p.draft.W) {
+            mine = kStatus + SFC_ROW_OVERFLOW;
+          } else if (!(lp < INFINITY) || !(lq < INFINITY)) {
+            mine = kStatus + SFC_ROW_BADPARAM;
+          } else {
+            const float u = p.uniforms[b * D + j], left = u * expf(lq), right = expf(lp);
+            bool accept = left < right;
+            if (!(fabsf(left - right) > 0x1p-14f * fmaxf(left, right) && right > 0x1p-100f))  // too near: in 64 bits
+              accept = u * exp(static_cast<double>(lq)) < exp(static_cast<double>(lp));
+            if (accept) mine = 0;
+          }
+        }
+      }
+      const unsigned open = __ballot_sync(kFull, mine != 0);
+      if (open) {
+        const int k = __ffs(static_cast<int>(open)) - 1;
+        a = j0 + k;
+        code = __shfl_sync(kFull, mine, k);
+        break;
+      }
     }
-    sh_a = a;
-    sh_status = status;
   }
-  __syncthreads();
-  const int a = sh_a;
-  if (sh_status != SFC_ROW_OK) {
-    for (int j = tid; j <= D; j += kThreads) p.out.refuse(b, D, j, sh_status);
+  if (code != kStop) {
+    for (int j = tid; j <= D; j += NT) p.out.refuse(b, D, j, code - kStatus);
     return;
   }
   const bool refused = a < n;
@@ -113,12 +163,10 @@ __global__ void __launch_bounds__(kThreads) verify_supports_kernel(const __grid_
   const float* lp = p.target.lps + (b * (D + 1) + a) * p.target.W;
   const int32_t* qids = nd > 0 ? p.draft.ids + (b * D + a) * p.draft.W : nullptr;
   const float* qlp = nd > 0 ? p.draft.lps + (b * D + a) * p.draft.W : nullptr;
-  const uint32_t mask = static_cast<uint32_t>(p.table) - 1;
   int bad = 0;
   if (nd > 0) {
-    for (int k = tid; k < p.table; k += kThreads) table[k] = kEmpty;
-    __syncthreads();
-    for (int k = tid; k < nd; k += kThreads) {
+#pragma unroll 2
+    for (int k = tid; k < nd; k += NT) {
       bad |= !(qlp[k] < INFINITY);
       // at most half full: an empty slot is found; ids that repeat take slots of their own
       for (uint32_t h = slot_of(qids[k], mask);; h = (h + 1) & mask)
@@ -128,13 +176,15 @@ __global__ void __launch_bounds__(kThreads) verify_supports_kernel(const __grid_
   }
   const int32_t refused_token = refused ? drafted[a] : -1;
   const uint32_t counter_row = p.row_offset + static_cast<uint32_t>(b);
-  RaceBest best;
-  for (int pass = 0; pass < 2 && best.ratio == 0.f; ++pass) {  // the second: no residual mass
-    RaceBest mine;
-    for (int k = tid; k < nt; k += kThreads) {
+  Drawn all;
+  for (int pass = 0; pass < 2 && all.best.ratio == 0.f; ++pass) {  // the second: no residual mass
+    Drawn mine;
+#pragma unroll 2
+    for (int k = tid; k < nt; k += NT) {
       const int32_t id = ids[k];
-      bad |= id < 0 || !(lp[k] < INFINITY);
-      float w = expf(lp[k]);
+      const float l = lp[k];
+      bad |= id < 0 || !(l < INFINITY);
+      float w = expf(l);
       if (pass == 0 && refused) {
         float q = 0.f;
         if (nd > 0) {
@@ -151,27 +201,48 @@ __global__ void __launch_bounds__(kThreads) verify_supports_kernel(const __grid_
       if (!(w > 0.f)) continue;
       const uint4 block = race_block(p.key, counter_row, static_cast<uint32_t>(id) >> 2);
       const uint32_t word = (id & 2) ? ((id & 1) ? block.w : block.z) : ((id & 1) ? block.y : block.x);
-      mine.offer(w / race_wait(word), id);
+      mine.offer(w / race_wait(word), id, k);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const float r = __shfl_xor_sync(kFull, mine.best.ratio, o);
+      const int32_t i = __shfl_xor_sync(kFull, mine.best.id, o);
+      const int k = __shfl_xor_sync(kFull, mine.at, o);
+      mine.offer(r, i, k);
     }
     __syncthreads();
-    best = block_best<kThreads>(mine, ratios, best_ids);
+    if (lane == 0) {
+      ratios[wp] = mine.best.ratio;
+      best_ids[wp] = mine.best.id;
+      best_at[wp] = mine.at;
+    }
+    __syncthreads();
+    for (int w = 0; w < NW; ++w) all.offer(ratios[w], best_ids[w], best_at[w]);
   }
   bad = __syncthreads_or(bad);
-  if (bad || best.ratio == 0.f) {  // a row without any mass has nothing to draw
-    for (int j = tid; j <= D; j += kThreads) p.out.refuse(b, D, j, SFC_ROW_BADPARAM);
+  if (bad || all.best.ratio == 0.f) {  // a row without any mass has nothing to draw
+    for (int j = tid; j <= D; j += NT) p.out.refuse(b, D, j, SFC_ROW_BADPARAM);
     return;
   }
-  for (int k = tid; k < nt; k += kThreads)
-    if (ids[k] == best.id) lps[a] = lp[k];
-  for (int j = a + 1 + tid; j <= D; j += kThreads) {
-    tokens[j] = -1;
-    lps[j] = 0.f;
+  for (int j = tid; j <= D; j += NT) {
+    tokens[j] = j < a ? drafted[j] : (j == a ? all.best.id : -1);
+    lps[j] = j < a ? lp_of[0][j] : (j == a ? lp[all.at] : 0.f);
   }
   if (tid == 0) {
-    tokens[a] = best.id;
     p.out.accepted[b] = a;
     p.out.row_status[b] = SFC_ROW_OK;
   }
+}
+
+template <int NT>
+cudaError_t start(const VerifySupportsParams& p, int64_t B, cudaStream_t stream) {
+  const int smem = p.draft.ids ? p.table * static_cast<int>(sizeof(uint16_t)) : 0;  // at most 64 KB
+  if (smem > 40 * 1024) {
+    const cudaError_t err = cudaFuncSetAttribute(verify_supports_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (err != cudaSuccess) return err;
+  }
+  verify_supports_kernel<NT><<<static_cast<unsigned>(B), NT, smem, stream>>>(p);
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -194,7 +265,6 @@ extern "C" int sfc_verify_supports(const int32_t* target_ids, const float* targe
   if (row_offset < 0 || row_offset + B > (int64_t{1} << 32)) return SFC_EINVAL;
   int32_t table = 64;  // a power of two of at least twice the entries
   while (draft_ids && table < 2 * draft_width) table *= 2;
-  const int smem = table * static_cast<int>(sizeof(uint16_t));  // at most 64 KB
   const sfc::VerifySupportsParams p{
       sfc::SupportRows{target_ids, target_logprobs, target_lengths, target_width},
       sfc::SupportRows{draft_ids, draft_logprobs, draft_lengths, draft_width},
@@ -202,11 +272,12 @@ extern "C" int sfc_verify_supports(const int32_t* target_ids, const float* targe
       sfc::RaceKey{static_cast<uint32_t>(seed), static_cast<uint32_t>(seed >> 32), static_cast<uint32_t>(step),
                    static_cast<uint32_t>(step >> 32)},
       static_cast<uint32_t>(row_offset), sfc::VerifyOutputs{accepted, tokens, token_logprobs, row_status}};
-  if (smem > 48 * 1024 && cudaFuncSetAttribute(sfc::verify_supports_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               smem) != cudaSuccess) {
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  // wide supports: more entries a request than a small CTA has threads (128 x 4, W = 8192: see the table of figures)
+  const bool wide = std::max(target_width, draft_ids ? draft_width : 0) > 2048;
+  if ((wide ? sfc::start<1024>(p, B, st) : sfc::start<256>(p, B, st)) != cudaSuccess) {
     (void)cudaGetLastError();
     return SFC_ECUDA;
   }
-  sfc::verify_supports_kernel<<<static_cast<unsigned>(B), sfc::kThreads, smem, static_cast<cudaStream_t>(stream)>>>(p);
-  return cudaGetLastError() == cudaSuccess ? SFC_OK : SFC_ECUDA;
+  return SFC_OK;
 }
