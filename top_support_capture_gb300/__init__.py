@@ -195,20 +195,32 @@ def _default_workspace(nbytes: int, device, stream):
     return ws
 
 
-def _enter(device, stream):
-    """(stream, context): the stream to launch on (the current one when None) and what to allocate and launch
-    under, so that outputs belong to the stream that writes them. Nothing is switched where nothing differs."""
-    import contextlib
+class _Nothing:
+    def __enter__(self):
+        return self
 
+    def __exit__(self, *exc):
+        return False
+
+
+_NOTHING = _Nothing()
+
+
+def _enter(device, stream):
+    """(handle, context): the stream to launch on (the current one when None) and what to allocate and launch
+    under, so that outputs belong to the stream that writes them. Nothing is switched where nothing differs:
+    the smallest calls take as long as their Python."""
     import torch
 
     if stream is None and device.index == torch.cuda.current_device():
-        return torch.cuda.current_stream(device), contextlib.nullcontext()
+        return torch._C._cuda_getCurrentRawStream(device.index), _NOTHING
+    import contextlib
+
     context = contextlib.ExitStack()
     context.enter_context(torch.cuda.device(device))
     stream = torch.cuda.current_stream(device) if stream is None else stream
     context.enter_context(torch.cuda.stream(stream))
-    return stream, context
+    return int(stream.cuda_stream), context
 
 
 def _check_tensor(name, t, device, dtype, numel=None, shape=None):

@@ -10,8 +10,8 @@
 // all hold the same bits. The teacher's mass is small work: every CTA sums it for itself.
 //
 // In the call that gives loss and gradient the slice stays in shared memory between its two uses, so the logits are
-// read from HBM once: each thread copies its own vectors there asynchronously (cp.async, no barrier needed) before
-// anything else. Rows longer than a cluster's shared memory are read again.
+// read from HBM once: one thread starts the bulk copies of its four parts before anything else, and the statistics
+// begin when the first has landed. Every wait for a copy is bounded (SFC_ROW_TIMEOUT). Rows longer than a cluster's shared memory are read again.
 //
 // The gradient's dense part tau p_j g / T is written first; after the CTA's barrier the teacher's entries that lie
 // in the slice overwrite theirs with the whole gradient, each rounded once, and add their part of the loss.
@@ -20,6 +20,7 @@
 #include <cstdint>
 
 #include "../../include/sfc.h"
+#include "sfc_host.cuh"
 #include "sfc_rows.cuh"
 
 namespace sfc {
@@ -40,7 +41,7 @@ struct DistillParams {
   int32_t* row_status;
   unsigned char* grad;
   int64_t grad_stride;
-  int32_t slices;
+  int32_t slices, per;  // CTAs a row, vectors a slice
 };
 
 // What the gradient needs of a row: its softmax (m, s) and its teacher's: t_i = exp((y_i - y0) / T_y) / ty, tau.
@@ -59,47 +60,44 @@ __device__ __forceinline__ RowTerms unpack_terms(const float4& v, bool normalise
 }
 
 constexpr int kMaxSlices = 8;  // the portable cluster size
-constexpr int kGroups = 4;     // cp.async groups per thread: the statistics begin when the first has landed
+constexpr int kParts = 4;      // bulk copies of a kept slice
 constexpr int kKeepBytes = 212992;  // shared memory of one SM that keeps logits: 13 vectors for each of 1024 threads
 constexpr int kPrefetch = 2;   // teacher entries per thread held from the start
-
-__device__ __forceinline__ void copy_async(void* dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
+constexpr float kLate = -1.f;  // in place of a mass: a copy did not arrive
 
 // KEEP: the slice's vectors lie in dynamic shared memory (16 bytes for each).
 template <int DT, int NT, int MINB, bool KEEP, bool FWD, bool BWD>
 __global__ void __launch_bounds__(NT, MINB) distill_kernel(const __grid_constant__ DistillParams p) {
   constexpr int NW = NT / 32, VEC = Elem<DT>::kVec;
-  constexpr int kStream = BWD ? 4 : 8;  // vectors in flight per thread where they are not kept
-  extern __shared__ __align__(16) uint4 kept[];
+  constexpr int U = BWD ? 4 : 2;  // vectors in flight per thread where they are not kept (and as many again)
+  extern __shared__ __align__(128) uint4 kept[];
+  __shared__ uint64_t full[kParts];
   __shared__ float2 red[2 * NW];
   __shared__ float red_mass[NW], red_loss[NW];
   __shared__ float2 table[kMaxSlices];  // (m, s) of the slices
   __shared__ float losses[kMaxSlices];
-  const int tid = threadIdx.x, S = p.slices;
-  const int rank = static_cast<int>(blockIdx.x % static_cast<unsigned>(S));
-  const int64_t r = blockIdx.x / static_cast<unsigned>(S);
+  const int tid = threadIdx.x, lane = tid & 31, wp = tid >> 5, S = p.slices, rank = blockIdx.y;
+  const int64_t r = blockIdx.x;
   const RowSpan<DT> row(p.logits, r * p.row_stride, p.V);
   const uint4* body = row.body();
-  const int nvec = static_cast<int>(row.nvec);
-  const int per = ((nvec + S - 1) / S + 7) & ~7;  // whole 128-byte lines
-  const int v0 = min(rank * per, nvec), v1 = min(v0 + per, nvec);
+  const int nvec = static_cast<int>(row.nvec), v0 = min(rank * p.per, nvec), v1 = min(v0 + p.per, nvec), mine = v1 - v0;
+  const int part = (mine + kParts - 1) / kParts;
   const bool scalar = rank == 0 && tid < row.scalars();
-  if (FWD && S > 1) cluster_arrive();  // its CTAs have started: waited for before the first store into another
-  const int quarter = (v1 - v0 + kGroups * NT - 1) / (kGroups * NT) * NT;  // vectors of one group
-  if (KEEP) {  // in flight while the row's parameters load
+  if (KEEP) {  // on their way while the row's parameters load
+    if (tid == 0) {
 #pragma unroll
-    for (int g = 0; g < kGroups; ++g) {
-      for (int k = g * quarter + tid; k < min((g + 1) * quarter, v1 - v0); k += NT) copy_async(kept + k, body + v0 + k);
-      copy_commit();
+      for (int g = 0; g < kParts; ++g) mbar_init(&full[g], 1);
+      mbar_init_fence();
+#pragma unroll
+      for (int g = 0; g < kParts; ++g) {
+        const int from = min(g * part, mine), bytes = (min(from + part, mine) - from) * 16;
+        mbar_arrive_expect_tx(&full[g], bytes);
+        if (bytes > 0) bulk_load(kept + from, body + v0 + from, bytes, &full[g]);
+      }
     }
+    __syncthreads();  // the barriers exist
   }
+  if (FWD && S > 1) cluster_arrive();  // the cluster's CTAs have started: waited for before the first store into another
   const float T = p.temperature[r];
   const int len = p.lengths[r];
   const int n = min(max(len, 0), p.W);
@@ -113,7 +111,7 @@ __global__ void __launch_bounds__(NT, MINB) distill_kernel(const __grid_constant
     id[e] = j < n ? ids[j] : 0;
     y[e] = j < n ? values[j] : -INFINITY;
   }
-  const float c = exponent_scale(T), T_y = p.normalise ? T : 1.f;
+  const float c = exponent_scale(T), inv_T = fminf(1.f / T, FLT_MAX), inv_Ty = p.normalise ? inv_T : 1.f;
   RowTerms q{__int_as_float(0x7fc00000), 1.f, 0.f, 0.f, 1.f};
   int status = SFC_ROW_OK;
   bool live;  // the row has a teacher and passes its checks: uniform over its CTAs
@@ -121,6 +119,7 @@ __global__ void __launch_bounds__(NT, MINB) distill_kernel(const __grid_constant
     if (len > p.W) status = SFC_ROW_OVERFLOW;
     if (!temperature_valid(T) || len < 0) status = SFC_ROW_BADPARAM;
     live = status != SFC_ROW_BADPARAM && n > 0;
+    bool late = false;
     if (live) {
       // the teacher: its mass, or its maximum and normaliser; an id outside the row makes it NaN
       SoftmaxAcc a, t;
@@ -130,9 +129,6 @@ __global__ void __launch_bounds__(NT, MINB) distill_kernel(const __grid_constant
         if (p.normalise) t.add(v, c);
         else mass += expf(v);
       };
-#pragma unroll
-      for (int e = 0; e < kPrefetch; ++e) entry(id[e], y[e]);
-      for (int j = tid + kPrefetch * NT; j < n; j += NT) entry(ids[j], values[j]);
       auto fold = [&](const uint4& w) {
         float x[VEC];
         Elem<DT>::unpack(w, x);
@@ -140,25 +136,26 @@ __global__ void __launch_bounds__(NT, MINB) distill_kernel(const __grid_constant
       };
       if (KEEP) {
 #pragma unroll
-        for (int g = 0; g < kGroups; ++g) {
-          if (g == 0) copy_wait<3>();
-          if (g == 1) copy_wait<2>();
-          if (g == 2) copy_wait<1>();
-          if (g == 3) copy_wait<0>();
+        for (int e = 0; e < kPrefetch; ++e)
+          if (tid + e * NT < n) entry(id[e], y[e]);
+        for (int j = tid + kPrefetch * NT; j < n; j += NT) entry(ids[j], values[j]);
+        for (int g = 0; g < kParts && !late; ++g) {
+          late = !__all_sync(kFull, mbar_wait(&full[g], 0));
+          const int to = min((g + 1) * part, mine);
+          if (!late) {
 #pragma unroll 2
-          for (int k = g * quarter + tid; k < min((g + 1) * quarter, v1 - v0); k += NT) fold(kept[k]);
+            for (int k = g * part + tid; k < to; k += NT) fold(kept[k]);
+          }
         }
       } else {
-        for (int k0 = v0 + tid; k0 < v1; k0 += NT * kStream) {
-          uint4 w[kStream];
+        RowStream<DT, NT, U> stream(row, v0, v1);
 #pragma unroll
-          for (int u = 0; u < kStream; ++u) w[u] = k0 + u * NT < v1 ? ld_once(body + k0 + u * NT) : Elem<DT>::neg_inf_vec();
-#pragma unroll
-          for (int u = 0; u < kStream; ++u) fold(w[u]);
-        }
+        for (int e = 0; e < kPrefetch; ++e)
+          if (tid + e * NT < n) entry(id[e], y[e]);
+        for (int j = tid + kPrefetch * NT; j < n; j += NT) entry(ids[j], values[j]);
+        stream.each([&](const uint4& w, int) { fold(w); });
       }
       if (scalar) a.add(row.at(row.scalar_index(tid)), c);
-      const int lane = tid & 31, wp = tid >> 5;
       const SoftmaxStats w = warp_stats(a, c);
       if (lane == 0) red[wp] = make_float2(w.m, w.s);
       if (p.normalise) {
@@ -168,14 +165,19 @@ __global__ void __launch_bounds__(NT, MINB) distill_kernel(const __grid_constant
         mass = warp_total(mass);
         if (lane == 0) red_mass[wp] = mass;
       }
-      __syncthreads();
+      if (KEEP) late = __syncthreads_or(late);
+      else __syncthreads();
       SoftmaxStats all = merge_warps<NT>(red, c);
+      if (KEEP && late) all = SoftmaxStats{-FLT_MAX, kLate};
       if (S > 1) {
         cluster_wait();
         if (tid < S) dsmem_st64(dsmem_addr(&table[rank], tid), pack_f2(all.m, all.s));
         cluster_sync_all();
-        all = SoftmaxStats{table[0].x, table[0].y};
-        for (int i = 1; i < S; ++i) all.merge(table[i].x, table[i].y, c);
+        // one lane per slice: its maximum first, then each mass rescaled, summed in a fixed order
+        const float2 v = table[lane < S ? lane : 0];
+        late = __any_sync(kFull, v.y == kLate);
+        all.m = warp_max(v.x);
+        all.s = warp_total(lane < S ? v.y * ex2_approx((v.x - all.m) * c) : 0.f);
       }
       q = RowTerms{all.m, all.s, 1.f, 0.f, 1.f};
       live = stats_valid(all.m, all.s);
@@ -188,22 +190,23 @@ __global__ void __launch_bounds__(NT, MINB) distill_kernel(const __grid_constant
         q.tau = warp_total(lane < NW ? red_mass[lane] : 0.f);
         live = live && q.tau < INFINITY;
       }
+      if (KEEP && late) live = false;
       if (!live) {
-        status = SFC_ROW_BADPARAM;
+        status = KEEP && late ? SFC_ROW_TIMEOUT : SFC_ROW_BADPARAM;
         q.m = __int_as_float(0x7fc00000);
       }
-    } else {
-      if (KEEP) copy_wait<0>();
-      if (S > 1) {
-        cluster_wait();
-        cluster_sync_all();
-      }
+    } else if (S > 1) {
+      cluster_wait();
+      cluster_sync_all();
     }
+    // nothing of the CTA's is still in flight when it ends
+    if (KEEP && !live && tid == 0)
+      for (int g = 0; g < kParts; ++g) mbar_wait(&full[g], 0);
   } else {
     q = unpack_terms(p.stats[r], p.normalise);
     live = q.m == q.m;
   }
-  const float g = BWD && live ? p.grad_loss[r] / T : 0.f;
+  const float g = BWD && live ? p.grad_loss[r] * inv_T : 0.f;
   const float k = live ? g * q.tau / q.s : 0.f, m = q.m;
   unsigned char* grad = BWD ? p.grad + r * p.grad_stride * Elem<DT>::kBytes : nullptr;
   if (BWD) {
@@ -217,10 +220,6 @@ __global__ void __launch_bounds__(NT, MINB) distill_kernel(const __grid_constant
       exponentials(x, minus_m2, c2, e2);
 #pragma unroll
       for (int e = 0; e < VEC / 2; ++e) unpack_f2(fmul_f2(e2[e], k2), x[2 * e], x[2 * e + 1]);
-      if (!live) {
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) x[e] = 0.f;
-      }
       if (same) {
         out[at] = Out<DT>::pack(x);
       } else {
@@ -228,19 +227,24 @@ __global__ void __launch_bounds__(NT, MINB) distill_kernel(const __grid_constant
         for (int e = 0; e < VEC; ++e) Out<DT>::store1(grad, row.head + static_cast<int64_t>(at) * VEC + e, x[e]);
       }
     };
-    if (KEEP) {
-#pragma unroll 2
-      for (int i = tid; i < v1 - v0; i += NT) put(v0 + i, kept[i]);
-    } else {
-      for (int k0 = v0 + tid; k0 < v1; k0 += NT * kStream) {
-        uint4 w[kStream];
+    if (!live) {
+      const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+      for (int i = v0 + tid; i < v1; i += NT) {
+        if (same) {
+          out[i] = zero;
+        } else {
 #pragma unroll
-        for (int u = 0; u < kStream; ++u)
-          if (k0 + u * NT < v1) w[u] = ld_once(body + k0 + u * NT);
-#pragma unroll
-        for (int u = 0; u < kStream; ++u)
-          if (k0 + u * NT < v1) put(k0 + u * NT, w[u]);
+          for (int e = 0; e < VEC; ++e) Out<DT>::store1(grad, row.head + static_cast<int64_t>(i) * VEC + e, 0.f);
+        }
       }
+    } else if (KEEP) {
+#pragma unroll 2
+      for (int i = tid; i < mine; i += NT) put(v0 + i, kept[i]);
+    } else {
+      RowStream<DT, NT, U> stream(row, v0, v1);
+      stream.each([&](const uint4& w, int at) {
+        if (at < v1) put(at, w);
+      });
     }
     if (scalar) {
       const int64_t i = row.scalar_index(tid);
@@ -250,14 +254,14 @@ __global__ void __launch_bounds__(NT, MINB) distill_kernel(const __grid_constant
   }
   float loss = 0.f;
   if (live) {
-    const float ln_ty = logf(q.ty);
+    const float ln_ty = p.normalise ? logf(q.ty) : 0.f;
     const int64_t lo = row.head + static_cast<int64_t>(v0) * VEC, hi = row.head + static_cast<int64_t>(v1) * VEC;
     auto entry = [&](int32_t i, float v) {
       const bool body_entry = i >= lo && i < hi;
       if (!body_entry && !(rank == 0 && (i < row.head || i >= row.tail()))) return;
-      const float ln_t = (v - q.y0) / T_y - ln_ty, e = expf(ln_t);
+      const float ln_t = (v - q.y0) * inv_Ty - ln_ty, e = expf(ln_t);
       const float x = KEEP && body_entry ? Elem<DT>::load1(reinterpret_cast<const unsigned char*>(kept), i - lo) : row.at(i);
-      if (FWD && e > 0.f) loss += e * (ln_t - (x - m) / T);
+      if (FWD && e > 0.f) loss += e * (ln_t - (x - m) * inv_T);
       if (BWD) Out<DT>::store1(grad, i, k * ex2_approx((x - m) * c) - e * g);
     };
 #pragma unroll
@@ -266,16 +270,22 @@ __global__ void __launch_bounds__(NT, MINB) distill_kernel(const __grid_constant
     for (int j = tid + kPrefetch * NT; j < n; j += NT) entry(ids[j], values[j]);
   }
   if (!FWD) return;
-  loss = block_total<NT>(loss, red_loss);
+  loss = warp_total(loss);
+  if (lane == 0) red_loss[wp] = loss;
+  __syncthreads();
   if (S > 1) {
-    if (tid == 0) dsmem_st32(dsmem_addr(&losses[rank], 0), __float_as_uint(loss));
+    if (tid == 0) {
+      loss = red_loss[0];
+      for (int i = 1; i < NW; ++i) loss += red_loss[i];
+      dsmem_st32(dsmem_addr(&losses[rank], 0), __float_as_uint(loss));
+    }
     cluster_sync_all();
     if (rank != 0) return;
-    loss = losses[0];
-    for (int i = 1; i < S; ++i) loss += losses[i];
   }
   if (tid == 0) {
-    p.loss[r] = live ? loss + q.tau * logf(q.s) : (status == SFC_ROW_BADPARAM ? __int_as_float(0x7fc00000) : 0.f);
+    loss = S > 1 ? losses[0] : red_loss[0];
+    for (int i = 1; i < (S > 1 ? S : NW); ++i) loss += S > 1 ? losses[i] : red_loss[i];
+    p.loss[r] = live ? loss + q.tau * logf(q.s) : (status < 0 ? __int_as_float(0x7fc00000) : 0.f);
     p.row_status[r] = status;
     if (p.stats) p.stats[r] = pack_terms(q, p.normalise);
   }
@@ -304,21 +314,23 @@ int check_grad(const void* logits, int dtype, int64_t B, int64_t V, int64_t row_
 }
 
 template <int DT, int NT, int MINB, bool KEEP, bool FWD, bool BWD>
-cudaError_t start(const DistillParams& p, int64_t B, cudaStream_t stream) {
+cudaError_t start(DistillParams p, int64_t B, cudaStream_t stream) {
   auto kern = distill_kernel<DT, NT, MINB, KEEP, FWD, BWD>;
+  const int64_t vectors = p.V / Elem<DT>::kVec;
+  p.per = static_cast<int32_t>((vectors + p.slices - 1) / p.slices + 7) & ~7;  // whole 128-byte lines
   cudaLaunchConfig_t cfg = {};
   if (KEEP) {
-    const int64_t vectors = p.V / Elem<DT>::kVec;
-    cfg.dynamicSmemBytes = static_cast<size_t>(((vectors + p.slices - 1) / p.slices + 7) & ~int64_t{7}) * 16;
-    const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kKeepBytes / MINB);
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t err = allow_shared(kern, kKeepBytes / MINB, done);
     if (err != cudaSuccess) return err;
+    cfg.dynamicSmemBytes = static_cast<size_t>(p.per) * 16;
   }
-  cfg.gridDim = dim3(static_cast<unsigned>(B * p.slices));
+  cfg.gridDim = dim3(static_cast<unsigned>(B), static_cast<unsigned>(p.slices));
   cfg.blockDim = dim3(NT);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim = {static_cast<unsigned>(p.slices), 1, 1};
+  attr[0].val.clusterDim = {1, static_cast<unsigned>(p.slices), 1};
   cfg.attrs = attr;
   cfg.numAttrs = FWD && p.slices > 1 ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, kern, p);
@@ -329,8 +341,8 @@ cudaError_t choose(DistillParams& p, int64_t B, cudaStream_t stream) {
   const int64_t vectors = p.V / Elem<DT>::kVec;
   auto cut = [&](int64_t per) { return std::max<int64_t>(1, (vectors + per - 1) / per); };
   auto fits = [&](int64_t S) {
-    p.slices = static_cast<int32_t>(S);
-    return S <= kMaxSlices && B * S <= INT32_MAX;
+    p.slices = static_cast<int32_t>(std::min<int64_t>(S, kMaxSlices));
+    return S <= kMaxSlices;
   };
   // few rows: enough slices to fill the GPU's 304 CTA slots, of at least two vectors per thread
   const int64_t fill = std::min<int64_t>({kMaxSlices, cut(1024), (304 + B - 1) / B});
@@ -338,7 +350,7 @@ cudaError_t choose(DistillParams& p, int64_t B, cudaStream_t stream) {
     if (fits(std::max(fill, cut(kKeepBytes / 2 / 16 - 8)))) return start<DT, 512, 2, true, true, true>(p, B, stream);
     if (fits(cut(kKeepBytes / 16 - 8))) return start<DT, 1024, 1, true, true, true>(p, B, stream);
   }
-  if (!fits(FWD ? fill : std::max(fill, std::min<int64_t>(kMaxSlices, cut(8192))))) p.slices = 1;
+  fits(FWD ? fill : std::max(fill, cut(8192)));
   return start<DT, 512, 2, false, FWD, BWD>(p, B, stream);
 }
 
@@ -366,7 +378,7 @@ extern "C" int sfc_distill_forward(const void* logits, int dtype, int64_t B, int
   if (!loss || !row_status || reinterpret_cast<uintptr_t>(row_stats) % 16) return SFC_EINVAL;
   const sfc::DistillParams p{logits, row_stride, V, packed_width, (flags & SFC_FLAG_NORMALISE_TEACHER) != 0,
                              temperature, teacher_ids, teacher_values, lengths, nullptr, loss,
-                             reinterpret_cast<float4*>(row_stats), row_status, nullptr, 0, 1};
+                             reinterpret_cast<float4*>(row_stats), row_status, nullptr, 0, 1, 0};
   return sfc::launch<true, false>(p, dtype, B, stream);
 }
 
@@ -383,7 +395,7 @@ extern "C" int sfc_distill_backward(const void* logits, int dtype, int64_t B, in
   const sfc::DistillParams p{logits, row_stride, V, packed_width, (flags & SFC_FLAG_NORMALISE_TEACHER) != 0,
                              temperature, teacher_ids, teacher_values, lengths, grad_loss, nullptr,
                              const_cast<float4*>(reinterpret_cast<const float4*>(row_stats)), nullptr,
-                             static_cast<unsigned char*>(grad_logits), grad_stride, 1};
+                             static_cast<unsigned char*>(grad_logits), grad_stride, 1, 0};
   return sfc::launch<false, true>(p, dtype, B, stream);
 }
 
@@ -400,6 +412,6 @@ extern "C" int sfc_distill_forward_backward(const void* logits, int dtype, int64
   if (!loss || !row_status) return SFC_EINVAL;
   const sfc::DistillParams p{logits, row_stride, V, packed_width, (flags & SFC_FLAG_NORMALISE_TEACHER) != 0,
                              temperature, teacher_ids, teacher_values, lengths, grad_loss, loss, nullptr, row_status,
-                             static_cast<unsigned char*>(grad_logits), grad_stride, 1};
+                             static_cast<unsigned char*>(grad_logits), grad_stride, 1, 0};
   return sfc::launch<true, true>(p, dtype, B, stream);
 }

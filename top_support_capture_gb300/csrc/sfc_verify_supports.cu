@@ -13,6 +13,7 @@
 #include <cstdint>
 
 #include "../../include/sfc.h"
+#include "sfc_host.cuh"
 #include "sfc_verify.cuh"
 
 namespace sfc {
@@ -238,7 +239,8 @@ template <int NT>
 cudaError_t start(const VerifySupportsParams& p, int64_t B, cudaStream_t stream) {
   const int smem = p.draft.ids ? p.table * static_cast<int>(sizeof(uint16_t)) : 0;  // at most 64 KB
   if (smem > 40 * 1024) {
-    const cudaError_t err = cudaFuncSetAttribute(verify_supports_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t err = allow_shared(verify_supports_kernel<NT>, 65536, done);
     if (err != cudaSuccess) return err;
   }
   verify_supports_kernel<NT><<<static_cast<unsigned>(B), NT, smem, stream>>>(p);

@@ -30,7 +30,7 @@ def verify_workspace_size(B: int, D: int, V: int, dtype: int) -> int:
 
 
 def _workspace(nbytes, device, stream):
-    key = (device.index, int(stream.cuda_stream))
+    key = (device.index, stream)
     ws = _workspaces.get(key)
     if ws is None or ws.numel() < nbytes:
         if torch.cuda.is_current_stream_capturing():
@@ -100,7 +100,7 @@ def verify_drafts(target_logits, draft_logits, draft_tokens, uniforms, temperatu
                                    _ptr(draft_temperature), _ptr(draft_tokens), _ptr(num_drafts), _ptr(uniforms), _u64(seed),
                                    _u64(step), int(row_offset), FLAG_GREEDY_T0 if greedy_t0 else 0, _ptr(out.accepted),
                                    _ptr(out.tokens), _ptr(out.token_logprobs), _ptr(out.row_status), _ptr(workspace),
-                                   workspace.numel() * workspace.element_size(), int(stream.cuda_stream))
+                                   workspace.numel() * workspace.element_size(), stream)
     if rc != SFC_OK:
         raise SfcError(f"sfc_verify_drafts: {strerror(rc)} ({rc})")
     return out
@@ -142,7 +142,7 @@ def verify_supports(target_ids, target_logprobs, target_lengths, draft_ids, draf
         rc = lib.sfc_verify_supports(_ptr(target_ids), _ptr(target_logprobs), _ptr(target_lengths), W, _ptr(draft_ids),
                                      _ptr(draft_logprobs), _ptr(draft_lengths), Wd, B, D, _ptr(draft_tokens), _ptr(num_drafts),
                                      _ptr(uniforms), _u64(seed), _u64(step), int(row_offset), _ptr(out.accepted),
-                                     _ptr(out.tokens), _ptr(out.token_logprobs), _ptr(out.row_status), int(stream.cuda_stream))
+                                     _ptr(out.tokens), _ptr(out.token_logprobs), _ptr(out.row_status), stream)
     if rc != SFC_OK:
         raise SfcError(f"sfc_verify_supports: {strerror(rc)} ({rc})")
     return out

@@ -27,22 +27,25 @@ class DistillGradOutput(NamedTuple):
 
 
 def check_rows(name, t):
-    """[B, V] rows of a CUDA tensor, each contiguous."""
+    """[B, V] rows of a CUDA tensor, each contiguous; returns the row stride."""
     if not t.is_cuda:
         raise SfcError(f"{name} must be a CUDA tensor, got {t.device}")
-    check_row_layout(name, t)
+    return check_row_layout(name, t)
 
 
 def check_row_layout(name, t):
     """A floating [B, V] tensor whose rows are contiguous and do not overlap; returns the row stride."""
-    if t.dim() != 2 or t.shape[0] < 1 or t.shape[1] < 1:
+    if t.dim() != 2 or t.numel() < 1:
         raise SfcError(f"{name} must be a non-empty [B, V] tensor")
     _dtype_code(t)
-    if t.stride(1) != 1 and t.shape[1] > 1:
+    (B, V), (row, one) = t.shape, t.stride()
+    if one != 1 and V > 1:
         raise SfcError(f"{name} rows must be contiguous")
-    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
-        raise SfcError(f"{name} rows must not overlap (an expanded tensor: make it contiguous)")
-    return int(t.stride(0)) if t.shape[0] > 1 else max(int(t.stride(0)), int(t.shape[1]))
+    if row < V:
+        if B > 1:
+            raise SfcError(f"{name} rows must not overlap (an expanded tensor: make it contiguous)")
+        row = V
+    return row
 
 
 def check_packed(logits, temperature, ids, lengths, values=None, values_name="teacher_values", ids_name="teacher_ids"):
@@ -66,39 +69,39 @@ def _raise(name, rc):
 
 
 def _check_grad(grad, logits):
-    check_row_layout("grad", grad)
     if grad.device != logits.device or grad.dtype != logits.dtype or grad.shape != logits.shape:
         raise SfcError("grad must have the logits' device, dtype and shape")
+    return check_row_layout("grad", grad)
 
 
-def _rows_args(logits, temperature):
-    B, V = int(logits.shape[0]), int(logits.shape[1])
-    return _ptr(logits), _dtype_code(logits), B, V, check_row_layout("logits", logits), _ptr(temperature)
+def _rows_args(logits, stride, temperature):
+    B, V = logits.shape
+    return logits.data_ptr(), _dtype_code(logits), B, V, stride, temperature.data_ptr()
 
 
 def _teacher_args(ids, values, lengths, normalise):
     return _ptr(ids), _ptr(values), _ptr(lengths), int(ids.shape[1]), FLAG_NORMALISE_TEACHER if normalise else 0
 
 
-def _distill_forward(logits, temperature, ids, values, lengths, normalise, stream, keep_stats):
+def _distill_forward(logits, stride, temperature, ids, values, lengths, normalise, stream, keep_stats):
     dev, B = logits.device, int(logits.shape[0])
     stream, context = _enter(dev, stream)
     with context:
         loss = torch.empty(B, dtype=torch.float32, device=dev)
         stats = torch.empty((B, 4), dtype=torch.float32, device=dev) if keep_stats else None
         status = torch.empty(B, dtype=torch.int32, device=dev)
-        rc = load_library().sfc_distill_forward(*_rows_args(logits, temperature), *_teacher_args(ids, values, lengths, normalise),
-                                                _ptr(loss), _ptr(stats), _ptr(status), int(stream.cuda_stream))
+        rc = load_library().sfc_distill_forward(*_rows_args(logits, stride, temperature), *_teacher_args(ids, values, lengths, normalise),
+                                                _ptr(loss), _ptr(stats), _ptr(status), stream)
     _raise("sfc_distill_forward", rc)
     return loss, stats, status
 
 
 class _Distill(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, logits, temperature, ids, values, lengths, normalise):
-        loss, stats, status = _distill_forward(logits, temperature, ids, values, lengths, normalise, None, True)
+    def forward(ctx, logits, stride, temperature, ids, values, lengths, normalise):
+        loss, stats, status = _distill_forward(logits, stride, temperature, ids, values, lengths, normalise, None, True)
         ctx.save_for_backward(logits, temperature, ids, values, lengths, stats)
-        ctx.normalise = normalise
+        ctx.normalise, ctx.stride = normalise, stride
         ctx.mark_non_differentiable(status)
         return loss, status
 
@@ -111,11 +114,11 @@ class _Distill(torch.autograd.Function):
         with context:
             grad_loss = grad_loss.to(torch.float32).contiguous()
             grad = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
-            rc = load_library().sfc_distill_backward(*_rows_args(logits, temperature),
+            rc = load_library().sfc_distill_backward(*_rows_args(logits, ctx.stride, temperature),
                                                      *_teacher_args(ids, values, lengths, ctx.normalise), _ptr(stats),
-                                                     _ptr(grad_loss), _ptr(grad), int(logits.shape[1]), int(stream.cuda_stream))
+                                                     _ptr(grad_loss), _ptr(grad), int(logits.shape[1]), stream)
         _raise("sfc_distill_backward", rc)
-        return grad, None, None, None, None, None
+        return grad, None, None, None, None, None, None
 
 
 def distill_loss(logits, temperature, teacher_ids, teacher_values, lengths, normalise: bool = False,
@@ -124,15 +127,15 @@ def distill_loss(logits, temperature, teacher_ids, teacher_values, lengths, norm
     ``teacher_ids`` [B, W] int32 with ``teacher_values`` [B, W] f32, log-probabilities (a capture's
     ``support_ids`` and ``support_logprobs``) or, with ``normalise``, raw top logits; ``lengths`` [B] int32 (0:
     the row has no teacher). Differentiable in ``logits``. See include/sfc.h."""
-    check_rows("logits", logits)
+    row = check_rows("logits", logits)
     check_packed(logits, temperature, teacher_ids, lengths, teacher_values)
     if teacher_values is None:
         raise SfcError("teacher_values is required")
     if torch.is_grad_enabled() and logits.requires_grad:
         stream, context = _enter(logits.device, stream)
         with context:
-            return DistillOutput(*_Distill.apply(logits, temperature, teacher_ids, teacher_values, lengths, bool(normalise)))
-    loss, _, status = _distill_forward(logits, temperature, teacher_ids, teacher_values, lengths, normalise, stream, False)
+            return DistillOutput(*_Distill.apply(logits, row, temperature, teacher_ids, teacher_values, lengths, bool(normalise)))
+    loss, _, status = _distill_forward(logits, row, temperature, teacher_ids, teacher_values, lengths, normalise, stream, False)
     return DistillOutput(loss, status)
 
 
@@ -141,14 +144,13 @@ def distill_loss_and_grad(logits, temperature, teacher_ids, teacher_values, leng
     """``distill_loss`` and its gradient in one call, for a known upstream gradient ``grad_loss`` [B] f32 (a mean
     over the batch: 1 / B each): the logits are read once. ``grad`` may give the [B, V] tensor to write (not the
     logits themselves). Outside autograd."""
-    check_rows("logits", logits)
+    row = check_rows("logits", logits)
     check_packed(logits, temperature, teacher_ids, lengths, teacher_values)
     if teacher_values is None:
         raise SfcError("teacher_values is required")
     dev, B = logits.device, int(logits.shape[0])
     _check_tensor("grad_loss", grad_loss, dev, torch.float32, numel=B)
-    if grad is not None:
-        _check_grad(grad, logits)
+    grad_row = logits.shape[1] if grad is None else _check_grad(grad, logits)
     stream, context = _enter(dev, stream)
     with context:
         loss = torch.empty(B, dtype=torch.float32, device=dev)
@@ -156,8 +158,8 @@ def distill_loss_and_grad(logits, temperature, teacher_ids, teacher_values, leng
         if grad is None:
             grad = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
         rc = load_library().sfc_distill_forward_backward(
-            *_rows_args(logits, temperature), *_teacher_args(teacher_ids, teacher_values, lengths, normalise), _ptr(grad_loss),
-            _ptr(loss), _ptr(status), _ptr(grad), check_row_layout("grad", grad), int(stream.cuda_stream))
+            *_rows_args(logits, row, temperature), *_teacher_args(teacher_ids, teacher_values, lengths, normalise), _ptr(grad_loss),
+            _ptr(loss), _ptr(status), _ptr(grad), grad_row, stream)
     _raise("sfc_distill_forward_backward", rc)
     return DistillGradOutput(loss, grad, status)
 
@@ -167,20 +169,19 @@ def replay_logprob_backward(logits, temperature, support_ids, lengths, tokens, g
     """The gradient of ``replay_logprob`` with respect to ``logits`` [B, V], from the upstream gradients
     ``grad_token_logprob`` [B] f32 and, where it is given, ``grad_support_logprobs`` [B, W] f32: a dense
     [B, V] tensor of the logits' dtype, zero outside the supports (written into ``grad`` when that is given)."""
-    check_rows("logits", logits)
+    row = check_rows("logits", logits)
     dev, B = logits.device, int(logits.shape[0])
     W = check_packed(logits, temperature, support_ids, lengths, grad_support_logprobs, "grad_support_logprobs", "support_ids")
     _check_tensor("tokens", tokens, dev, torch.int32, numel=B)
     _check_tensor("grad_token_logprob", grad_token_logprob, dev, torch.float32, numel=B)
-    if grad is not None:
-        _check_grad(grad, logits)
+    grad_row = logits.shape[1] if grad is None else _check_grad(grad, logits)
     stream, context = _enter(dev, stream)
     with context:
         if grad is None:
             grad = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
-        rc = load_library().sfc_replay_backward(*_rows_args(logits, temperature), _ptr(support_ids), _ptr(lengths), W,
+        rc = load_library().sfc_replay_backward(*_rows_args(logits, row, temperature), _ptr(support_ids), _ptr(lengths), W,
                                                 _ptr(tokens), _ptr(grad_token_logprob), _ptr(grad_support_logprobs),
-                                                _ptr(grad), check_row_layout("grad", grad), int(stream.cuda_stream))
+                                                _ptr(grad), grad_row, stream)
     _raise("sfc_replay_backward", rc)
     return grad
 
