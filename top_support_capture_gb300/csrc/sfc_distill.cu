@@ -10,8 +10,12 @@
 // all hold the same bits. The teacher's mass is small work: every CTA sums it for itself.
 //
 // In the call that gives loss and gradient the slice stays in shared memory between its two uses, so the logits are
-// read from HBM once: one thread starts the bulk copies of its four parts before anything else, and the statistics
-// begin when the first has landed. Every wait for a copy is bounded (SFC_ROW_TIMEOUT). Rows longer than a cluster's shared memory are read again.
+// read from HBM once: one thread starts a bulk copy of it before anything else. The wait for the copy is bounded
+// (SFC_ROW_TIMEOUT). 2048 x 151936 bf16: 260 us (0.71 of the measured copy rate); 262 / 274 us with the copy in two /
+// four parts that are waited for one by one; 248 us with clusters that go from row to row and start the next copy as
+// the slice is used up, at the price of slower small calls (9.0 against 7.8 us) and twice the code; 282-300 us with
+// three CTAs a SM. Issue slots and HBM are each about half busy: the CTAs of a SM read, compute and write in turns.
+// Rows longer than a cluster's shared memory are read again.
 //
 // The gradient's dense part tau p_j g / T is written first; after the CTA's barrier the teacher's entries that lie
 // in the slice overwrite theirs with the whole gradient, each rounded once, and add their part of the loss.
@@ -60,18 +64,17 @@ __device__ __forceinline__ RowTerms unpack_terms(const float4& v, bool normalise
 }
 
 constexpr int kMaxSlices = 8;  // the portable cluster size
-constexpr int kParts = 4;      // bulk copies of a kept slice
 constexpr int kKeepBytes = 212992;  // shared memory of one SM that keeps logits: 13 vectors for each of 1024 threads
-constexpr int kPrefetch = 2;   // teacher entries per thread held from the start
 constexpr float kLate = -1.f;  // in place of a mass: a copy did not arrive
 
 // KEEP: the slice's vectors lie in dynamic shared memory (16 bytes for each).
 template <int DT, int NT, int MINB, bool KEEP, bool FWD, bool BWD>
 __global__ void __launch_bounds__(NT, MINB) distill_kernel(const __grid_constant__ DistillParams p) {
   constexpr int NW = NT / 32, VEC = Elem<DT>::kVec;
-  constexpr int U = BWD ? 4 : 2;  // vectors in flight per thread where they are not kept (and as many again)
+  constexpr int U = 4;  // vectors in flight per thread where they are not kept (and as many again)
+  constexpr int kBatch = KEEP ? 2 : 4;  // teacher entries that a thread has on their way at once
   extern __shared__ __align__(128) uint4 kept[];
-  __shared__ uint64_t full[kParts];
+  __shared__ uint64_t full;
   __shared__ float2 red[2 * NW];
   __shared__ float red_mass[NW], red_loss[NW];
   __shared__ float2 table[kMaxSlices];  // (m, s) of the slices
@@ -81,21 +84,15 @@ __global__ void __launch_bounds__(NT, MINB) distill_kernel(const __grid_constant
   const RowSpan<DT> row(p.logits, r * p.row_stride, p.V);
   const uint4* body = row.body();
   const int nvec = static_cast<int>(row.nvec), v0 = min(rank * p.per, nvec), v1 = min(v0 + p.per, nvec), mine = v1 - v0;
-  const int part = (mine + kParts - 1) / kParts;
   const bool scalar = rank == 0 && tid < row.scalars();
   if (KEEP) {  // on their way while the row's parameters load
     if (tid == 0) {
-#pragma unroll
-      for (int g = 0; g < kParts; ++g) mbar_init(&full[g], 1);
+      mbar_init(&full, 1);
       mbar_init_fence();
-#pragma unroll
-      for (int g = 0; g < kParts; ++g) {
-        const int from = min(g * part, mine), bytes = (min(from + part, mine) - from) * 16;
-        mbar_arrive_expect_tx(&full[g], bytes);
-        if (bytes > 0) bulk_load(kept + from, body + v0 + from, bytes, &full[g]);
-      }
+      mbar_arrive_expect_tx(&full, mine * 16);
+      if (mine > 0) bulk_load(kept, body + v0, mine * 16, &full);
     }
-    __syncthreads();  // the barriers exist
+    __syncthreads();  // the barrier exists
   }
   if (FWD && S > 1) cluster_arrive();  // the cluster's CTAs have started: waited for before the first store into another
   const float T = p.temperature[r];
@@ -103,14 +100,30 @@ __global__ void __launch_bounds__(NT, MINB) distill_kernel(const __grid_constant
   const int n = min(max(len, 0), p.W);
   const int32_t* ids = p.ids + r * p.W;
   const float* values = p.values + r * p.W;
-  int32_t id[kPrefetch];
-  float y[kPrefetch];
+  // the row's entries, a batch at a time (the first is on its way from here): use(ids, values), past the end -1
+  struct Entries {
+    int32_t id[kBatch];
+    float y[kBatch];
+  };
+  auto load = [&](int j0) {
+    Entries b;
 #pragma unroll
-  for (int e = 0; e < kPrefetch; ++e) {
-    const int j = tid + e * NT;
-    id[e] = j < n ? ids[j] : 0;
-    y[e] = j < n ? values[j] : -INFINITY;
-  }
+    for (int e = 0; e < kBatch; ++e) {
+      const int j = j0 + e * NT;
+      b.id[e] = j < n ? ids[j] : -1;
+      b.y[e] = j < n ? values[j] : 0.f;
+    }
+    return b;
+  };
+  const Entries first = load(tid);
+  auto entries = [&](auto use) {
+    Entries b = first;
+    for (int j0 = tid; j0 < n; j0 += kBatch * NT) {
+      const Entries next = load(j0 + kBatch * NT);
+      use(b, j0);
+      b = next;
+    }
+  };
   const float c = exponent_scale(T), inv_T = fminf(1.f / T, FLT_MAX), inv_Ty = p.normalise ? inv_T : 1.f;
   RowTerms q{__int_as_float(0x7fc00000), 1.f, 0.f, 0.f, 1.f};
   int status = SFC_ROW_OK;
@@ -124,10 +137,16 @@ __global__ void __launch_bounds__(NT, MINB) distill_kernel(const __grid_constant
       // the teacher: its mass, or its maximum and normaliser; an id outside the row makes it NaN
       SoftmaxAcc a, t;
       float mass = 0.f;
-      auto entry = [&](int32_t i, float v) {
-        if (i < 0 || i >= p.V) v = __int_as_float(0x7fc00000);
-        if (p.normalise) t.add(v, c);
-        else mass += expf(v);
+      auto teacher_mass = [&] {
+        entries([&](const Entries& b, int j0) {
+#pragma unroll
+          for (int e = 0; e < kBatch; ++e) {
+            if (j0 + e * NT >= n) break;
+            const float v = b.id[e] < 0 || b.id[e] >= p.V ? __int_as_float(0x7fc00000) : b.y[e];
+            if (p.normalise) t.add(v, c);
+            else mass += expf(v);
+          }
+        });
       };
       auto fold = [&](const uint4& w) {
         float x[VEC];
@@ -135,24 +154,15 @@ __global__ void __launch_bounds__(NT, MINB) distill_kernel(const __grid_constant
         a.add(x, Elem<DT>::vmax(w), c);
       };
       if (KEEP) {
-#pragma unroll
-        for (int e = 0; e < kPrefetch; ++e)
-          if (tid + e * NT < n) entry(id[e], y[e]);
-        for (int j = tid + kPrefetch * NT; j < n; j += NT) entry(ids[j], values[j]);
-        for (int g = 0; g < kParts && !late; ++g) {
-          late = !__all_sync(kFull, mbar_wait(&full[g], 0));
-          const int to = min((g + 1) * part, mine);
-          if (!late) {
+        teacher_mass();
+        late = !__all_sync(kFull, mbar_wait(&full, 0));
+        if (!late) {
 #pragma unroll 2
-            for (int k = g * part + tid; k < to; k += NT) fold(kept[k]);
-          }
+          for (int k = tid; k < mine; k += NT) fold(kept[k]);
         }
       } else {
         RowStream<DT, NT, U> stream(row, v0, v1);
-#pragma unroll
-        for (int e = 0; e < kPrefetch; ++e)
-          if (tid + e * NT < n) entry(id[e], y[e]);
-        for (int j = tid + kPrefetch * NT; j < n; j += NT) entry(ids[j], values[j]);
+        teacher_mass();
         stream.each([&](const uint4& w, int) { fold(w); });
       }
       if (scalar) a.add(row.at(row.scalar_index(tid)), c);
@@ -200,8 +210,7 @@ __global__ void __launch_bounds__(NT, MINB) distill_kernel(const __grid_constant
       cluster_sync_all();
     }
     // nothing of the CTA's is still in flight when it ends
-    if (KEEP && !live && tid == 0)
-      for (int g = 0; g < kParts; ++g) mbar_wait(&full[g], 0);
+    if (KEEP && !live && tid == 0) mbar_wait(&full, 0);
   } else {
     q = unpack_terms(p.stats[r], p.normalise);
     live = q.m == q.m;
@@ -255,19 +264,27 @@ __global__ void __launch_bounds__(NT, MINB) distill_kernel(const __grid_constant
   float loss = 0.f;
   if (live) {
     const float ln_ty = p.normalise ? logf(q.ty) : 0.f;
-    const int64_t lo = row.head + static_cast<int64_t>(v0) * VEC, hi = row.head + static_cast<int64_t>(v1) * VEC;
-    auto entry = [&](int32_t i, float v) {
-      const bool body_entry = i >= lo && i < hi;
-      if (!body_entry && !(rank == 0 && (i < row.head || i >= row.tail()))) return;
-      const float ln_t = (v - q.y0) * inv_Ty - ln_ty, e = expf(ln_t);
-      const float x = KEEP && body_entry ? Elem<DT>::load1(reinterpret_cast<const unsigned char*>(kept), i - lo) : row.at(i);
-      if (FWD && e > 0.f) loss += e * (ln_t - (x - m) * inv_T);
-      if (BWD) Out<DT>::store1(grad, i, k * ex2_approx((x - m) * c) - e * g);
-    };
+    const int32_t lo = row.head + v0 * VEC, span = (v1 - v0) * VEC, tail = static_cast<int32_t>(row.tail());
+    entries([&](const Entries& b, int) {
+      float x[kBatch];
+      bool here[kBatch];
 #pragma unroll
-    for (int e = 0; e < kPrefetch; ++e)
-      if (tid + e * NT < n) entry(id[e], y[e]);
-    for (int j = tid + kPrefetch * NT; j < n; j += NT) entry(ids[j], values[j]);
+      for (int e = 0; e < kBatch; ++e) {  // an entry of this slice (the first has the elements outside the body)
+        const int32_t i = b.id[e];
+        const bool body_entry = static_cast<uint32_t>(i - lo) < static_cast<uint32_t>(span);
+        here[e] = body_entry || (rank == 0 && i >= 0 && (i < row.head || i >= tail));
+        x[e] = !here[e] ? 0.f
+               : KEEP && body_entry ? Elem<DT>::load1(reinterpret_cast<const unsigned char*>(kept), i - lo)
+                                    : row.at(i);
+      }
+#pragma unroll
+      for (int e = 0; e < kBatch; ++e) {
+        if (!here[e]) continue;
+        const float ln_t = (b.y[e] - q.y0) * inv_Ty - ln_ty, w = expf(ln_t);
+        if (FWD && w > 0.f) loss += w * (ln_t - (x[e] - m) * inv_T);
+        if (BWD) Out<DT>::store1(grad, b.id[e], k * ex2_approx((x[e] - m) * c) - w * g);
+      }
+    });
   }
   if (!FWD) return;
   loss = warp_total(loss);

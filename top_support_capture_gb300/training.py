@@ -102,12 +102,15 @@ class _Distill(torch.autograd.Function):
         loss, stats, status = _distill_forward(logits, stride, temperature, ids, values, lengths, normalise, None, True)
         ctx.save_for_backward(logits, temperature, ids, values, lengths, stats)
         ctx.normalise, ctx.stride = normalise, stride
+        ctx.set_materialize_grads(False)  # none is made for the status
         ctx.mark_non_differentiable(status)
         return loss, status
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, grad_loss, _):
+        if grad_loss is None:
+            return (None,) * 7
         logits, temperature, ids, values, lengths, stats = ctx.saved_tensors
         dev = logits.device
         stream, context = _enter(dev, None)  # autograd runs a backward on its forward's stream
