@@ -105,6 +105,36 @@ struct SoftmaxAcc {
   }
 };
 
+// The same against a fixed reference m in place of the maximum, which no vector's maximum has to be found for (a
+// quarter of the fold's instructions). m is the first vector's maximum; the sum overflows only where a later logit
+// is more than about 88 T above it (or infinite, or NaN), and then the caller takes the statistics again with
+// SoftmaxAcc.
+struct ReferenceAcc {
+  float m = -FLT_MAX;
+  uint64_t s2 = 0;
+
+  __device__ __forceinline__ void start(float first) { m = fabsf(first) < 1e30f ? first : 0.f; }
+  template <int N>
+  __device__ __forceinline__ void add(const float (&x)[N], uint64_t minus_m, uint64_t c) {
+    uint64_t e[N / 2];
+    exponentials(x, minus_m, c, e);
+#pragma unroll
+    for (int w = N / 4; w > 0; w /= 2)  // a fixed tree
+#pragma unroll
+      for (int i = 0; i < w; ++i) e[i] = fadd_f2(e[i], e[i + w]);
+    s2 = fadd_f2(s2, e[0]);
+  }
+  __device__ __forceinline__ void add(float x, float c) {
+    if (m == -FLT_MAX) start(x);
+    s2 = fadd_f2(s2, pack_f2(ex2_approx((x - m) * c), 0.f));
+  }
+  __device__ __forceinline__ float sum() const {
+    float a, b;
+    unpack_f2(s2, a, b);
+    return a + b;
+  }
+};
+
 // Merged statistics: of a warp, a CTA, a row.
 struct SoftmaxStats {
   float m, s;
@@ -116,7 +146,7 @@ struct SoftmaxStats {
   }
 };
 
-// A finite maximum and a mass: false for rows with NaN or +inf logits (s is NaN) or without a finite one.
+// A finite reference and a mass: false for rows with NaN or +inf logits (s is NaN) or without a finite one.
 __device__ __forceinline__ bool stats_valid(float m, float s) { return s > 0.f && s < INFINITY && m < INFINITY; }
 
 __device__ __forceinline__ float warp_total(float x) {  // butterflies: the same bits in every lane
@@ -126,7 +156,8 @@ __device__ __forceinline__ float warp_total(float x) {  // butterflies: the same
 }
 
 // The warp's statistics: its maximum first, then each thread's sum rescaled once.
-__device__ __forceinline__ SoftmaxStats warp_stats(const SoftmaxAcc& a, float c) {
+template <class Acc>
+__device__ __forceinline__ SoftmaxStats warp_stats(const Acc& a, float c) {
   const float m = warp_max(a.m);
   return SoftmaxStats{m, warp_total(a.sum() * ex2_approx((a.m - m) * c))};
 }
@@ -141,8 +172,8 @@ __device__ __forceinline__ SoftmaxStats merge_warps(const float2* red, float c) 
 
 // The accumulators of the CTA's NT threads as one, in a fixed order, the same bits in every thread. `red` holds
 // NT / 32 entries; a barrier must separate two uses of it.
-template <int NT>
-__device__ __forceinline__ SoftmaxStats block_stats(const SoftmaxAcc& a, float c, float2* red) {
+template <int NT, class Acc>
+__device__ __forceinline__ SoftmaxStats block_stats(const Acc& a, float c, float2* red) {
   const SoftmaxStats w = warp_stats(a, c);
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = make_float2(w.m, w.s);
   __syncthreads();

@@ -29,9 +29,9 @@
 namespace sfc {
 namespace {
 
-constexpr int kStatThreads = 512, kStatUnroll = 2, kDrawThreads = 256;
-constexpr int64_t kSlots = 456;  // CTAs of statistics that a GB300 runs at once: three a SM
-constexpr int64_t kStatCtas = 1216, kDrawCtas = 608;  // CTAs wanted
+constexpr int kStatThreads = 512, kStatUnroll = 4, kDrawThreads = 256;
+constexpr int64_t kSlots = 304;  // CTAs of statistics that a GB300 runs at once: two a SM
+constexpr int64_t kDrawCtas = 608;  // of the draw, four a SM
 
 struct RowStats {  // 16 bytes
   float m, s;
@@ -57,7 +57,7 @@ constexpr uint32_t kStopBase = SFC_MAX_DRAFTS + 2;
 static_assert(sizeof(Decision) % 16 == 0 && sizeof(BlockHeader) % 16 == 0, "blocks are cut into 16-byte pieces");
 
 // How the work is cut, by sizes alone. At least `kMinVectors` 16-byte vectors a slice.
-constexpr int kMaxStatSlices = 16, kMaxDrawSlices = 128, kMinVectors = 512;
+constexpr int kMaxStatSlices = 32, kMaxDrawSlices = 128, kMinVectors = 512;
 struct Cut {
   int stat, draw;                                     // slices per row, per request
   bool waves;                                         // more CTAs of statistics than run at once
@@ -65,16 +65,18 @@ struct Cut {
   int32_t rec_at, decision_at, best_at, block_bytes;  // a request's block: header, [2D+1][stat], [D+1], [draw]
 };
 Cut cut_of(int64_t B, int D, int64_t V, int elt) {
-  const int64_t vectors = V * elt / 16, rows = B * (2 * D + 1);
+  const int64_t vectors = V * elt / 16, rows = B * (D + 1);
   auto slices = [&](int64_t want, int most, int64_t least) {
     return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({want, most, vectors / least})));
   };
   Cut c;
-  c.stat = slices((kStatCtas + rows - 1) / rows, kMaxStatSlices, kMinVectors);
+  c.stat = slices(kSlots / rows, kMaxStatSlices, kMinVectors);  // one wave where the rows allow
   c.draw = slices(kDrawCtas / B, kMaxDrawSlices, 128);
+  const int64_t groups = (V + 7) / 8, per = (groups + c.draw - 1) / c.draw;
+  c.draw_per = static_cast<int32_t>((per + kDrawThreads - 1) / kDrawThreads * kDrawThreads);  // a group for every thread
+  c.draw = static_cast<int>((groups + c.draw_per - 1) / c.draw_per);
   c.waves = rows * c.stat > kSlots;
   c.stat_per = static_cast<int32_t>((vectors + c.stat - 1) / c.stat);
-  c.draw_per = static_cast<int32_t>(((V + 7) / 8 + c.draw - 1) / c.draw);
   c.rec_at = sizeof(BlockHeader);
   c.decision_at = c.rec_at + (2 * D + 1) * c.stat * static_cast<int>(sizeof(RowStats));
   c.best_at = c.decision_at + (D + 1) * static_cast<int>(sizeof(Decision));
@@ -165,79 +167,127 @@ __device__ __forceinline__ void wait_for_primary() { asm volatile("griddepcontro
 __device__ __forceinline__ float stat_scale(float T) { return T == 0.f ? kLog2e : exponent_scale(T); }
 
 template <int DT>
-__global__ void __launch_bounds__(kStatThreads, 3) verify_stats_kernel(const __grid_constant__ VerifyParams p) {
-  constexpr int VEC = Elem<DT>::kVec;
-  __shared__ float2 red[kStatThreads / 32];
-  __shared__ int lowest;
-  __shared__ bool last;
-  // grid: request, slice, position and side (the earliest positions first)
-  const int S = p.cut.stat, slice = blockIdx.y;
+__global__ void __launch_bounds__(kStatThreads, 2) verify_stats_kernel(const __grid_constant__ VerifyParams p) {
+  constexpr int VEC = Elem<DT>::kVec, NW = kStatThreads / 32;
+  __shared__ float2 red[2 * NW];
+  __shared__ int lowest[2];
+  // grid: request, slice, position (the earliest first); a CTA takes its slice of both rows of a position
+  const int S = p.cut.stat, slice = blockIdx.y, j = blockIdx.z;
   const int64_t b = blockIdx.x;
-  const bool of_target = !p.draft || (blockIdx.z & 1) == 0;
-  const int j = p.draft ? blockIdx.z >> 1 : blockIdx.z, n = p.drafts(b);
+  const int tid = threadIdx.x, lane = tid & 31, n = p.drafts(b);
   BlockHeader* head = p.header(b);
   if (!p.cut.waves) launch_dependents();
-  const RowSpan<DT> row = of_target ? target_row<DT>(p, b, j) : draft_row<DT>(p, b, j < p.D ? j : 0);
-  const int nvec = static_cast<int>(row.nvec), v0 = min(slice * p.cut.stat_per, nvec), v1 = min(v0 + p.cut.stat_per, nvec);
-  RowStream<DT, kStatThreads, kStatUnroll> stream(row, v0, v1);  // on its way while the parameters load
-  if (!p.sound(b, n) || j > n || (!of_target && j == n)) return;  // not part of the request
+  const RowSpan<DT> row = target_row<DT>(p, b, j);
+  auto first = [&](const RowSpan<DT>& r) { return min(slice * p.cut.stat_per, static_cast<int>(r.nvec)); };
+  auto end = [&](const RowSpan<DT>& r) { return min((slice + 1) * p.cut.stat_per, static_cast<int>(r.nvec)); };
+  RowStream<DT, kStatThreads, kStatUnroll> stream(row, first(row), end(row));  // on its way while the parameters load
+  if (!p.sound(b, n) || j > n) return;  // not part of the request
   if (p.cut.waves) {
     // past a refusal (one vote: the mark may rise while the CTA's threads read it)
     const uint32_t stop = *reinterpret_cast<volatile uint32_t*>(&head->stop);
     if (__syncthreads_or(stop != 0 && static_cast<int>(kStopBase - stop) < j)) return;
   }
-  const float T = of_target ? p.temperature[b] : p.draft_temperature[b], c = stat_scale(T);
-  const bool scalar = slice == 0 && static_cast<int>(threadIdx.x) < row.scalars();
-  SoftmaxAcc acc;
-  stream.each([&](const uint4& v, int) {
-    float x[VEC];
-    Elem<DT>::unpack(v, x);
-    acc.add(x, Elem<DT>::vmax(v), c);
-  });
-  if (scalar) acc.add(row.at(row.scalar_index(threadIdx.x)), c);
-  const SoftmaxStats a = block_stats<kStatThreads>(acc, c, red);
-  int arg = 0;
-  if (T == 0.f) {  // the slice once more, for the lowest id of its maximum
-    if (threadIdx.x == 0) lowest = INT32_MAX;
-    __syncthreads();
-    int mine = INT32_MAX;
-    RowStream<DT, kStatThreads, kStatUnroll> again(row, v0, v1);
-    again.each([&](const uint4& v, int at) {
-      float x[VEC];
-      Elem<DT>::unpack(v, x);
-#pragma unroll
-      for (int e = 0; e < VEC; ++e)
-        if (x[e] == a.m && at < v1) mine = min(mine, row.head + at * VEC + e);
-    });
-    if (scalar) {
-      const int64_t k = row.scalar_index(threadIdx.x);
-      if (row.at(k) == a.m) mine = min(mine, static_cast<int>(k));
-    }
-    atomicMin(&lowest, mine);
-    __syncthreads();
-    arg = lowest;
-  }
-  if (threadIdx.x == 0) {
-    p.records(b, of_target, j)[slice] = RowStats{a.m, a.s, arg, 0};
-    __threadfence();
-    const uint32_t all = static_cast<uint32_t>(S) * (p.draft && j < n ? 2u : 1u);
-    last = atomicAdd(&head->tickets[j], 1u) == all - 1;
-  }
-  __syncthreads();
-  if (!last || threadIdx.x >= 32) return;
-  __threadfence();
-  Decision d{};
-  const bool drafted = j < n, certain = !p.draft;
-  const float Tt = p.temperature[b], Td = certain ? 0.f : p.draft_temperature[b];
-  // the draft's token and logits travel while the records merge
+  const bool drafted = j < n, certain = !p.draft, two = drafted && !certain;
+  const float Tt = p.temperature[b], Td = certain ? 0.f : p.draft_temperature[b], ct = stat_scale(Tt), cd = stat_scale(Td);
+  const RowSpan<DT> qrow = two ? draft_row<DT>(p, b, j) : row;
+  // the draft's token and logits, on their way long before the decision
   const int32_t t = drafted ? p.draft_tokens[b * p.D + j] : 0;
   const bool in = t >= 0 && t < p.V;
-  const float u = drafted ? p.uniforms[b * p.D + j] : 0.f;
-  const float x = target_row<DT>(p, b, j).at(in ? t : 0);
-  const float y = drafted && !certain ? draft_row<DT>(p, b, j).at(in ? t : 0) : 0.f;
-  d.target = merge_records(p.records(b, true, j), S, stat_scale(Tt));
+  float u = 0.f, x = 0.f, y = 0.f;
+  if (drafted && tid == 0) {
+    u = p.uniforms[b * p.D + j];
+    x = row.at(in ? t : 0);
+    if (two) y = qrow.at(in ? t : 0);
+  }
+  // one side's statistics into the warp's place: against a reference, or (again) against the maximum
+  auto fold = [&](RowStream<DT, kStatThreads, kStatUnroll>& from, int side, bool again) {
+    const RowSpan<DT>& r = side ? qrow : row;
+    const float c = side ? cd : ct;
+    const bool scalar = slice == 0 && tid < r.scalars();
+    SoftmaxStats w;
+    if (again) {
+      SoftmaxAcc acc;
+      from.each([&](const uint4& v, int) {
+        float x[VEC];
+        Elem<DT>::unpack(v, x);
+        acc.add(x, Elem<DT>::vmax(v), c);
+      });
+      if (scalar) acc.add(r.at(r.scalar_index(tid)), c);
+      w = warp_stats(acc, c);
+    } else {
+      ReferenceAcc acc;
+      if (from.k < from.v1) acc.start(Elem<DT>::vmax(from.v[0]));
+      const uint64_t minus_m = pack_f2(-acc.m, -acc.m), c2 = pack_f2(c, c);
+      from.each([&](const uint4& v, int) {
+        float x[VEC];
+        Elem<DT>::unpack(v, x);
+        acc.add(x, minus_m, c2);
+      });
+      if (scalar) acc.add(r.at(r.scalar_index(tid)), c);
+      w = warp_stats(acc, c);
+    }
+    if (lane == 0) red[side * NW + (tid >> 5)] = make_float2(w.m, w.s);
+    return !(w.s < INFINITY);
+  };
+  const bool greedy = Tt == 0.f || (two && Td == 0.f);
+  bool again = fold(stream, 0, greedy);
+  if (two) {
+    RowStream<DT, kStatThreads, kStatUnroll> from(qrow, first(qrow), end(qrow));
+    again |= fold(from, 1, greedy);
+  }
+  if (tid < 2) lowest[tid] = INT32_MAX;
+  if (__syncthreads_or(again) && !greedy) {  // a logit far above the reference, infinite or NaN
+    for (int side = 0; side < (two ? 2 : 1); ++side) {
+      RowStream<DT, kStatThreads, kStatUnroll> from(side ? qrow : row, first(side ? qrow : row), end(side ? qrow : row));
+      fold(from, side, true);
+    }
+    __syncthreads();
+  }
+  if (greedy) {  // the slice once more, for the lowest id of its maximum
+    for (int side = Tt == 0.f ? 0 : 1; side < (two && Td == 0.f ? 2 : 1); ++side) {
+      const RowSpan<DT>& r = side ? qrow : row;
+      const float m = merge_warps<kStatThreads>(red + side * NW, side ? cd : ct).m;
+      int mine = INT32_MAX;
+      RowStream<DT, kStatThreads, kStatUnroll> again(r, first(r), end(r));
+      again.each([&](const uint4& v, int at) {
+        float x[VEC];
+        Elem<DT>::unpack(v, x);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+          if (x[e] == m && at < end(r)) mine = min(mine, r.head + at * VEC + e);
+      });
+      if (slice == 0 && tid < r.scalars()) {
+        const int64_t k = r.scalar_index(tid);
+        if (r.at(k) == m) mine = min(mine, static_cast<int>(k));
+      }
+      atomicMin(&lowest[side], mine);
+    }
+    __syncthreads();
+  }
+  if (tid >= 32) return;  // the first warp closes the slice, and the last slice's the position
+  Decision d{};
+  const SoftmaxStats at = merge_warps<kStatThreads>(red, ct);
+  d.target = RowStats{at.m, at.s, lowest[0], 0};
   d.draft = RowStats{0.f, 1.f, INT32_MAX, 0};
-  if (drafted && !certain) d.draft = merge_records(p.records(b, false, j), S, stat_scale(Td));
+  if (two) {
+    const SoftmaxStats ad = merge_warps<kStatThreads>(red + NW, cd);
+    d.draft = RowStats{ad.m, ad.s, lowest[1], 0};
+  }
+  if (S > 1) {
+    int last = 0;
+    if (lane == 0) {
+      p.records(b, true, j)[slice] = d.target;
+      if (two) p.records(b, false, j)[slice] = d.draft;
+      __threadfence();
+      last = atomicAdd(&head->tickets[j], 1u) == static_cast<uint32_t>(S - 1);
+    }
+    if (!__shfl_sync(kFull, last, 0)) return;
+    __threadfence();
+  }
+  if (S > 1) {
+    d.target = merge_records(p.records(b, true, j), S, ct);
+    if (two) d.draft = merge_records(p.records(b, false, j), S, cd);
+  }
   if (threadIdx.x != 0) return;
   d.code = kStopped;
   if (!in || !stats_valid(d.target.m, d.target.s) || !stats_valid(d.draft.m, d.draft.s)) {
@@ -328,8 +378,9 @@ __device__ __forceinline__ RaceBest race(const VerifyParams& p, const RowSpan<DT
   }
   for (int64_t base = g0 + (threadIdx.x & ~31); base < g1; base += kDrawThreads) {  // uniform over the warp
     const int64_t g = base + lane;
-    float w[8], u[8];
-    float most[2] = {0.f, 0.f};  // of each four
+    float w[8], u[8], most = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[e] = 0.f;
     if (g < g1) {
       float x[8];
       uint64_t e2[4];
@@ -356,13 +407,14 @@ __device__ __forceinline__ RaceBest race(const VerifyParams& p, const RowSpan<DT
         for (int e = 0; e < 8; ++e) w[e] = off == e ? w[e] - 1.f : w[e];
       }
 #pragma unroll
-      for (int h = 0; h < 2; ++h) most[h] = fmaxf(fmaxf(w[4 * h], w[4 * h + 1]), fmaxf(w[4 * h + 2], w[4 * h + 3]));
+      for (int e = 0; e < 8; ++e) most = fmaxf(most, w[e]);
     }
+    // E >= -ln(1 - 2^-24): where every weight is too small, no word can make one win
+    if (!__any_sync(kFull, most > bar * 0x1p-25f)) continue;
     bool pass = false;
     float reach = 0.f;  // the largest ratio that is certain
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      if (!(most[h] > bar * 0x1p-25f)) continue;  // nothing here, or E >= -ln(1 - 2^-24) and no word can make one win
       const uint4 block = race_block(p.key, counter_row, static_cast<uint32_t>(2 * g + h));
       const uint32_t words[4] = {block.x, block.y, block.z, block.w};
 #pragma unroll
@@ -378,8 +430,7 @@ __device__ __forceinline__ RaceBest race(const VerifyParams& p, const RowSpan<DT
     if (pass) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        if (!(most[e / 4] > 0.f) || !(w[e] > 0.f)) continue;
-        if (most[e / 4] > bar * 0x1p-25f && w[e] >= bar * fmaf(lg2_approx(u[e]), -0.69314f, -4e-7f))
+        if (w[e] > 0.f && w[e] >= bar * fmaf(lg2_approx(u[e]), -0.69314f, -4e-7f))
           best.offer(w[e] / -logf(u[e]), static_cast<int32_t>(8 * g + e));
       }
     }
@@ -541,12 +592,11 @@ extern "C" int sfc_verify_drafts(const void* target_logits, const void* draft_lo
                             draft_request_stride, draft_row_stride, static_cast<int32_t>(B), D,
                             (flags & SFC_FLAG_GREEDY_T0) != 0, temperature,
                             draft_temperature ? draft_temperature : temperature, draft_tokens, num_drafts, uniforms,
-                            sfc::RaceKey{static_cast<uint32_t>(seed), static_cast<uint32_t>(seed >> 32),
-                                         static_cast<uint32_t>(step), static_cast<uint32_t>(step >> 32)},
+                            sfc::RaceKey(seed, step),
                             static_cast<uint32_t>(row_offset), static_cast<unsigned char*>(workspace), cut,
                             sfc::VerifyOutputs{accepted, tokens, token_logprobs, row_status}};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const dim3 stat(static_cast<unsigned>(B), static_cast<unsigned>(cut.stat), static_cast<unsigned>((D + 1) * (draft_logits ? 2 : 1)));
+  const dim3 stat(static_cast<unsigned>(B), static_cast<unsigned>(cut.stat), static_cast<unsigned>(D + 1));
   const dim3 draw(static_cast<unsigned>(B), static_cast<unsigned>(cut.draw));
   const cudaError_t err = dtype == SFC_BF16 ? sfc::start<0>(p, stat, draw, st) : sfc::start<1>(p, stat, draw, st);
   if (err != cudaSuccess) {

@@ -16,22 +16,32 @@
 
 namespace sfc {
 
+// The ten round keys and the step. They are made on the host and passed as kernel parameters, which the
+// instructions take as constant operands: the schedule costs the kernels nothing.
 struct RaceKey {
-  uint32_t seed_lo, seed_hi, step_lo, step_hi;
+  uint32_t round[10][2];
+  uint32_t step_lo, step_hi;
+
+  RaceKey(uint64_t seed, uint64_t step) : step_lo(static_cast<uint32_t>(step)), step_hi(static_cast<uint32_t>(step >> 32)) {
+    uint32_t k0 = static_cast<uint32_t>(seed), k1 = static_cast<uint32_t>(seed >> 32);
+    for (auto& k : round) {
+      k[0] = k0;
+      k[1] = k1;
+      k0 += 0x9E3779B9u;
+      k1 += 0xBB67AE85u;
+    }
+  }
 };
 
 __device__ __forceinline__ uint4 race_block(const RaceKey& key, uint32_t row, uint32_t quad) {
   uint32_t c0 = 0x80000000u | quad, c1 = row, c2 = key.step_lo, c3 = key.step_hi;
-  uint32_t k0 = key.seed_lo, k1 = key.seed_hi;
 #pragma unroll
   for (int r = 0; r < 10; ++r) {
     const uint64_t p0 = static_cast<uint64_t>(0xD2511F53u) * c0, p1 = static_cast<uint64_t>(0xCD9E8D57u) * c2;
-    c0 = static_cast<uint32_t>(p1 >> 32) ^ c1 ^ k0;
+    c0 = static_cast<uint32_t>(p1 >> 32) ^ c1 ^ key.round[r][0];
     c1 = static_cast<uint32_t>(p1);
-    c2 = static_cast<uint32_t>(p0 >> 32) ^ c3 ^ k1;
+    c2 = static_cast<uint32_t>(p0 >> 32) ^ c3 ^ key.round[r][1];
     c3 = static_cast<uint32_t>(p0);
-    k0 += 0x9E3779B9u;
-    k1 += 0xBB67AE85u;
   }
   return make_uint4(c0, c1, c2, c3);
 }

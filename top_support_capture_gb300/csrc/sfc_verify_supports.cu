@@ -271,8 +271,7 @@ extern "C" int sfc_verify_supports(const int32_t* target_ids, const float* targe
       sfc::SupportRows{target_ids, target_logprobs, target_lengths, target_width},
       sfc::SupportRows{draft_ids, draft_logprobs, draft_lengths, draft_width},
       D, table, draft_tokens, num_drafts, uniforms,
-      sfc::RaceKey{static_cast<uint32_t>(seed), static_cast<uint32_t>(seed >> 32), static_cast<uint32_t>(step),
-                   static_cast<uint32_t>(step >> 32)},
+      sfc::RaceKey(seed, step),
       static_cast<uint32_t>(row_offset), sfc::VerifyOutputs{accepted, tokens, token_logprobs, row_status}};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   // wide supports: more entries a request than a small CTA has threads (128 x 4, W = 8192: see the table of figures)
