@@ -112,7 +112,7 @@ def test_row_layouts():
 def test_packed_layouts():
     x, T = torch.zeros(3, 10), torch.ones(3)
     ids, y, n = torch.zeros(3, 4, dtype=torch.int32), torch.zeros(3, 4), torch.ones(3, dtype=torch.int32)
-    assert training.check_packed(x, T, ids, n, y) == 4
+    assert training.check_packed(x, T, ids, n, y) == (x.device, 3, 4)
     for kw in (dict(ids=ids.long()), dict(ids=ids[:2]), dict(ids=ids.t().contiguous().t()), dict(ids=ids[:, :0]), dict(y=y.double()),
                dict(y=y[:, :3]), dict(n=n[:2]), dict(n=n.long()), dict(T=T[:2]), dict(T=T.double()),
                dict(ids=torch.zeros(3, sfc.MAX_PACKED_WIDTH + 1, dtype=torch.int32))):

@@ -240,6 +240,14 @@ def _check_tensor(name, t, device, dtype, numel=None, shape=None):
         raise SfcError(f"{name} must hold at least {numel} elements, got {t.numel()}")
 
 
+def _expect(name, t, device, dtype, shape=None, numel=0):
+    """_check_tensor for the calls whose smallest forms take as long as their Python: nothing is built unless
+    something is wrong."""
+    if (t.dtype is not dtype or t.device != device or not t.is_contiguous() or (shape is not None and t.shape != shape)
+            or t.numel() < numel):
+        _check_tensor(name, t, device, dtype, numel=numel, shape=shape)
+
+
 def allocate_outputs(B: int, packed_width: int, device, capture: bool = True, support_logprobs: bool = True,
                      mask_V: int = 0):
     """Output tensors for one call (uninitialised: the kernels write every entry they define).

@@ -9,7 +9,7 @@ from typing import NamedTuple
 
 import torch
 
-from . import (FLAG_GREEDY_T0, MAX_DRAFTS, MAX_PACKED_WIDTH, SFC_OK, SfcError, _check_tensor, _dtype_code, _enter, _ptr,
+from . import (FLAG_GREEDY_T0, MAX_DRAFTS, MAX_PACKED_WIDTH, SFC_OK, SfcError, _check_tensor, _dtype_code, _enter, _expect, _ptr,
                allocate_workspace, load_library, strerror)
 
 
@@ -20,8 +20,10 @@ class VerifyOutput(NamedTuple):
     row_status: "object"  # int32 [B]
 
 
-# Workspaces the binding supplies when the caller passes none: one per (device, stream).
+# Workspaces the binding supplies when the caller passes none: one per (device, stream). One that a larger call
+# replaces is kept: a captured CUDA graph may still use it.
 _workspaces = {}
+_outgrown = []
 
 
 def verify_workspace_size(B: int, D: int, V: int, dtype: int) -> int:
@@ -36,7 +38,9 @@ def _workspace(nbytes, device, stream):
         if torch.cuda.is_current_stream_capturing():
             raise SfcError("a CUDA graph is being captured and no workspace of this size exists for the stream: "
                            "pass workspace= (allocate_workspace(verify_workspace_size(...))) or call once before capture")
-        ws = allocate_workspace(nbytes, device)
+        if ws is not None:
+            _outgrown.append(ws)
+        ws = allocate_workspace(1 << (nbytes - 1).bit_length(), device)  # the next power of two: few are outgrown
         _workspaces[key] = ws
     return ws
 
@@ -44,34 +48,38 @@ def _workspace(nbytes, device, stream):
 def check_positions(name, t, B, positions):
     """[B, positions, V] logits whose rows are contiguous (the rows may lie anywhere: they are only read);
     returns (V, request stride, row stride)."""
-    if t.dim() != 3 or int(t.shape[0]) != B or int(t.shape[1]) != positions or t.shape[2] < 1:
-        raise SfcError(f"{name} must be [{B}, {positions}, V], got {tuple(t.shape)}")
+    shape = t.shape
+    if len(shape) != 3 or shape[0] != B or shape[1] != positions or shape[2] < 1:
+        raise SfcError(f"{name} must be [{B}, {positions}, V], got {tuple(shape)}")
     _dtype_code(t)
-    if t.stride(2) != 1 and t.shape[2] > 1:
+    V, (request, row, one) = shape[2], t.stride()
+    if one != 1 and V > 1:
         raise SfcError(f"{name} rows must be contiguous")
-    return int(t.shape[2]), int(t.stride(0)), int(t.stride(1))
+    return V, request, row
 
 
 def check_drafts(draft_tokens, uniforms, num_drafts, device):
     """[B, D] drafted tokens and uniforms, [B] counts; returns (B, D)."""
-    if draft_tokens.dim() != 2 or draft_tokens.shape[0] < 1:
+    shape = draft_tokens.shape
+    if len(shape) != 2 or shape[0] < 1:
         raise SfcError("draft_tokens must be a non-empty [B, D] tensor")
-    B, D = int(draft_tokens.shape[0]), int(draft_tokens.shape[1])
+    B, D = shape
     if D < 1 or D > MAX_DRAFTS:
         raise SfcError(f"draft_tokens must hold 1 to {MAX_DRAFTS} drafts a request, got {D}")
-    _check_tensor("draft_tokens", draft_tokens, device, torch.int32)
-    _check_tensor("uniforms", uniforms, device, torch.float32, shape=(B, D))
-    _check_tensor("num_drafts", num_drafts, device, torch.int32, numel=B)
+    _expect("draft_tokens", draft_tokens, device, torch.int32)
+    _expect("uniforms", uniforms, device, torch.float32, shape)
+    if num_drafts is not None:
+        _expect("num_drafts", num_drafts, device, torch.int32, numel=B)
     return B, D
 
 
 def _outputs(B, D, dev):
-    return VerifyOutput(torch.empty(B, dtype=torch.int32, device=dev), torch.empty((B, D + 1), dtype=torch.int32, device=dev),
-                        torch.empty((B, D + 1), dtype=torch.float32, device=dev), torch.empty(B, dtype=torch.int32, device=dev))
+    empty, i32 = torch.empty, torch.int32
+    return VerifyOutput(empty(B, dtype=i32, device=dev), empty((B, D + 1), dtype=i32, device=dev),
+                        empty((B, D + 1), dtype=torch.float32, device=dev), empty(B, dtype=i32, device=dev))
 
 
-def _u64(x):
-    return int(x) & 0xFFFFFFFFFFFFFFFF
+_U64 = 0xFFFFFFFFFFFFFFFF
 
 
 def verify_drafts(target_logits, draft_logits, draft_tokens, uniforms, temperature, seed: int, step: int,
@@ -93,14 +101,15 @@ def verify_drafts(target_logits, draft_logits, draft_tokens, uniforms, temperatu
     stream, context = _enter(dev, stream)
     with context:
         if workspace is None:
-            workspace = _workspace(verify_workspace_size(B, D, V, dt), dev, stream)
-        _check_tensor("workspace", workspace, dev, workspace.dtype)
+            workspace = _workspace(lib.sfc_verify_workspace_size(B, D, V, dt), dev, stream)
+        else:
+            _check_tensor("workspace", workspace, dev, workspace.dtype)
         out = _outputs(B, D, dev)
-        rc = lib.sfc_verify_drafts(_ptr(target_logits), _ptr(draft_logits), dt, B, D, V, *strides, _ptr(temperature),
-                                   _ptr(draft_temperature), _ptr(draft_tokens), _ptr(num_drafts), _ptr(uniforms), _u64(seed),
-                                   _u64(step), int(row_offset), FLAG_GREEDY_T0 if greedy_t0 else 0, _ptr(out.accepted),
-                                   _ptr(out.tokens), _ptr(out.token_logprobs), _ptr(out.row_status), _ptr(workspace),
-                                   workspace.numel() * workspace.element_size(), stream)
+        rc = lib.sfc_verify_drafts(
+            target_logits.data_ptr(), _ptr(draft_logits), dt, B, D, V, *strides, temperature.data_ptr(), _ptr(draft_temperature),
+            draft_tokens.data_ptr(), _ptr(num_drafts), uniforms.data_ptr(), seed & _U64, step & _U64, row_offset,
+            FLAG_GREEDY_T0 if greedy_t0 else 0, out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(), out[3].data_ptr(),
+            workspace.data_ptr(), workspace.nbytes, stream)
     if rc != SFC_OK:
         raise SfcError(f"sfc_verify_drafts: {strerror(rc)} ({rc})")
     return out
@@ -120,8 +129,9 @@ def check_verify_layout(target_logits, draft_logits, draft_tokens, uniforms, tem
             raise SfcError(f"draft_logits must have the target's vocabulary of {V}, got {Vd}")
     if temperature is None:
         raise SfcError("temperature is required")
-    _check_tensor("temperature", temperature, dev, torch.float32, numel=B)
-    _check_tensor("draft_temperature", draft_temperature, dev, torch.float32, numel=B)
+    _expect("temperature", temperature, dev, torch.float32, numel=B)
+    if draft_temperature is not None:
+        _expect("draft_temperature", draft_temperature, dev, torch.float32, numel=B)
     return B, D, V, strides
 
 
@@ -139,10 +149,10 @@ def verify_supports(target_ids, target_logprobs, target_lengths, draft_ids, draf
     stream, context = _enter(dev, stream)
     with context:
         out = _outputs(B, D, dev)
-        rc = lib.sfc_verify_supports(_ptr(target_ids), _ptr(target_logprobs), _ptr(target_lengths), W, _ptr(draft_ids),
-                                     _ptr(draft_logprobs), _ptr(draft_lengths), Wd, B, D, _ptr(draft_tokens), _ptr(num_drafts),
-                                     _ptr(uniforms), _u64(seed), _u64(step), int(row_offset), _ptr(out.accepted),
-                                     _ptr(out.tokens), _ptr(out.token_logprobs), _ptr(out.row_status), stream)
+        rc = lib.sfc_verify_supports(
+            target_ids.data_ptr(), target_logprobs.data_ptr(), target_lengths.data_ptr(), W, _ptr(draft_ids), _ptr(draft_logprobs),
+            _ptr(draft_lengths), Wd, B, D, draft_tokens.data_ptr(), _ptr(num_drafts), uniforms.data_ptr(), seed & _U64, step & _U64,
+            row_offset, out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(), out[3].data_ptr(), stream)
     if rc != SFC_OK:
         raise SfcError(f"sfc_verify_supports: {strerror(rc)} ({rc})")
     return out
@@ -153,17 +163,22 @@ def check_supports_layout(target_ids, target_logprobs, target_lengths, draft_ids
     """The host-side checks of ``verify_supports``; returns (B, D, the target's width, the draft's or 0)."""
     dev = target_ids.device
     B, D = check_drafts(draft_tokens, uniforms, num_drafts, dev)
+    W = _check_supports(_TARGET, target_ids, target_logprobs, target_lengths, B, D + 1, dev)
+    return B, D, W, 0 if draft_ids is None else _check_supports(_DRAFT, draft_ids, draft_logprobs, draft_lengths, B, D, dev)
 
-    def rows(side, ids, lps, lengths, positions):
-        if ids.dim() != 3 or lps is None or lengths is None:
-            raise SfcError(f"{side} supports need ids and logprobs [B, positions, W] and lengths")
-        W = int(ids.shape[2])
-        if W < 1 or W > MAX_PACKED_WIDTH:
-            raise SfcError(f"{side}_ids must be 1 to {MAX_PACKED_WIDTH} wide, got {W}")
-        _check_tensor(f"{side}_ids", ids, dev, torch.int32, shape=(B, positions, W))
-        _check_tensor(f"{side}_logprobs", lps, dev, torch.float32, shape=(B, positions, W))
-        _check_tensor(f"{side}_lengths", lengths, dev, torch.int32, shape=(B, positions))
-        return W
 
-    W = rows("target", target_ids, target_logprobs, target_lengths, D + 1)
-    return B, D, W, 0 if draft_ids is None else rows("draft", draft_ids, draft_logprobs, draft_lengths, D)
+_TARGET = ("target_ids", "target_logprobs", "target_lengths")
+_DRAFT = ("draft_ids", "draft_logprobs", "draft_lengths")
+
+
+def _check_supports(names, ids, lps, lengths, B, positions, dev):
+    shape = ids.shape
+    if len(shape) != 3 or shape[0] != B or shape[1] != positions or lps is None or lengths is None:
+        raise SfcError(f"{names[0]} and {names[1]} must be [{B}, {positions}, W], {names[2]} [{B}, {positions}]")
+    W = shape[2]
+    if W < 1 or W > MAX_PACKED_WIDTH:
+        raise SfcError(f"{names[0]} must be 1 to {MAX_PACKED_WIDTH} wide, got {W}")
+    _expect(names[0], ids, dev, torch.int32)
+    _expect(names[1], lps, dev, torch.float32, shape)
+    _expect(names[2], lengths, dev, torch.int32, (B, positions))
+    return W

@@ -11,7 +11,7 @@ from typing import NamedTuple
 
 import torch
 
-from . import (FLAG_NORMALISE_TEACHER, MAX_PACKED_WIDTH, SFC_OK, ReplayOutput, SfcError, _check_tensor, _dtype_code, _enter, _ptr,
+from . import (FLAG_NORMALISE_TEACHER, MAX_PACKED_WIDTH, SFC_OK, ReplayOutput, SfcError, _dtype_code, _enter, _expect, _ptr,
                load_library, replay_logprob, strerror)
 
 
@@ -49,23 +49,23 @@ def check_row_layout(name, t):
 
 
 def check_packed(logits, temperature, ids, lengths, values=None, values_name="teacher_values", ids_name="teacher_ids"):
-    """The packed per-row arrays beside [B, V] logits, as the kernels assume them; returns W."""
-    dev, B = logits.device, int(logits.shape[0])
-    if ids.dim() != 2 or int(ids.shape[0]) != B:
+    """The packed per-row arrays beside [B, V] logits, as the kernels assume them; returns (device, B, W)."""
+    dev, B, shape = logits.device, logits.shape[0], ids.shape
+    if len(shape) != 2 or shape[0] != B:
         raise SfcError(f"{ids_name} must be [B, W]")
-    W = int(ids.shape[1])
+    W = shape[1]
     if W < 1 or W > MAX_PACKED_WIDTH:
         raise SfcError(f"{ids_name} must be 1 to {MAX_PACKED_WIDTH} wide, got {W}")
-    _check_tensor(ids_name, ids, dev, torch.int32, shape=(B, W))
-    _check_tensor("temperature", temperature, dev, torch.float32, numel=B)
-    _check_tensor("lengths", lengths, dev, torch.int32, numel=B)
-    _check_tensor(values_name, values, dev, torch.float32, shape=(B, W))
-    return W
+    _expect(ids_name, ids, dev, torch.int32)
+    _expect("temperature", temperature, dev, torch.float32, numel=B)
+    _expect("lengths", lengths, dev, torch.int32, numel=B)
+    if values is not None:
+        _expect(values_name, values, dev, torch.float32, shape)
+    return dev, B, W
 
 
 def _raise(name, rc):
-    if rc != SFC_OK:
-        raise SfcError(f"{name}: {strerror(rc)} ({rc})")
+    raise SfcError(f"{name}: {strerror(rc)} ({rc})")
 
 
 def _check_grad(grad, logits):
@@ -80,19 +80,20 @@ def _rows_args(logits, stride, temperature):
 
 
 def _teacher_args(ids, values, lengths, normalise):
-    return _ptr(ids), _ptr(values), _ptr(lengths), int(ids.shape[1]), FLAG_NORMALISE_TEACHER if normalise else 0
+    return ids.data_ptr(), values.data_ptr(), lengths.data_ptr(), ids.shape[1], FLAG_NORMALISE_TEACHER if normalise else 0
 
 
 def _distill_forward(logits, stride, temperature, ids, values, lengths, normalise, stream, keep_stats):
-    dev, B = logits.device, int(logits.shape[0])
+    dev, B = logits.device, logits.shape[0]
     stream, context = _enter(dev, stream)
     with context:
         loss = torch.empty(B, dtype=torch.float32, device=dev)
         stats = torch.empty((B, 4), dtype=torch.float32, device=dev) if keep_stats else None
         status = torch.empty(B, dtype=torch.int32, device=dev)
         rc = load_library().sfc_distill_forward(*_rows_args(logits, stride, temperature), *_teacher_args(ids, values, lengths, normalise),
-                                                _ptr(loss), _ptr(stats), _ptr(status), stream)
-    _raise("sfc_distill_forward", rc)
+                                                loss.data_ptr(), _ptr(stats), status.data_ptr(), stream)
+    if rc != SFC_OK:
+        _raise("sfc_distill_forward", rc)
     return loss, stats, status
 
 
@@ -118,9 +119,10 @@ class _Distill(torch.autograd.Function):
             grad_loss = grad_loss.to(torch.float32).contiguous()
             grad = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
             rc = load_library().sfc_distill_backward(*_rows_args(logits, ctx.stride, temperature),
-                                                     *_teacher_args(ids, values, lengths, ctx.normalise), _ptr(stats),
-                                                     _ptr(grad_loss), _ptr(grad), int(logits.shape[1]), stream)
-        _raise("sfc_distill_backward", rc)
+                                                     *_teacher_args(ids, values, lengths, ctx.normalise), stats.data_ptr(),
+                                                     grad_loss.data_ptr(), grad.data_ptr(), logits.shape[1], stream)
+        if rc != SFC_OK:
+            _raise("sfc_distill_backward", rc)
         return grad, None, None, None, None, None, None
 
 
@@ -131,9 +133,9 @@ def distill_loss(logits, temperature, teacher_ids, teacher_values, lengths, norm
     ``support_ids`` and ``support_logprobs``) or, with ``normalise``, raw top logits; ``lengths`` [B] int32 (0:
     the row has no teacher). Differentiable in ``logits``. See include/sfc.h."""
     row = check_rows("logits", logits)
-    check_packed(logits, temperature, teacher_ids, lengths, teacher_values)
     if teacher_values is None:
         raise SfcError("teacher_values is required")
+    check_packed(logits, temperature, teacher_ids, lengths, teacher_values)
     if torch.is_grad_enabled() and logits.requires_grad:
         stream, context = _enter(logits.device, stream)
         with context:
@@ -148,11 +150,10 @@ def distill_loss_and_grad(logits, temperature, teacher_ids, teacher_values, leng
     over the batch: 1 / B each): the logits are read once. ``grad`` may give the [B, V] tensor to write (not the
     logits themselves). Outside autograd."""
     row = check_rows("logits", logits)
-    check_packed(logits, temperature, teacher_ids, lengths, teacher_values)
     if teacher_values is None:
         raise SfcError("teacher_values is required")
-    dev, B = logits.device, int(logits.shape[0])
-    _check_tensor("grad_loss", grad_loss, dev, torch.float32, numel=B)
+    dev, B, _ = check_packed(logits, temperature, teacher_ids, lengths, teacher_values)
+    _expect("grad_loss", grad_loss, dev, torch.float32, numel=B)
     grad_row = logits.shape[1] if grad is None else _check_grad(grad, logits)
     stream, context = _enter(dev, stream)
     with context:
@@ -161,9 +162,10 @@ def distill_loss_and_grad(logits, temperature, teacher_ids, teacher_values, leng
         if grad is None:
             grad = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
         rc = load_library().sfc_distill_forward_backward(
-            *_rows_args(logits, row, temperature), *_teacher_args(teacher_ids, teacher_values, lengths, normalise), _ptr(grad_loss),
-            _ptr(loss), _ptr(status), _ptr(grad), grad_row, stream)
-    _raise("sfc_distill_forward_backward", rc)
+            *_rows_args(logits, row, temperature), *_teacher_args(teacher_ids, teacher_values, lengths, normalise),
+            grad_loss.data_ptr(), loss.data_ptr(), status.data_ptr(), grad.data_ptr(), grad_row, stream)
+    if rc != SFC_OK:
+        _raise("sfc_distill_forward_backward", rc)
     return DistillGradOutput(loss, grad, status)
 
 
@@ -173,19 +175,19 @@ def replay_logprob_backward(logits, temperature, support_ids, lengths, tokens, g
     ``grad_token_logprob`` [B] f32 and, where it is given, ``grad_support_logprobs`` [B, W] f32: a dense
     [B, V] tensor of the logits' dtype, zero outside the supports (written into ``grad`` when that is given)."""
     row = check_rows("logits", logits)
-    dev, B = logits.device, int(logits.shape[0])
-    W = check_packed(logits, temperature, support_ids, lengths, grad_support_logprobs, "grad_support_logprobs", "support_ids")
-    _check_tensor("tokens", tokens, dev, torch.int32, numel=B)
-    _check_tensor("grad_token_logprob", grad_token_logprob, dev, torch.float32, numel=B)
+    dev, B, W = check_packed(logits, temperature, support_ids, lengths, grad_support_logprobs, "grad_support_logprobs", "support_ids")
+    _expect("tokens", tokens, dev, torch.int32, numel=B)
+    _expect("grad_token_logprob", grad_token_logprob, dev, torch.float32, numel=B)
     grad_row = logits.shape[1] if grad is None else _check_grad(grad, logits)
     stream, context = _enter(dev, stream)
     with context:
         if grad is None:
             grad = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
-        rc = load_library().sfc_replay_backward(*_rows_args(logits, row, temperature), _ptr(support_ids), _ptr(lengths), W,
-                                                _ptr(tokens), _ptr(grad_token_logprob), _ptr(grad_support_logprobs),
-                                                _ptr(grad), grad_row, stream)
-    _raise("sfc_replay_backward", rc)
+        rc = load_library().sfc_replay_backward(
+            *_rows_args(logits, row, temperature), support_ids.data_ptr(), lengths.data_ptr(), W, tokens.data_ptr(),
+            grad_token_logprob.data_ptr(), _ptr(grad_support_logprobs), grad.data_ptr(), grad_row, stream)
+    if rc != SFC_OK:
+        _raise("sfc_replay_backward", rc)
     return grad
 
 
