@@ -4,9 +4,9 @@
 //
 // One CTA per request, every step as wide as the CTA: its warps look the drafted tokens up in both supports, all
 // positions at once, in 16-byte loads; each warp then has every decision (a lane a position); and the CTA draws over
-// the target's support at the position it stopped at. What the draft gives a member is found through a hash table in
-// shared memory (open addressing, 16-bit entry indices, at most half full). Latency bounds it: about ten dependent
-// steps whatever the sizes.
+// the target's support at the position it stopped at. The draft's entries of that position move to shared memory, and
+// what they give a member is found through a hash table there (open addressing, 16-bit entry indices, at most half
+// full). Latency bounds it: about ten dependent steps whatever the sizes.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -87,7 +87,10 @@ struct Drawn {
 template <int NT>
 __global__ void __launch_bounds__(NT) verify_supports_kernel(const __grid_constant__ VerifySupportsParams p) {
   constexpr int NW = NT / 32;
-  extern __shared__ uint16_t table[];
+  extern __shared__ __align__(16) unsigned char shared[];  // [slots] entry indices, [draft.W] ids and probabilities
+  uint16_t* table = reinterpret_cast<uint16_t*>(shared);
+  int32_t* qids = reinterpret_cast<int32_t*>(shared + p.table * sizeof(uint16_t));
+  float* qs = reinterpret_cast<float*>(qids + p.draft.W);
   __shared__ float lp_of[2][SFC_MAX_DRAFTS];  // of the drafted tokens: the target's, the draft's
   __shared__ float ratios[NW];
   __shared__ int32_t best_ids[NW], best_at[NW];
@@ -162,15 +165,19 @@ __global__ void __launch_bounds__(NT) verify_supports_kernel(const __grid_consta
   const int nt = tlen[a], nd = refused && dlen ? dlen[a] : 0;
   const int32_t* ids = p.target.ids + (b * (D + 1) + a) * p.target.W;
   const float* lp = p.target.lps + (b * (D + 1) + a) * p.target.W;
-  const int32_t* qids = nd > 0 ? p.draft.ids + (b * D + a) * p.draft.W : nullptr;
-  const float* qlp = nd > 0 ? p.draft.lps + (b * D + a) * p.draft.W : nullptr;
   int bad = 0;
   if (nd > 0) {
+    const int32_t* from = p.draft.ids + (b * D + a) * p.draft.W;
+    const float* from_lp = p.draft.lps + (b * D + a) * p.draft.W;
 #pragma unroll 2
     for (int k = tid; k < nd; k += NT) {
-      bad |= !(qlp[k] < INFINITY);
+      const int32_t id = from[k];
+      const float l = from_lp[k];
+      bad |= !(l < INFINITY);
+      qids[k] = id;
+      qs[k] = expf(l);
       // at most half full: an empty slot is found; ids that repeat take slots of their own
-      for (uint32_t h = slot_of(qids[k], mask);; h = (h + 1) & mask)
+      for (uint32_t h = slot_of(id, mask);; h = (h + 1) & mask)
         if (atomicCAS(reinterpret_cast<unsigned short*>(table + h), kEmpty, static_cast<unsigned short>(k)) == kEmpty) break;
     }
     __syncthreads();
@@ -180,29 +187,38 @@ __global__ void __launch_bounds__(NT) verify_supports_kernel(const __grid_consta
   Drawn all;
   for (int pass = 0; pass < 2 && all.best.ratio == 0.f; ++pass) {  // the second: no residual mass
     Drawn mine;
-#pragma unroll 2
-    for (int k = tid; k < nt; k += NT) {
-      const int32_t id = ids[k];
-      const float l = lp[k];
-      bad |= id < 0 || !(l < INFINITY);
-      float w = expf(l);
-      if (pass == 0 && refused) {
-        float q = 0.f;
-        if (nd > 0) {
-          for (uint32_t h = slot_of(id, mask); table[h] != kEmpty; h = (h + 1) & mask)
-            if (qids[table[h]] == id) {
-              q = expf(qlp[table[h]]);
-              break;
-            }
-        } else if (id == refused_token) {
-          q = INFINITY;
-        }
-        w = fmaxf(w - q, 0.f);
+    constexpr int E = 4;  // entries on their way at once
+    for (int k0 = tid; k0 < nt; k0 += E * NT) {
+      int32_t id[E];
+      float l[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const int k = k0 + e * NT;
+        id[e] = k < nt ? ids[k] : 0;
+        l[e] = k < nt ? lp[k] : -INFINITY;
       }
-      if (!(w > 0.f)) continue;
-      const uint4 block = race_block(p.key, counter_row, static_cast<uint32_t>(id) >> 2);
-      const uint32_t word = (id & 2) ? ((id & 1) ? block.w : block.z) : ((id & 1) ? block.y : block.x);
-      mine.offer(w / race_wait(word), id, k);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        bad |= id[e] < 0 || !(l[e] < INFINITY);
+        float w = expf(l[e]);
+        if (pass == 0 && refused && w > 0.f) {
+          float q = 0.f;
+          if (nd > 0) {
+            for (uint32_t h = slot_of(id[e], mask); table[h] != kEmpty; h = (h + 1) & mask)
+              if (qids[table[h]] == id[e]) {
+                q = qs[table[h]];
+                break;
+              }
+          } else if (id[e] == refused_token) {
+            q = INFINITY;
+          }
+          w = fmaxf(w - q, 0.f);
+        }
+        if (!(w > 0.f)) continue;
+        const uint4 block = race_block(p.key, counter_row, static_cast<uint32_t>(id[e]) >> 2);
+        const uint32_t word = (id[e] & 2) ? ((id[e] & 1) ? block.w : block.z) : ((id[e] & 1) ? block.y : block.x);
+        mine.offer(w / race_wait(word), id[e], k0 + e * NT);
+      }
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
@@ -237,10 +253,11 @@ __global__ void __launch_bounds__(NT) verify_supports_kernel(const __grid_consta
 
 template <int NT>
 cudaError_t start(const VerifySupportsParams& p, int64_t B, cudaStream_t stream) {
-  const int smem = p.draft.ids ? p.table * static_cast<int>(sizeof(uint16_t)) : 0;  // at most 64 KB
+  constexpr int kMost = 2 * SFC_MAX_PACKED_WIDTH * 2 + SFC_MAX_PACKED_WIDTH * 8;  // 192 KB
+  const int smem = p.draft.ids ? p.table * 2 + p.draft.W * 8 : 0;
   if (smem > 40 * 1024) {
     static std::atomic<uint64_t> done{0};
-    const cudaError_t err = allow_shared(verify_supports_kernel<NT>, 65536, done);
+    const cudaError_t err = allow_shared(verify_supports_kernel<NT>, kMost, done);
     if (err != cudaSuccess) return err;
   }
   verify_supports_kernel<NT><<<static_cast<unsigned>(B), NT, smem, stream>>>(p);
@@ -269,7 +286,7 @@ extern "C" int sfc_verify_supports(const int32_t* target_ids, const float* targe
   while (draft_ids && table < 2 * draft_width) table *= 2;
   const sfc::VerifySupportsParams p{
       sfc::SupportRows{target_ids, target_logprobs, target_lengths, target_width},
-      sfc::SupportRows{draft_ids, draft_logprobs, draft_lengths, draft_width},
+      sfc::SupportRows{draft_ids, draft_logprobs, draft_lengths, draft_ids ? draft_width : 0},
       D, table, draft_tokens, num_drafts, uniforms,
       sfc::RaceKey(seed, step),
       static_cast<uint32_t>(row_offset), sfc::VerifyOutputs{accepted, tokens, token_logprobs, row_status}};
