@@ -99,7 +99,7 @@ def check_grad(c, ref, grad):
 
 
 SHAPES = [(1, 1, 1), (2, 7, 3), (3, 8, 8), (4, 31, 64), (5, 1000, 1), (4, 1024, 1024), (3, 4099, 33), (3, 50021, 1024),
-          (2, 151936, 1024), (2, 129280, 8192), (2, 262144, 16384), (1, 300001, 7)]
+          (2, 151936, 1024), (2, 129280, 8192), (2, 262144, 16384), (1, 300001, 7), (1, 900001, 2000), (40, 12345, 600)]
 
 
 @pytest.mark.parametrize("dtype", [wl.DT_BF16, wl.DT_F32])
@@ -305,3 +305,42 @@ def test_replay_gradient_writes_its_rows_only(dtype, pad, out_offset):
     want, mag = oracle.replay_gradient(c["l"], dtype, c["T"], c["ids"], c["lens"], W, c["tok"], c["g"])
     check_grad(c, oracle.DistillResult(None, want, None, mag, None), grad)
     assert (buf[:out_offset] == 7).all() and (buf[out_offset:].view(B, V + pad)[:, V:] == 7).all()
+
+
+@pytest.mark.parametrize("dtype", [wl.DT_BF16])
+def test_rows_past_32_bit_offsets(dtype):
+    """Rows that start more than 2^31 elements (2^32 bytes) into their array; all others have no teacher."""
+    import top_support_capture_gb300 as sfc
+
+    if torch.cuda.mem_get_info()[0] < 16 << 30:
+        pytest.skip("needs 16 GB")
+    V, B, W, last = 262144, 8200, 8, 2
+    assert (B - last) * V > 2 ** 31
+    c = make(last, V, W, dtype, 5)
+    c["lens"][:] = W
+    for r in range(last):
+        c["ids"][r] = np.random.default_rng(r).choice(V, W, replace=False)
+        c["y"][r] = np.log(1 / W)
+    big = torch.empty((B, V), dtype=torch.bfloat16, device="cuda")
+    big[-last:] = dev_logits(c["l"], dtype)
+    T, g = torch.ones(B, device="cuda"), torch.zeros(B, device="cuda")
+    T[-last:], g[-last:] = cuda(c["T"], np.float32), cuda(c["g"], np.float32)
+    ids, y = torch.zeros((B, W), dtype=torch.int32, device="cuda"), torch.zeros((B, W), device="cuda")
+    ids[-last:], y[-last:] = cuda(c["ids"], np.int32), cuda(c["y"], np.float32)
+    n = torch.zeros(B, dtype=torch.int32, device="cuda")
+    n[-last:] = W
+    ref = reference(c)
+    grad = torch.full((B, V), 3.0, dtype=torch.bfloat16, device="cuda")
+    out = sfc.distill_loss_and_grad(big, T, ids, y, n, g, grad=grad)
+    check_loss(ref, out.loss[-last:], out.row_status[-last:])
+    check_grad(c, ref, grad[-last:])
+    assert (out.loss[:-last] == 0).all() and not grad[:-last].any()
+    x = big.requires_grad_()
+    (grad,) = torch.autograd.grad(sfc.distill_loss(x, T, ids, y, n).loss, x, g)
+    check_grad(c, ref, grad[-last:])
+    del x
+    tok = ids[:, 0].contiguous()
+    want, mag = oracle.replay_gradient(c["l"], dtype, c["T"], c["ids"], c["lens"], W, c["ids"][:, 0], c["g"])
+    got = sfc.replay_logprob_backward(big.detach(), T, ids, n, tok, g)
+    check_grad(c, oracle.DistillResult(None, want, None, mag, None), got[-last:])
+    assert not got[:-last].any()

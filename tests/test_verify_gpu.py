@@ -153,6 +153,35 @@ def test_bad_requests_and_masked_rows():
     check(ref, run(c), most_unclear=0.1)
 
 
+@pytest.mark.parametrize("dtype", [wl.DT_BF16, wl.DT_F32])
+def test_steep_rows(dtype):
+    """Logits that rise hundreds of units over what comes first in the row, and differ by as much: the masses are
+    held against a reference that has to be given up; rows that start with masked entries."""
+    c = make(12, 3, 6007, dtype, 21, spread=200.0, near=2.0)
+    t, d = (np.array(oracle.widen_logits(c[k].reshape(-1, 6007), dtype), np.float32).reshape(c[k].shape) for k in "td")
+    t[:4, :, :3000] -= 1000.0
+    d[:4, :, :3000] -= 1000.0
+    t[4:6, :, :5000] = -np.inf
+    d[6:8, :, :2500] = -3.3895313892515355e38
+    c["drafted"] = np.argmax(np.where(np.isfinite(d), d, -np.inf), axis=2).astype(np.int32)
+    c["t"], c["d"] = as_input(t.reshape(-1, 6007), dtype).reshape(t.shape), as_input(d.reshape(-1, 6007), dtype).reshape(d.shape)
+    ref = ref_of(c)
+    assert (ref.row_status == 0).all()
+    check(ref, run(c), most_unclear=0.1)
+
+
+def test_rows_past_32_bit_offsets():
+    V, D = 262144, 2
+    if torch.cuda.mem_get_info()[0] < 12 << 30:
+        pytest.skip("needs 12 GB")
+    c = make(2, D, V, wl.DT_BF16, 9)
+    t, d = dev(c["t"], c["dtype"]), dev(c["d"], c["dtype"])
+    far = torch.empty(2 ** 31 + 8 * V, dtype=torch.bfloat16, device="cuda")
+    target = far.as_strided((2, D + 1, V), (2 ** 31 + 3, V, 1), 5)
+    target.copy_(t)
+    check(ref_of(c), run(c, target, d))
+
+
 def test_no_residual_mass():
     """A refused certain draft that has all of the target's mass leaves nothing: the draw is from the target."""
     c = make(4, 1, 9, wl.DT_F32, 3, mode="lookup")

@@ -199,6 +199,7 @@ __global__ void __launch_bounds__(kStatThreads, 2) verify_stats_kernel(const __g
     x = row.at(in ? t : 0);
     if (two) y = qrow.at(in ? t : 0);
   }
+  constexpr float kFar = 1e30f;  // a warp's sum up to which those of all warps and slices stay finite
   // one side's statistics into the warp's place: against a reference, or (again) against the maximum
   auto fold = [&](RowStream<DT, kStatThreads, kStatUnroll>& from, int side, bool again) {
     const RowSpan<DT>& r = side ? qrow : row;
@@ -227,7 +228,7 @@ __global__ void __launch_bounds__(kStatThreads, 2) verify_stats_kernel(const __g
       w = warp_stats(acc, c);
     }
     if (lane == 0) red[side * NW + (tid >> 5)] = make_float2(w.m, w.s);
-    return !(w.s < INFINITY);
+    return !(w.s < kFar);
   };
   const bool greedy = Tt == 0.f || (two && Td == 0.f);
   bool again = fold(stream, 0, greedy);
