@@ -235,6 +235,27 @@ def test_reductions_and_training_step():
     check_grad(c, reference(c), held.grad_logits)
 
 
+@pytest.mark.parametrize("dtype", [wl.DT_BF16, wl.DT_F32])
+@pytest.mark.parametrize("V", [3001, 129280])
+def test_a_copy_that_never_arrives(dtype, V):
+    """The bounded wait for a kept slice gives up: every row that has work reports the timeout, with a NaN loss and
+    no gradient; rows without a teacher and bad rows are as ever; and the next call is right."""
+    import top_support_capture_gb300 as sfc
+
+    c = make(6, V, 16, dtype, 8)
+    c["lens"][:] = [16, 0, 3, 16, -1, 2]
+    for r, n in ((0, 16), (2, 3), (3, 16), (5, 2)):
+        c["ids"][r, :n], c["y"][r, :n] = np.arange(n), np.log(1 / n)
+    a, g = args(c), cuda(c["g"], np.float32)
+    out = sfc.distill_loss_and_grad(*a, g, test_stall=True)
+    assert list(out.row_status.cpu()) == [-2, 0, -2, -2, -1, -2]
+    assert list(torch.isnan(out.loss).cpu()) == [True, False, True, True, True, True] and out.loss[1] == 0
+    assert not out.grad_logits.any()
+    ref, out = reference(c), sfc.distill_loss_and_grad(*a, g)
+    check_loss(ref, out.loss, out.row_status)
+    check_grad(c, ref, out.grad_logits)
+
+
 # ------------------------------------------------------------------------------------------------ replay
 
 

@@ -46,6 +46,7 @@ struct DistillParams {
   unsigned char* grad;
   int64_t grad_stride;
   int32_t slices, per;  // CTAs a row, vectors a slice
+  bool stall;           // test of the failure path: the copies are never started
 };
 
 // What the gradient needs of a row: its softmax (m, s) and its teacher's: t_i = exp((y_i - y0) / T_y) / ty, tau.
@@ -65,6 +66,7 @@ __device__ __forceinline__ RowTerms unpack_terms(const float4& v, bool normalise
 
 constexpr int kMaxSlices = 8;  // the portable cluster size
 constexpr int kKeepBytes = 212992;  // shared memory of one SM that keeps logits: 13 vectors for each of 1024 threads
+constexpr uint32_t kStallPolls = 16;
 constexpr float kLate = -1.f;  // in place of a mass: a copy did not arrive
 
 // KEEP: the slice's vectors lie in dynamic shared memory (16 bytes for each).
@@ -89,8 +91,10 @@ __global__ void __launch_bounds__(NT, MINB) distill_kernel(const __grid_constant
     if (tid == 0) {
       mbar_init(&full, 1);
       mbar_init_fence();
-      mbar_arrive_expect_tx(&full, mine * 16);
-      if (mine > 0) bulk_load(kept, body + v0, mine * 16, &full);
+      if (!p.stall) {
+        mbar_arrive_expect_tx(&full, mine * 16);
+        if (mine > 0) bulk_load(kept, body + v0, mine * 16, &full);
+      }
     }
     __syncthreads();  // the barrier exists
   }
@@ -155,7 +159,7 @@ __global__ void __launch_bounds__(NT, MINB) distill_kernel(const __grid_constant
       };
       if (KEEP) {
         teacher_mass();
-        late = !__all_sync(kFull, mbar_wait(&full, 0));
+        late = !__all_sync(kFull, mbar_wait(&full, 0, p.stall ? kStallPolls : kWaitPolls));
         if (!late) {
 #pragma unroll 2
           for (int k = tid; k < mine; k += NT) fold(kept[k]);
@@ -210,7 +214,7 @@ __global__ void __launch_bounds__(NT, MINB) distill_kernel(const __grid_constant
       cluster_sync_all();
     }
     // nothing of the CTA's is still in flight when it ends
-    if (KEEP && !live && tid == 0) mbar_wait(&full, 0);
+    if (KEEP && !live && tid == 0 && !p.stall) mbar_wait(&full, 0);
   } else {
     q = unpack_terms(p.stats[r], p.normalise);
     live = q.m == q.m;
@@ -309,12 +313,13 @@ __global__ void __launch_bounds__(NT, MINB) distill_kernel(const __grid_constant
 }
 
 int check(const void* logits, int dtype, int64_t B, int64_t V, int64_t row_stride, const float* temperature,
-          const int32_t* ids, const float* values, const int32_t* lengths, int32_t W, uint32_t flags) {
+          const int32_t* ids, const float* values, const int32_t* lengths, int32_t W, uint32_t flags,
+          uint32_t known_flags = SFC_FLAG_NORMALISE_TEACHER) {
   if (!logits || !temperature || !ids || !values || !lengths) return SFC_EINVAL;
   if (dtype != SFC_BF16 && dtype != SFC_F32) return SFC_EINVAL;
   if (B < 1 || B > INT32_MAX || V < 1 || V > INT32_MAX || row_stride < V) return SFC_EINVAL;
   if (W < 1 || W > SFC_MAX_PACKED_WIDTH) return SFC_EINVAL;
-  if (flags & ~static_cast<uint32_t>(SFC_FLAG_NORMALISE_TEACHER)) return SFC_EINVAL;
+  if (flags & ~known_flags) return SFC_EINVAL;
   if (reinterpret_cast<uintptr_t>(logits) % (dtype == SFC_BF16 ? 2 : 4)) return SFC_EINVAL;
   return SFC_OK;
 }
@@ -395,7 +400,7 @@ extern "C" int sfc_distill_forward(const void* logits, int dtype, int64_t B, int
   if (!loss || !row_status || reinterpret_cast<uintptr_t>(row_stats) % 16) return SFC_EINVAL;
   const sfc::DistillParams p{logits, row_stride, V, packed_width, (flags & SFC_FLAG_NORMALISE_TEACHER) != 0,
                              temperature, teacher_ids, teacher_values, lengths, nullptr, loss,
-                             reinterpret_cast<float4*>(row_stats), row_status, nullptr, 0, 1, 0};
+                             reinterpret_cast<float4*>(row_stats), row_status, nullptr, 0, 1, 0, false};
   return sfc::launch<true, false>(p, dtype, B, stream);
 }
 
@@ -412,7 +417,7 @@ extern "C" int sfc_distill_backward(const void* logits, int dtype, int64_t B, in
   const sfc::DistillParams p{logits, row_stride, V, packed_width, (flags & SFC_FLAG_NORMALISE_TEACHER) != 0,
                              temperature, teacher_ids, teacher_values, lengths, grad_loss, nullptr,
                              const_cast<float4*>(reinterpret_cast<const float4*>(row_stats)), nullptr,
-                             static_cast<unsigned char*>(grad_logits), grad_stride, 1, 0};
+                             static_cast<unsigned char*>(grad_logits), grad_stride, 1, 0, false};
   return sfc::launch<false, true>(p, dtype, B, stream);
 }
 
@@ -423,12 +428,12 @@ extern "C" int sfc_distill_forward_backward(const void* logits, int dtype, int64
                                             int32_t* row_status, void* grad_logits, int64_t grad_stride,
                                             void* stream) {
   int rc = sfc::check(logits, dtype, B, V, row_stride, temperature, teacher_ids, teacher_values, lengths,
-                      packed_width, flags);
+                      packed_width, flags, SFC_FLAG_NORMALISE_TEACHER | SFC_FLAG_TEST_STALL);
   if (rc == SFC_OK) rc = sfc::check_grad(logits, dtype, B, V, row_stride, grad_loss, grad_logits, grad_stride);
   if (rc != SFC_OK) return rc;
   if (!loss || !row_status) return SFC_EINVAL;
   const sfc::DistillParams p{logits, row_stride, V, packed_width, (flags & SFC_FLAG_NORMALISE_TEACHER) != 0,
                              temperature, teacher_ids, teacher_values, lengths, grad_loss, loss, nullptr, row_status,
-                             static_cast<unsigned char*>(grad_logits), grad_stride, 1, 0};
+                             static_cast<unsigned char*>(grad_logits), grad_stride, 1, 0, (flags & SFC_FLAG_TEST_STALL) != 0};
   return sfc::launch<true, true>(p, dtype, B, stream);
 }

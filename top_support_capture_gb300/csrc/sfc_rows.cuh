@@ -17,6 +17,10 @@
 
 namespace sfc {
 
+// The two halves of a cluster barrier (release / acquire).
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
 constexpr float kLog2e = 1.4426950408889634f;
 
 // log2(e) / T, finite for every T > 0 (a subnormal T would give +inf, and 0 * inf a NaN at the maximum).

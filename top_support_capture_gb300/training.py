@@ -11,7 +11,7 @@ from typing import NamedTuple
 
 import torch
 
-from . import (FLAG_NORMALISE_TEACHER, MAX_PACKED_WIDTH, SFC_OK, ReplayOutput, SfcError, _dtype_code, _enter, _expect, _ptr,
+from . import (FLAG_NORMALISE_TEACHER, FLAG_TEST_STALL, MAX_PACKED_WIDTH, SFC_OK, ReplayOutput, SfcError, _dtype_code, _enter, _expect, _ptr,
                load_library, replay_logprob, strerror)
 
 
@@ -79,8 +79,9 @@ def _rows_args(logits, stride, temperature):
     return logits.data_ptr(), _dtype_code(logits), B, V, stride, temperature.data_ptr()
 
 
-def _teacher_args(ids, values, lengths, normalise):
-    return ids.data_ptr(), values.data_ptr(), lengths.data_ptr(), ids.shape[1], FLAG_NORMALISE_TEACHER if normalise else 0
+def _teacher_args(ids, values, lengths, normalise, flags=0):
+    return (ids.data_ptr(), values.data_ptr(), lengths.data_ptr(), ids.shape[1],
+            flags | FLAG_NORMALISE_TEACHER if normalise else flags)
 
 
 def _distill_forward(logits, stride, temperature, ids, values, lengths, normalise, stream, keep_stats):
@@ -145,7 +146,7 @@ def distill_loss(logits, temperature, teacher_ids, teacher_values, lengths, norm
 
 
 def distill_loss_and_grad(logits, temperature, teacher_ids, teacher_values, lengths, grad_loss, normalise: bool = False,
-                          grad=None, stream=None) -> DistillGradOutput:
+                          grad=None, stream=None, test_stall: bool = False) -> DistillGradOutput:
     """``distill_loss`` and its gradient in one call, for a known upstream gradient ``grad_loss`` [B] f32 (a mean
     over the batch: 1 / B each): the logits are read once. ``grad`` may give the [B, V] tensor to write (not the
     logits themselves). Outside autograd."""
@@ -162,7 +163,7 @@ def distill_loss_and_grad(logits, temperature, teacher_ids, teacher_values, leng
         if grad is None:
             grad = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
         rc = load_library().sfc_distill_forward_backward(
-            *_rows_args(logits, row, temperature), *_teacher_args(teacher_ids, teacher_values, lengths, normalise),
+            *_rows_args(logits, row, temperature), *_teacher_args(teacher_ids, teacher_values, lengths, normalise, FLAG_TEST_STALL if test_stall else 0),
             grad_loss.data_ptr(), loss.data_ptr(), status.data_ptr(), grad.data_ptr(), grad_row, stream)
     if rc != SFC_OK:
         _raise("sfc_distill_forward_backward", rc)
