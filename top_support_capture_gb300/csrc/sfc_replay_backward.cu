@@ -9,6 +9,9 @@
 // exchanges the softmax statistics and sum_S u (distributed shared memory), and after its barrier, which also orders
 // the zeros, each CTA writes its share of the entries wherever in the row they lie. The first kHeld entries of a
 // thread stay in registers in between.
+//
+// 512 x 151936 bf16, W = 1024: 37 us for 155 MB of rows and 30 MB of gathered logits (DRAM answers in 64 bytes), 0.74
+// of the measured copy rate; 256 x 129280 f32, W = 8192: 46 us for 132 + 86 MB. One CTA per row: 42 and 95 us.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -132,7 +135,8 @@ __global__ void __launch_bounds__(kThreads) replay_backward_kernel(const __grid_
 template <int DT>
 cudaError_t start(ReplayBackwardParams p, int64_t B, cudaStream_t stream) {
   const int64_t vectors = p.V / Elem<DT>::kVec;
-  // slices of about kSliceVectors, more where the rows are few (1216 CTAs of this kernel run at once)
+  // slices of about kSliceVectors (128 KB: 64 KB measured 41 us and 256 KB 37 us at 512 x 151936 bf16, 44 and 57 us at
+  // 256 x 129280 f32), more where the rows are few
   const int64_t want = std::max((vectors + kSliceVectors - 1) / kSliceVectors, std::min((kFillCtas + B - 1) / B, vectors / 512));
   p.slices = static_cast<int32_t>(std::clamp<int64_t>(want, 1, kMaxSlices));
   p.per = static_cast<int32_t>((vectors + p.slices - 1) / p.slices + 7) & ~7;  // whole 128-byte lines

@@ -6,7 +6,8 @@
 // positions at once, in 16-byte loads; each warp then has every decision (a lane a position); and the CTA draws over
 // the target's support at the position it stopped at. The draft's entries of that position move to shared memory, and
 // what they give a member is found through a hash table there (open addressing, 16-bit entry indices, at most half
-// full). Latency bounds it: about ten dependent steps whatever the sizes.
+// full). Latency bounds it, about ten dependent steps: 9.3 us for one request of 4 drafts at W = 1024, 30 us for 128 at
+// W = 8192, where the request with the longest supports sets the end (its CTA works twice as long as the mean).
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -291,7 +292,8 @@ extern "C" int sfc_verify_supports(const int32_t* target_ids, const float* targe
       sfc::RaceKey(seed, step),
       static_cast<uint32_t>(row_offset), sfc::VerifyOutputs{accepted, tokens, token_logprobs, row_status}};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  // wide supports: more entries a request than a small CTA has threads (128 x 4, W = 8192: see the table of figures)
+  // wide supports have more entries than a small CTA has threads: 128 x 4 at W = 8192 29.6 us with 1024 threads, 37.5
+  // with 512, 60 with 256; 1 x 4 at W = 1024 9.3 us with 256, 9.5 with 512, 12.0 with 128
   const bool wide = std::max(target_width, draft_ids ? draft_width : 0) > 2048;
   if ((wide ? sfc::start<1024>(p, B, st) : sfc::start<256>(p, B, st)) != cudaSuccess) {
     (void)cudaGetLastError();
