@@ -226,41 +226,42 @@ __global__ void __launch_bounds__(NT, MINB) distill_kernel(const __grid_constant
   const float k = live ? g * q.tau / q.s : 0.f, m = q.m;
   unsigned char* grad = BWD ? p.grad + r * p.grad_stride * Elem<DT>::kBytes : nullptr;
   if (BWD) {
-    const bool same = ((reinterpret_cast<uintptr_t>(grad) ^ reinterpret_cast<uintptr_t>(row.row)) & 15) == 0;
-    uint4* out = reinterpret_cast<uint4*>(grad + static_cast<int64_t>(row.head) * Elem<DT>::kBytes);
+    unsigned char* out = grad + static_cast<int64_t>(row.head) * Elem<DT>::kBytes;
+    const int shift = static_cast<int>(reinterpret_cast<uintptr_t>(out) & 15);
     const uint64_t minus_m2 = pack_f2(-m, -m), c2 = pack_f2(c, c), k2 = pack_f2(k, k);
-    auto put = [&](int at, const uint4& w) {
+    auto gradient = [&](const uint4& w) {
       float x[VEC];
       Elem<DT>::unpack(w, x);
       uint64_t e2[VEC / 2];
       exponentials(x, minus_m2, c2, e2);
 #pragma unroll
       for (int e = 0; e < VEC / 2; ++e) unpack_f2(fmul_f2(e2[e], k2), x[2 * e], x[2 * e + 1]);
-      if (same) {
-        out[at] = Out<DT>::pack(x);
-      } else {
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) Out<DT>::store1(grad, row.head + static_cast<int64_t>(at) * VEC + e, x[e]);
+      return Out<DT>::pack(x);
+    };
+    const bool by_warp = DT == 0 && shift != 0;
+    auto put = [&](int at, const uint4& w) {
+      unsigned char* to = out + static_cast<int64_t>(at) * 16;
+      if (by_warp) {
+        store_shifted(to, w, shift, at < v1);
+      } else if (at < v1) {
+        if (shift == 0) {
+          *reinterpret_cast<uint4*>(to) = w;
+        } else {
+          uint32_t* four = reinterpret_cast<uint32_t*>(to);
+          four[0] = w.x, four[1] = w.y, four[2] = w.z, four[3] = w.w;
+        }
       }
     };
     if (!live) {
-      const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-      for (int i = v0 + tid; i < v1; i += NT) {
-        if (same) {
-          out[i] = zero;
-        } else {
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) Out<DT>::store1(grad, row.head + static_cast<int64_t>(i) * VEC + e, 0.f);
-        }
-      }
+      for (int i = v0 + tid; i - lane < v1; i += NT) put(i, make_uint4(0u, 0u, 0u, 0u));
+    } else if (KEEP && by_warp) {
+      for (int i = tid; i - lane < mine; i += NT) put(v0 + i, gradient(kept[min(i, mine - 1)]));
     } else if (KEEP) {
 #pragma unroll 2
-      for (int i = tid; i < mine; i += NT) put(v0 + i, kept[i]);
+      for (int i = tid; i < mine; i += NT) put(v0 + i, gradient(kept[i]));
     } else {
       RowStream<DT, NT, U> stream(row, v0, v1);
-      stream.each([&](const uint4& w, int at) {
-        if (at < v1) put(at, w);
-      });
+      stream.each([&](const uint4& w, int at) { put(at, gradient(w)); });
     }
     if (scalar) {
       const int64_t i = row.scalar_index(tid);
