@@ -13,7 +13,7 @@
 // read from HBM once: one thread starts a bulk copy of it before anything else. The wait for the copy is bounded
 // (SFC_ROW_TIMEOUT). Rows longer than a cluster's shared memory are read again.
 //
-// 2048 x 151936 bf16, loss and gradient: 263 us, 0.70 of the measured copy rate (2 x 622 MB). The two CTAs of a SM
+// 2048 x 151936 bf16, loss and gradient: 258 us, 0.72 of the measured copy rate (2 x 622 MB). The two CTAs of a SM
 // read, compute and write in turns; the copies alone take 126 us, the folds 24, the teacher's entries and merges 44, the
 // gradient's rows 70, added up. Measured against it: one CTA per row that streams it twice 313-360 us (the second pass
 // finds 8 % in L2); the slice in registers, five CTAs a row 422; the copy in two or four parts that are waited for one by
@@ -376,7 +376,8 @@ cudaError_t choose(DistillParams& p, int64_t B, cudaStream_t stream) {
     if (fits(std::max(fill, cut(kKeepBytes / 2 / 16 - 8)))) return start<DT, 512, 2, true, true, true>(p, B, stream);
     if (fits(cut(kKeepBytes / 16 - 8))) return start<DT, 1024, 1, true, true, true>(p, B, stream);
   }
-  fits(FWD ? fill : std::max(fill, cut(8192)));
+  // the gradient alone needs no cluster: slices of 320 KB (2048 x 151936 bf16 222 us, of 128 KB 248)
+  fits(FWD ? fill : std::max(fill, cut(20480)));
   return start<DT, 512, 2, false, FWD, BWD>(p, B, stream);
 }
 

@@ -174,26 +174,6 @@ __device__ __forceinline__ SoftmaxStats merge_warps(const float2* red, float c) 
   return SoftmaxStats{m, warp_total(lane < NT / 32 ? v.y * ex2_approx((v.x - m) * c) : 0.f)};
 }
 
-// The accumulators of the CTA's NT threads as one, in a fixed order, the same bits in every thread. `red` holds
-// NT / 32 entries; a barrier must separate two uses of it.
-template <int NT, class Acc>
-__device__ __forceinline__ SoftmaxStats block_stats(const Acc& a, float c, float2* red) {
-  const SoftmaxStats w = warp_stats(a, c);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = make_float2(w.m, w.s);
-  __syncthreads();
-  return merge_warps<NT>(red, c);
-}
-
-// A sum over the CTA in a fixed order, the same bits in every thread. `red` holds NT / 32 floats.
-template <int NT>
-__device__ __forceinline__ float block_total(float v, float* red) {
-  const float w = warp_total(v);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = w;
-  __syncthreads();
-  const int lane = threadIdx.x & 31;
-  return warp_total(lane < NT / 32 ? red[lane] : 0.f);
-}
-
 // This thread's vectors of [v0, v1) of a row, every NT-th, U of them at a time. The first batch can be on its way
 // before anything else of the row is known, and each later one is while the one before it is used.
 template <int DT, int NT, int U>
