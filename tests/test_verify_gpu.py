@@ -232,6 +232,13 @@ def test_repeats_streams_graphs_and_workspaces():
     t, d = dev(c["t"], c["dtype"]), dev(c["d"], c["dtype"])
     rest = (cuda(c["drafted"], np.int32), cuda(c["u"], np.float32), cuda(c["T"], np.float32))
     kw = dict(draft_temperature=cuda(c["Td"], np.float32), num_drafts=cuda(c["n"], np.int32))
+    own = t.clone()  # goes out of scope while the other stream may still read it
+    side.wait_stream(torch.cuda.current_stream())
+    there = sfc.verify_drafts(own, d, *rest, c["seed"], c["step"], stream=side, **kw)
+    del own
+    junk = [torch.full_like(t, 9.0) for _ in range(4)]
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(first, there)) and len(junk) == 4
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         held = sfc.verify_drafts(t, d, *rest, c["seed"], c["step"], workspace=ws, **kw)

@@ -206,16 +206,20 @@ class _Nothing:
 _NOTHING = _Nothing()
 
 
-def _enter(device, stream):
+def _enter(device, stream, *inputs):
     """(handle, context): the stream to launch on (the current one when None) and what to allocate and launch
-    under, so that outputs belong to the stream that writes them. Nothing is switched where nothing differs:
-    the smallest calls take as long as their Python."""
+    under, so that outputs belong to the stream that writes them and the inputs outlive their use there. Nothing is
+    switched where nothing differs: the smallest calls take as long as their Python. The caller orders the streams
+    (inputs written before, outputs used after)."""
     import torch
 
     if stream is None and device.index == torch.cuda.current_device():
         return torch._C._cuda_getCurrentRawStream(device.index), _NOTHING
     import contextlib
 
+    for t in inputs:  # their memory is not given to anyone else before `stream` is through with it
+        if t is not None and stream is not None and not torch.cuda.is_current_stream_capturing():
+            t.record_stream(stream)
     context = contextlib.ExitStack()
     context.enter_context(torch.cuda.device(device))
     stream = torch.cuda.current_stream(device) if stream is None else stream

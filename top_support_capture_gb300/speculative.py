@@ -98,7 +98,8 @@ def verify_drafts(target_logits, draft_logits, draft_tokens, uniforms, temperatu
                                            num_drafts)
     dt = _dtype_code(target_logits)
     lib = load_library()
-    stream, context = _enter(dev, stream)
+    stream, context = _enter(dev, stream, target_logits, draft_logits, draft_tokens, uniforms, temperature, draft_temperature,
+                             num_drafts, workspace)
     with context:
         if workspace is None:
             workspace = _workspace(lib.sfc_verify_workspace_size(B, D, V, dt), dev, stream)
@@ -146,7 +147,8 @@ def verify_supports(target_ids, target_logprobs, target_lengths, draft_ids, draf
     B, D, W, Wd = check_supports_layout(target_ids, target_logprobs, target_lengths, draft_ids, draft_logprobs, draft_lengths,
                                         draft_tokens, uniforms, num_drafts)
     lib = load_library()
-    stream, context = _enter(dev, stream)
+    stream, context = _enter(dev, stream, target_ids, target_logprobs, target_lengths, draft_ids, draft_logprobs, draft_lengths,
+                             draft_tokens, uniforms, num_drafts)
     with context:
         out = _outputs(B, D, dev)
         rc = lib.sfc_verify_supports(

@@ -86,7 +86,7 @@ def _teacher_args(ids, values, lengths, normalise, flags=0):
 
 def _distill_forward(logits, stride, temperature, ids, values, lengths, normalise, stream, keep_stats):
     dev, B = logits.device, logits.shape[0]
-    stream, context = _enter(dev, stream)
+    stream, context = _enter(dev, stream, logits, temperature, ids, values, lengths)
     with context:
         loss = torch.empty(B, dtype=torch.float32, device=dev)
         stats = torch.empty((B, 4), dtype=torch.float32, device=dev) if keep_stats else None
@@ -138,7 +138,7 @@ def distill_loss(logits, temperature, teacher_ids, teacher_values, lengths, norm
         raise SfcError("teacher_values is required")
     check_packed(logits, temperature, teacher_ids, lengths, teacher_values)
     if torch.is_grad_enabled() and logits.requires_grad:
-        stream, context = _enter(logits.device, stream)
+        _, context = _enter(logits.device, stream, logits, temperature, teacher_ids, teacher_values, lengths)
         with context:
             return DistillOutput(*_Distill.apply(logits, row, temperature, teacher_ids, teacher_values, lengths, bool(normalise)))
     loss, _, status = _distill_forward(logits, row, temperature, teacher_ids, teacher_values, lengths, normalise, stream, False)
@@ -156,7 +156,7 @@ def distill_loss_and_grad(logits, temperature, teacher_ids, teacher_values, leng
     dev, B, _ = check_packed(logits, temperature, teacher_ids, lengths, teacher_values)
     _expect("grad_loss", grad_loss, dev, torch.float32, numel=B)
     grad_row = logits.shape[1] if grad is None else _check_grad(grad, logits)
-    stream, context = _enter(dev, stream)
+    stream, context = _enter(dev, stream, logits, temperature, teacher_ids, teacher_values, lengths, grad_loss, grad)
     with context:
         loss = torch.empty(B, dtype=torch.float32, device=dev)
         status = torch.empty(B, dtype=torch.int32, device=dev)
@@ -180,7 +180,8 @@ def replay_logprob_backward(logits, temperature, support_ids, lengths, tokens, g
     _expect("tokens", tokens, dev, torch.int32, numel=B)
     _expect("grad_token_logprob", grad_token_logprob, dev, torch.float32, numel=B)
     grad_row = logits.shape[1] if grad is None else _check_grad(grad, logits)
-    stream, context = _enter(dev, stream)
+    stream, context = _enter(dev, stream, logits, temperature, support_ids, lengths, tokens, grad_token_logprob,
+                             grad_support_logprobs, grad)
     with context:
         if grad is None:
             grad = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
@@ -216,6 +217,6 @@ class _Replay(torch.autograd.Function):
 
 def differentiable_replay(logits, temperature, support_ids, lengths, tokens, support_logprobs, stream) -> ReplayOutput:
     check_rows("logits", logits)
-    _, context = _enter(logits.device, stream)
+    _, context = _enter(logits.device, stream, logits, temperature, support_ids, lengths, tokens)
     with context:
         return ReplayOutput(*_Replay.apply(logits, temperature, support_ids, lengths, tokens, support_logprobs))
