@@ -13,9 +13,10 @@
 // read from HBM once: one thread starts a bulk copy of it before anything else. The wait for the copy is bounded
 // (SFC_ROW_TIMEOUT). Rows longer than a cluster's shared memory are read again.
 //
-// 2048 x 151936 bf16, loss and gradient: 258 us, 0.72 of the measured copy rate (2 x 622 MB). The two CTAs of a SM
-// read, compute and write in turns; the copies alone take 126 us, the folds 24, the teacher's entries and merges 44, the
-// gradient's rows 70, added up. Measured against it: one CTA per row that streams it twice 313-360 us (the second pass
+// 2048 x 151936 bf16, loss and gradient: 243 us, 0.76 of the measured copy rate (2 x 622 MB). The two CTAs of a SM
+// read, compute and write in turns; before the prefetch, which lets HBM work while they compute (258 -> 243 us), the copies
+// alone took 126 us, the folds 24, the teacher's entries and merges 44, the gradient's rows 70, added up. Measured
+// against that: one CTA per row that streams it twice 313-360 us (the second pass
 // finds 8 % in L2); the slice in registers, five CTAs a row 422; the copy in two or four parts that are waited for one by
 // one 262 / 274; three or four CTAs a SM 282 / 268 (each thread's fixed work grows); clusters that go from row to row
 // and start the next copy as the slice is used up 248, at 9.0 instead of 7.4 us for 64 x 32000 and twice the code.
@@ -69,8 +70,13 @@ __device__ __forceinline__ RowTerms unpack_terms(const float4& v, bool normalise
 
 constexpr int kMaxSlices = 8;  // the portable cluster size
 constexpr int kKeepBytes = 212992;  // shared memory of one SM that keeps logits: 13 vectors for each of 1024 threads
+constexpr int kAhead = 152;  // CTAs that a prefetch runs ahead: half of what runs at once (152 to 304: 243 to 247 us)
 constexpr uint32_t kStallPolls = 16;
 constexpr float kLate = -1.f;  // in place of a mass: a copy did not arrive
+
+__device__ __forceinline__ void prefetch_l2(const void* from, uint32_t bytes) {  // 16-byte aligned, a multiple of 16
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(from), "r"(bytes) : "memory");
+}
 
 // KEEP: the slice's vectors lie in dynamic shared memory (16 bytes for each).
 template <int DT, int NT, int MINB, bool KEEP, bool FWD, bool BWD>
@@ -163,6 +169,11 @@ __global__ void __launch_bounds__(NT, MINB) distill_kernel(const __grid_constant
       if (KEEP) {
         teacher_mass();
         late = !__all_sync(kFull, mbar_wait(&full, 0, p.stall ? kStallPolls : kWaitPolls));
+        if (tid == 0 && r + kAhead / S < gridDim.x) {  // a later CTA's slice on its way to L2 while HBM would idle
+          const RowSpan<DT> later(p.logits, (r + kAhead / S) * p.row_stride, p.V);
+          const int vecs = static_cast<int>(later.nvec), at = min(rank * p.per, vecs), bytes = (min(at + p.per, vecs) - at) * 16;
+          if (bytes > 0) prefetch_l2(later.body() + at, bytes);
+        }
         if (!late) {
 #pragma unroll 2
           for (int k = tid; k < mine; k += NT) fold(kept[k]);
