@@ -99,7 +99,7 @@ def check_grad(c, ref, grad):
 
 
 SHAPES = [(1, 1, 1), (2, 7, 3), (3, 8, 8), (4, 31, 64), (5, 1000, 1), (4, 1024, 1024), (3, 4099, 33), (3, 50021, 1024),
-          (2, 151936, 1024), (2, 129280, 8192), (2, 262144, 16384), (1, 300001, 7), (1, 900001, 2000), (40, 12345, 600)]
+          (2, 151936, 1024), (2, 129280, 8192), (2, 262144, 16384), (1, 300001, 7), (1, 900001, 2000), (40, 12345, 600), (700, 257, 40)]
 
 
 @pytest.mark.parametrize("dtype", [wl.DT_BF16, wl.DT_F32])
