@@ -398,9 +398,11 @@ cudaError_t choose(DistillParams& p, int64_t B, cudaStream_t stream) {
   }
   // the gradient alone needs no cluster: slices of 320 KB (2048 x 151936 bf16 222 us, of 128 KB 248)
   fits(FWD ? fill : std::max(fill, cut(20480)));
-  // the loss alone in CTAs of 256 (64 x 151936 bf16 9.5 us, of 512 13.4), the gradient of 512 (2048 x 151936 222, 238)
-  if constexpr (FWD && !BWD) return start<DT, 256, 4, false, true, false>(p, B, stream);
-  else return start<DT, 512, 2, false, FWD, BWD>(p, B, stream);
+  // the loss alone in CTAs of 256 (64 x 151936 bf16 9.5 us, of 512 13.4) unless each has a SM to itself (8 x 262144 7.4,
+  // 6.5), the gradient alone in CTAs of 512 (2048 x 151936 222 us, of 256 238)
+  if constexpr (FWD && !BWD)
+    if (B * p.slices > 152) return start<DT, 256, 4, false, true, false>(p, B, stream);
+  return start<DT, 512, 2, false, FWD, BWD>(p, B, stream);
 }
 
 template <bool FWD, bool BWD>
