@@ -13,12 +13,12 @@
 // read from HBM once: one thread starts a bulk copy of it before anything else. The wait for the copy is bounded
 // (SFC_ROW_TIMEOUT). Rows longer than a cluster's shared memory are read again.
 //
-// 2048 x 151936 bf16, loss and gradient: 243 us, 0.76 of the measured copy rate (2 x 622 MB). The two CTAs of a SM
-// read, compute and write in turns; before the prefetch, which lets HBM work while they compute (258 -> 243 us), the copies
+// 2048 x 151936 bf16, loss and gradient: 245 us, 0.75 of the measured copy rate (2 x 622 MB). The two CTAs of a SM
+// read, compute and write in turns; before the prefetch, which lets HBM work while they compute (258 -> 245 us), the copies
 // alone took 126 us, the folds 24, the teacher's entries and merges 44, the gradient's rows 70, added up. Measured
 // against that: one CTA per row that streams it twice 313-360 us (the second pass
 // finds 8 % in L2); the slice in registers, five CTAs a row 422; the copy in two or four parts that are waited for one by
-// one 262 / 274; three or four CTAs a SM 282 / 268 (each thread's fixed work grows); clusters that go from row to row
+// one 262 / 274; three or four CTAs a SM in clusters of five or six 282 / 268 (each thread's fixed work grows); clusters that go from row to row
 // and start the next copy as the slice is used up 248, at 9.0 instead of 7.4 us for 64 x 32000 and twice the code.
 //
 // The gradient's dense part tau p_j g / T is written first; after the CTA's barrier the teacher's entries that lie
@@ -70,7 +70,6 @@ __device__ __forceinline__ RowTerms unpack_terms(const float4& v, bool normalise
 
 constexpr int kMaxSlices = 8;  // the portable cluster size
 constexpr int kKeepBytes = 212992;  // shared memory of one SM that keeps logits: 13 vectors for each of 1024 threads
-constexpr int kAhead = 152;  // CTAs that a prefetch runs ahead: half of what runs at once (152 to 304: 243 to 247 us)
 constexpr uint32_t kStallPolls = 16;
 constexpr float kLate = -1.f;  // in place of a mass: a copy did not arrive
 
@@ -83,6 +82,7 @@ template <int DT, int NT, int MINB, bool KEEP, bool FWD, bool BWD>
 __global__ void __launch_bounds__(NT, MINB) distill_kernel(const __grid_constant__ DistillParams p) {
   constexpr int NW = NT / 32, VEC = Elem<DT>::kVec;
   constexpr int U = 4;  // vectors in flight per thread where they are not kept (and as many again)
+  constexpr int kAhead = 76 * MINB;  // CTAs that a prefetch runs ahead: half of what runs at once (a quarter to all: within 2 %)
   constexpr int kBatch = KEEP ? 2 : 4;  // teacher entries that a thread has on their way at once
   extern __shared__ __align__(128) uint4 kept[];
   __shared__ uint64_t full;
@@ -385,8 +385,7 @@ cudaError_t choose(DistillParams& p, int64_t B, cudaStream_t stream) {
   const int64_t fill = std::min<int64_t>({kMaxSlices, cut(1024), (304 + B - 1) / B});
   // Rows that one CTA holds, enough of them to fill the GPU: the smaller the CTA the better, since each thread's fixed
   // work and the CTA's barriers weigh less and more CTAs take turns on a SM (2048 rows, loss and gradient: 5000 bf16 12.6
-  // us against 30.9 with two CTAs of 512, 12000 20.6 : 36.2, 26000 39 : 48,
-  // 32000 51 : 57).
+  // us against 30.9 with two CTAs of 512 a SM, 12000 20.6 : 36.2, 26000 39 : 48, 32000 51 : 57).
   if (B >= 304) {
     if (vectors <= kKeepBytes / 8 / 16 - 8 && fits(1)) return start<DT, 128, 8, FWD && BWD, FWD, BWD>(p, B, stream);
     if (vectors <= kKeepBytes / 4 / 16 - 8 && fits(1)) return start<DT, 256, 4, FWD && BWD, FWD, BWD>(p, B, stream);
