@@ -203,58 +203,31 @@ __global__ void __launch_bounds__(kStatThreads, 2) verify_stats_kernel(const __g
     x = row.at(in ? t : 0);
     if (two) y = qrow.at(in ? t : 0);
   }
-  constexpr float kFar = 1e30f;  // a warp's sum up to which those of all warps and slices stay finite
-  // one side's statistics into the warp's place: against a reference, or (again) against the maximum
-  auto fold = [&](RowStream<DT, kStatThreads, kStatUnroll>& from, int side, bool again) {
+  // one side's statistics into the warp's place
+  auto fold = [&](RowStream<DT, kStatThreads, kStatUnroll>& from, int side) {
     const RowSpan<DT>& r = side ? qrow : row;
     const float c = side ? cd : ct;
-    const bool scalar = slice == 0 && tid < r.scalars();
-    SoftmaxStats w;
-    if (again) {
-      SoftmaxAcc acc;
-      from.each([&](const uint4& v, int) {
-        float x[VEC];
-        Elem<DT>::unpack(v, x);
-        acc.add(x, Elem<DT>::vmax(v), c);
-      });
-      if (scalar) acc.add(r.at(r.scalar_index(tid)), c);
-      w = warp_stats(acc, c);
-    } else {
-      ReferenceAcc acc;
-      if (from.k < from.v1) acc.start(Elem<DT>::vmax(from.v[0]));
-      const uint64_t minus_m = pack_f2(-acc.m, -acc.m), c2 = pack_f2(c, c);
-      from.each([&](const uint4& v, int) {
-        float x[VEC];
-        Elem<DT>::unpack(v, x);
-        acc.add(x, minus_m, c2);
-      });
-      if (scalar) acc.add(r.at(r.scalar_index(tid)), c);
-      w = warp_stats(acc, c);
-    }
+    SoftmaxAcc acc;
+    from.batches([&](const uint4 (&v)[kStatUnroll]) { acc.template add<DT>(v, c); });
+    if (slice == 0 && tid < r.scalars()) acc.add(r.at(r.scalar_index(tid)), c);
+    const SoftmaxStats w = warp_stats(acc, c);
     if (lane == 0) red[side * NW + (tid >> 5)] = make_float2(w.m, w.s);
-    return !(w.s < kFar);
   };
-  const bool greedy = Tt == 0.f || (two && Td == 0.f);
-  bool again = fold(stream, 0, greedy);
+  fold(stream, 0);
   if (two) {
     RowStream<DT, kStatThreads, kStatUnroll> from(qrow, first(qrow), end(qrow));
-    again |= fold(from, 1, greedy);
+    fold(from, 1);
   }
   if (tid < 2) lowest[tid] = INT32_MAX;
-  if (__syncthreads_or(again) && !greedy) {  // a logit far above the reference, infinite or NaN
-    for (int side = 0; side < (two ? 2 : 1); ++side) {
-      RowStream<DT, kStatThreads, kStatUnroll> from(side ? qrow : row, first(side ? qrow : row), end(side ? qrow : row));
-      fold(from, side, true);
-    }
-    __syncthreads();
-  }
+  __syncthreads();
+  const bool greedy = Tt == 0.f || (two && Td == 0.f);
   if (greedy) {  // the slice once more, for the lowest id of its maximum
     for (int side = Tt == 0.f ? 0 : 1; side < (two && Td == 0.f ? 2 : 1); ++side) {
       const RowSpan<DT>& r = side ? qrow : row;
       const float m = merge_warps<kStatThreads>(red + side * NW, side ? cd : ct).m;
       int mine = INT32_MAX;
-      RowStream<DT, kStatThreads, kStatUnroll> again(r, first(r), end(r));
-      again.each([&](const uint4& v, int at) {
+      RowStream<DT, kStatThreads, kStatUnroll> from(r, first(r), end(r));
+      from.each([&](const uint4& v, int at) {
         float x[VEC];
         Elem<DT>::unpack(v, x);
 #pragma unroll
@@ -517,6 +490,7 @@ __global__ void __launch_bounds__(kDrawThreads, 4) verify_draw_kernel(const __gr
       __syncthreads();
       best = block_best<kDrawThreads>(mine, ratios, best_ids);
     }
+    if (best.ratio == 0.f) code = kBad;  // no winner (a sound row has one): there is no id to read the row at
   }
   const int32_t token = T == 0.f ? st.argmax : best.id;
   float* lps = p.out.token_logprobs + b * (p.D + 1);
