@@ -176,23 +176,32 @@ def allocate_workspace(nbytes: int, device):
     return torch.zeros(nbytes, dtype=torch.uint8, device=device)
 
 
-# Workspaces the binding supplies when the caller passes none: one per (device, stream), so that calls
-# on different streams never share one. Each call leaves its workspace ready for the next.
-_workspaces = {}
+class _Workspaces:
+    """Workspaces the binding supplies when the caller passes none: one per (device, stream), so that calls on different
+    streams never share one. Each call leaves its workspace ready for the next. Sizes are powers of two, and one that a
+    larger call replaces is kept: a captured CUDA graph may still use it."""
+
+    def __init__(self, size_call: str):
+        self.size_call = size_call  # what tells the bytes a call needs, for the error
+        self.current = {}
+        self.outgrown = []
+
+    def get(self, nbytes: int, device, stream: int):
+        import torch
+
+        key = (device.index, stream)
+        ws = self.current.get(key)
+        if ws is None or ws.numel() < nbytes:
+            if torch.cuda.is_current_stream_capturing():
+                raise SfcError("a CUDA graph is being captured and no workspace of this size exists for the stream: "
+                               f"pass workspace= (allocate_workspace({self.size_call}(...))) or call once before capture")
+            if ws is not None:
+                self.outgrown.append(ws)
+            ws = self.current[key] = allocate_workspace(1 << (nbytes - 1).bit_length(), device)
+        return ws
 
 
-def _default_workspace(nbytes: int, device, stream):
-    import torch
-
-    key = (device.index, int(stream.cuda_stream))
-    ws = _workspaces.get(key)
-    if ws is None or ws.numel() < nbytes:
-        if torch.cuda.is_current_stream_capturing():
-            raise SfcError("a CUDA graph is being captured and no workspace of this size exists for the stream: "
-                           "pass workspace= (allocate_workspace(workspace_size(...))) or call once before capture")
-        ws = allocate_workspace(nbytes, device)
-        _workspaces[key] = ws
-    return ws
+_step_workspaces = _Workspaces("workspace_size")
 
 
 class _Nothing:
@@ -330,7 +339,7 @@ def sample_filter_capture_into(out: SfcOutput, logits, temperature, top_k, top_p
         stream = torch.cuda.current_stream(logits.device)
     need = workspace_size(B, V, packed_width, dt, slices)
     if workspace is None and need > 0:
-        workspace = _default_workspace(need, logits.device, stream)
+        workspace = _step_workspaces.get(need, logits.device, int(stream.cuda_stream))
     if workspace is not None:
         _check_tensor("workspace", workspace, logits.device, workspace.dtype)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()

@@ -9,8 +9,8 @@ from typing import NamedTuple
 
 import torch
 
-from . import (FLAG_GREEDY_T0, MAX_DRAFTS, MAX_PACKED_WIDTH, SFC_OK, SfcError, _check_tensor, _dtype_code, _enter, _expect, _ptr,
-               allocate_workspace, load_library, strerror)
+from . import (FLAG_GREEDY_T0, MAX_DRAFTS, MAX_PACKED_WIDTH, SFC_OK, SfcError, _Workspaces, _check_tensor, _dtype_code, _enter, _expect,
+               _ptr, load_library, strerror)
 
 
 class VerifyOutput(NamedTuple):
@@ -20,29 +20,12 @@ class VerifyOutput(NamedTuple):
     row_status: "object"  # int32 [B]
 
 
-# Workspaces the binding supplies when the caller passes none: one per (device, stream). One that a larger call
-# replaces is kept: a captured CUDA graph may still use it.
-_workspaces = {}
-_outgrown = []
+_workspaces = _Workspaces("verify_workspace_size")
 
 
 def verify_workspace_size(B: int, D: int, V: int, dtype: int) -> int:
     """Bytes of workspace that ``verify_drafts`` needs: zero-filled before its first use, one call at a time."""
     return int(load_library().sfc_verify_workspace_size(B, D, V, dtype))
-
-
-def _workspace(nbytes, device, stream):
-    key = (device.index, stream)
-    ws = _workspaces.get(key)
-    if ws is None or ws.numel() < nbytes:
-        if torch.cuda.is_current_stream_capturing():
-            raise SfcError("a CUDA graph is being captured and no workspace of this size exists for the stream: "
-                           "pass workspace= (allocate_workspace(verify_workspace_size(...))) or call once before capture")
-        if ws is not None:
-            _outgrown.append(ws)
-        ws = allocate_workspace(1 << (nbytes - 1).bit_length(), device)  # the next power of two: few are outgrown
-        _workspaces[key] = ws
-    return ws
 
 
 def check_positions(name, t, B, positions):
@@ -102,7 +85,7 @@ def verify_drafts(target_logits, draft_logits, draft_tokens, uniforms, temperatu
                              num_drafts, workspace)
     with context:
         if workspace is None:
-            workspace = _workspace(lib.sfc_verify_workspace_size(B, D, V, dt), dev, stream)
+            workspace = _workspaces.get(lib.sfc_verify_workspace_size(B, D, V, dt), dev, stream)
         else:
             _check_tensor("workspace", workspace, dev, workspace.dtype)
         out = _outputs(B, D, dev)
