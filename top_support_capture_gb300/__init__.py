@@ -186,10 +186,12 @@ class _Workspaces:
         self.current = {}
         self.outgrown = []
 
-    def get(self, nbytes: int, device, stream: int):
+    def get(self, nbytes: int, device, handle: int, stream=None):
+        """The workspace of the stream with that handle; ``stream`` is the stream where it is not the current one (a new
+        workspace is zero-filled in its order)."""
         import torch
 
-        key = (device.index, stream)
+        key = (device.index, handle)
         ws = self.current.get(key)
         if ws is None or ws.numel() < nbytes:
             if torch.cuda.is_current_stream_capturing():
@@ -197,7 +199,8 @@ class _Workspaces:
                                f"pass workspace= (allocate_workspace({self.size_call}(...))) or call once before capture")
             if ws is not None:
                 self.outgrown.append(ws)
-            ws = self.current[key] = allocate_workspace(1 << (nbytes - 1).bit_length(), device)
+            with torch.cuda.stream(stream):
+                ws = self.current[key] = allocate_workspace(1 << (nbytes - 1).bit_length(), device)
         return ws
 
 
@@ -339,7 +342,7 @@ def sample_filter_capture_into(out: SfcOutput, logits, temperature, top_k, top_p
         stream = torch.cuda.current_stream(logits.device)
     need = workspace_size(B, V, packed_width, dt, slices)
     if workspace is None and need > 0:
-        workspace = _step_workspaces.get(need, logits.device, int(stream.cuda_stream))
+        workspace = _step_workspaces.get(need, logits.device, int(stream.cuda_stream), stream)
     if workspace is not None:
         _check_tensor("workspace", workspace, logits.device, workspace.dtype)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
