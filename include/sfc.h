@@ -434,6 +434,13 @@ int sfc_sample_filter_capture_noalloc(const void* logits, int dtype, int64_t B, 
                                       float* support_logprobs, int32_t* lengths, float* selected_logprob,
                                       int32_t* row_status, int32_t slices, void* stream);
 
+/*
+ * Which CUDA graph capture `stream` takes part in: a number of its own for each capture of the process, 0 for none. For
+ * callers that keep workspaces: a graph goes on using the workspace that it was captured with, so calls of
+ * different captures, and calls outside any, must not share one unless nothing lets them overlap.
+ */
+uint64_t sfc_capture_id(void* stream);
+
 /* Static, NUL-terminated text for a return code. */
 const char* sfc_strerror(int code);
 

@@ -1,5 +1,4 @@
 """The workspaces that the binding keeps, on the streams and in the graphs that use them."""
-import numpy as np
 import pytest
 
 from top_support_capture_gb300 import workloads as wl
@@ -29,6 +28,9 @@ def decode_args(seed=0, B=2, V=151936, W=1024):
 
 
 def same(a, b):
+    if not hasattr(a, "lengths"):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+        return
     n = a.lengths.tolist()
     assert n == b.lengths.tolist() and torch.equal(a.tokens, b.tokens) and torch.equal(a.row_status, b.row_status)
     for r, k in enumerate(n):
@@ -54,3 +56,69 @@ def test_made_on_the_stream_that_uses_it(monkeypatch):
     assert made == [side]
     assert torch.cuda.current_stream() != side
     same(ref, out)
+
+
+def test_capture_ids():
+    """Its own for each capture, the same on every stream that joined it, 0 outside."""
+    import top_support_capture_gb300 as sfc
+
+    lib, ids = sfc.load_library(), []
+    here = lambda: lib.sfc_capture_id(torch.cuda.current_stream().cuda_stream)
+    assert here() == 0 and lib.sfc_capture_id(None) == 0
+    x = torch.zeros(8, device="cuda")
+    for _ in range(2):
+        side, other = torch.cuda.Stream(), torch.cuda.Stream()
+        with torch.cuda.graph(torch.cuda.CUDAGraph(), stream=side):
+            ids.append(here())
+            assert ids[-1] != 0 and lib.sfc_capture_id(other.cuda_stream) == 0
+            other.wait_stream(side)
+            assert lib.sfc_capture_id(other.cuda_stream) == ids[-1]
+            x.add_(1)
+            side.wait_stream(other)
+    assert ids[0] != ids[1] and here() == 0
+
+
+@pytest.mark.parametrize("kind", ["decode", "verify"])
+def test_graphs_of_one_stream_replayed_beside_each_other(kind):
+    """Two graphs captured on one stream after one warm-up there, replayed at once on two streams, beside eager calls on
+    the stream they were captured on: each result is that of a call by itself."""
+    import top_support_capture_gb300 as sfc
+    from top_support_capture_gb300 import speculative
+
+    if kind == "decode":
+        inputs = [decode_args(seed) for seed in range(3)]
+        call = lambda i: sfc.sample_filter_capture(*inputs[i][0], 3, 4 + i, inputs[i][1])
+    else:
+        def one(seed, B=2, D=3, V=50021):
+            gen = torch.Generator("cuda").manual_seed(seed)
+            t = 2 * torch.randn((B, D + 1, V), generator=gen, device="cuda")
+            d = t[:, :D] + 0.5 * torch.randn((B, D, V), generator=gen, device="cuda")
+            return t, d.contiguous(), d.argmax(2).int(), torch.rand((B, D), generator=gen, device="cuda"), torch.ones(B, device="cuda")
+
+        inputs = [one(seed) for seed in range(3)]
+        call = lambda i: sfc.verify_drafts(*inputs[i], 3, 4 + i)
+    alone = [call(i) for i in range(3)]
+    torch.cuda.synchronize()
+    side, replay = torch.cuda.Stream(), [torch.cuda.Stream(), torch.cuda.Stream()]
+    with torch.cuda.stream(side):
+        call(2)
+    graphs, held = [], []
+    for i in range(2):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[i], stream=side):
+            held.append([call(i) for _ in range(8)])
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for i in range(2):
+            with torch.cuda.stream(replay[i]):
+                graphs[i].replay()
+        with torch.cuda.stream(side):
+            eager = call(2)
+    torch.cuda.synchronize()
+    same(alone[2], eager)
+    for i in range(2):
+        for out in held[i]:
+            same(alone[i], out)
+    for kept in (sfc._step_workspaces, speculative._workspaces):  # each left as it has to be
+        for ws in (*kept.current.values(), *(w for had in kept.captured.values() for w in had)):
+            assert not ws.any()

@@ -38,7 +38,8 @@ MAX_SLICES = 8
 EXPORTED = ("sfc_sample_filter_capture", "sfc_sample_filter_capture_ex", "sfc_workspace_size",
             "sfc_workspace_size_ex", "sfc_strerror", "sfc_replay_logprob", "sfc_pack_supports",
             "sfc_sample_filter_capture_noalloc", "sfc_replay_backward", "sfc_distill_forward", "sfc_distill_backward",
-            "sfc_distill_forward_backward", "sfc_verify_workspace_size", "sfc_verify_drafts", "sfc_verify_supports")
+            "sfc_distill_forward_backward", "sfc_verify_workspace_size", "sfc_verify_drafts", "sfc_verify_supports",
+            "sfc_capture_id")
 STATIC_SCRATCH_BYTES = 5 * 1024 * 1024
 
 _lib = None
@@ -82,6 +83,8 @@ def load_library() -> ctypes.CDLL:
                                                       [c.c_int32, c.c_void_p])
     lib.sfc_workspace_size_ex.restype = c.c_size_t
     lib.sfc_workspace_size_ex.argtypes = [c.c_int64, c.c_int64, c.c_int32, c.c_int, c.c_int32]
+    lib.sfc_capture_id.restype = c.c_uint64
+    lib.sfc_capture_id.argtypes = [c.c_void_p]  # stream
     lib.sfc_strerror.restype = c.c_char_p
     lib.sfc_strerror.argtypes = [c.c_int]
     lib.sfc_pack_supports.restype = c.c_int
@@ -176,32 +179,61 @@ def allocate_workspace(nbytes: int, device):
     return torch.zeros(nbytes, dtype=torch.uint8, device=device)
 
 
+def _capture_id(handle: int) -> int:
+    return load_library().sfc_capture_id(handle)
+
+
 class _Workspaces:
     """Workspaces the binding supplies when the caller passes none: one per (device, stream), so that calls on different
-    streams never share one. Each call leaves its workspace ready for the next. Sizes are powers of two, and one that a
-    larger call replaces is kept: a captured CUDA graph may still use it."""
+    streams never share one. Each call leaves its workspace ready for the next. Sizes are powers of two.
+
+    A graph uses the workspace that it was captured with for as long as it lives, on whatever stream it is replayed. So a
+    capture shares none with other captures or with calls outside, and its workspaces are kept: its first call on a stream
+    takes that stream's, and where an earlier capture has taken it, makes one inside the capture (the graph then zero-fills
+    it on every replay)."""
 
     def __init__(self, size_call: str):
         self.size_call = size_call  # what tells the bytes a call needs, for the error
-        self.current = {}
-        self.outgrown = []
+        self.current = {}  # (device, stream): of calls outside captures
+        self.largest = {}  # (device, stream): bytes of the largest of those so far
+        self.captured = {}  # (device, stream, capture): all that the capture's calls have had, the largest last
 
     def get(self, nbytes: int, device, handle: int, stream=None):
         """The workspace of the stream with that handle; ``stream`` is the stream where it is not the current one (a new
         workspace is zero-filled in its order)."""
-        import torch
-
         key = (device.index, handle)
+        capture = _capture_id(handle)
+        if capture:
+            return self._of_capture(nbytes, device, key, capture, stream)
         ws = self.current.get(key)
         if ws is None or ws.numel() < nbytes:
-            if torch.cuda.is_current_stream_capturing():
-                raise SfcError("a CUDA graph is being captured and no workspace of this size exists for the stream: "
-                               f"pass workspace= (allocate_workspace({self.size_call}(...))) or call once before capture")
-            if ws is not None:
-                self.outgrown.append(ws)
-            with torch.cuda.stream(stream):
-                ws = self.current[key] = allocate_workspace(1 << (nbytes - 1).bit_length(), device)
+            self.largest[key] = max(self.largest.get(key, 0), _power_of_two(nbytes))
+            ws = self.current[key] = self._make(self.largest[key], device, stream)
         return ws
+
+    def _of_capture(self, nbytes, device, key, capture, stream):
+        had = self.captured.get((*key, capture), ())
+        if had and had[-1].numel() >= nbytes:
+            return had[-1]
+        if self.largest.get(key, 0) < nbytes:
+            raise SfcError("a CUDA graph is being captured and no workspace of this size exists for the stream: "
+                           f"pass workspace= (allocate_workspace({self.size_call}(...))) or call once before capture")
+        ws = self.current.pop(key, None)
+        if ws is None:
+            ws = self._make(_power_of_two(nbytes), device, stream)
+        self.captured[(*key, capture)] = (*had, ws)
+        return ws
+
+    @staticmethod
+    def _make(nbytes, device, stream):
+        import torch
+
+        with torch.cuda.stream(stream):
+            return allocate_workspace(nbytes, device)
+
+
+def _power_of_two(n: int) -> int:
+    return 1 << (n - 1).bit_length()
 
 
 _step_workspaces = _Workspaces("workspace_size")
@@ -331,7 +363,7 @@ def sample_filter_capture_into(out: SfcOutput, logits, temperature, top_k, top_p
                                test_stall: bool = False) -> None:
     """Enqueue one call writing into preallocated ``out`` (all CUDA tensors, contiguous). ``workspace``
     (a zero-filled uint8 CUDA tensor of ``workspace_size(...)`` bytes, used by one call at a time) may be
-    omitted: the binding then keeps one per device and stream."""
+    omitted: the binding then keeps one per device and stream, and one for each graph capture on it."""
     import torch
 
     lib = load_library()

@@ -88,6 +88,16 @@ extern "C" size_t sfc_workspace_size(int64_t B, int64_t V, int32_t packed_width,
   return sfc_workspace_size_ex(B, V, packed_width, dtype, 0);
 }
 
+extern "C" uint64_t sfc_capture_id(void* stream) {
+  cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+  unsigned long long id = 0;
+  if (cudaStreamGetCaptureInfo(static_cast<cudaStream_t>(stream), &status, &id) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return 0;
+  }
+  return status == cudaStreamCaptureStatusActive ? id + 1 : 0;
+}
+
 extern "C" const char* sfc_strerror(int code) {
   switch (code) {
     case SFC_OK: return "success";

@@ -73,7 +73,8 @@ def verify_drafts(target_logits, draft_logits, draft_tokens, uniforms, temperatu
     drafts that were not drawn (looked up); ``uniforms`` [B, D] f32 in [0, 1) decide; ``temperature`` [B] f32 (and
     ``draft_temperature``, the same when omitted); ``num_drafts`` [B] int32 for requests with fewer than D drafts;
     ``greedy_t0`` makes rows of temperature 0 greedy; ``seed``, ``step`` and ``row_offset`` key the draw's noise.
-    The workspace may be omitted: the binding then keeps one per device and stream. See include/sfc.h."""
+    The workspace may be omitted: the binding then keeps one per device and stream, and one for each graph capture on it
+    (after a call on that stream outside the capture). See include/sfc.h."""
     if not target_logits.is_cuda:
         raise SfcError(f"target_logits must be a CUDA tensor, got {target_logits.device}")
     dev = target_logits.device
