@@ -434,11 +434,14 @@ def replay_logprob(logits, temperature, support_ids, lengths, tokens, support_lo
                    stream=None) -> ReplayOutput:
     """The sampled tokens' log-probabilities under ``logits`` [B, V] (bf16/f32 CUDA) renormalised over
     captured supports ``support_ids`` [B, W] int32 with ``lengths`` [B] int32 (see include/sfc.h).
-    Differentiable in ``logits`` (through ``replay_logprob_backward``): a row with status OVERFLOW or BADPARAM
-    passes no gradient on, nor does the token of an OUTSIDE row."""
+    Differentiable in ``logits`` (through ``replay_logprob_backward``; reverse mode, and in nothing else): a row with status
+    OVERFLOW or BADPARAM passes no gradient on, nor does the token of an OUTSIDE row."""
     import torch
+    from torch.autograd import forward_ad
 
-    if torch.is_grad_enabled() and logits.requires_grad:
+    dual = getattr(forward_ad, "_current_level", 0) >= 0 and any(  # refused there, not dropped
+        forward_ad.unpack_dual(t).tangent is not None for t in (logits, temperature))
+    if dual or (torch.is_grad_enabled() and logits.requires_grad):
         from .training import differentiable_replay
 
         return differentiable_replay(logits, temperature, support_ids, lengths, tokens, support_logprobs, stream)

@@ -10,6 +10,7 @@ from __future__ import annotations
 from typing import NamedTuple
 
 import torch
+from torch.autograd import forward_ad
 
 from . import (FLAG_NORMALISE_TEACHER, FLAG_TEST_STALL, MAX_PACKED_WIDTH, SFC_OK, ReplayOutput, SfcError, _dtype_code, _enter, _expect, _ptr,
                load_library, replay_logprob, strerror)
@@ -62,6 +63,19 @@ def check_packed(logits, temperature, ids, lengths, values=None, values_name="te
     if values is not None:
         _expect(values_name, values, dev, torch.float32, shape)
     return dev, B, W
+
+
+def check_derivatives(logits, **constants):
+    """Refuses derivatives that the calls here do not give, which would be lost without a word: forward-mode, and gradients
+    of anything but the logits."""
+    if getattr(forward_ad, "_current_level", 0) >= 0:  # (inside a dual level)
+        for name, t in (("logits", logits), *constants.items()):
+            if forward_ad.unpack_dual(t).tangent is not None:
+                raise SfcError(f"{name} is a forward-mode dual tensor: there is no forward-mode derivative")
+    if torch.is_grad_enabled():
+        for name, t in constants.items():
+            if t.requires_grad:
+                raise SfcError(f"{name} requires a gradient, which is given for the logits only: detach it")
 
 
 def _raise(name, rc):
@@ -132,11 +146,13 @@ def distill_loss(logits, temperature, teacher_ids, teacher_values, lengths, norm
     """Per-row distillation losses of a student's ``logits`` [B, V] (bf16/f32 CUDA) against packed teachers:
     ``teacher_ids`` [B, W] int32 with ``teacher_values`` [B, W] f32, log-probabilities (a capture's
     ``support_ids`` and ``support_logprobs``) or, with ``normalise``, raw top logits; ``lengths`` [B] int32 (0:
-    the row has no teacher). Differentiable in ``logits``. See include/sfc.h."""
+    the row has no teacher). Differentiable in ``logits`` (reverse mode), and in nothing else: a ``temperature`` or
+    ``teacher_values`` that requires a gradient is refused. See include/sfc.h."""
     row = check_rows("logits", logits)
     if teacher_values is None:
         raise SfcError("teacher_values is required")
     check_packed(logits, temperature, teacher_ids, lengths, teacher_values)
+    check_derivatives(logits, temperature=temperature, teacher_values=teacher_values)
     if torch.is_grad_enabled() and logits.requires_grad:
         _, context = _enter(logits.device, stream, logits, temperature, teacher_ids, teacher_values, lengths)
         with context:
@@ -217,6 +233,7 @@ class _Replay(torch.autograd.Function):
 
 def differentiable_replay(logits, temperature, support_ids, lengths, tokens, support_logprobs, stream) -> ReplayOutput:
     check_rows("logits", logits)
+    check_derivatives(logits, temperature=temperature)
     _, context = _enter(logits.device, stream, logits, temperature, support_ids, lengths, tokens)
     with context:
         return ReplayOutput(*_Replay.apply(logits, temperature, support_ids, lengths, tokens, support_logprobs))
