@@ -295,7 +295,8 @@ int sfc_distill_forward(const void* logits, int dtype, int64_t B, int64_t V, int
 
 /*
  * The gradient of sfc_distill_forward with respect to its logits, from the row_stats that the forward call
- * wrote for the same arguments.
+ * wrote for the same arguments. (Entries that have changed since then give other gradients; ids outside [0, V) write
+ * nothing.)
  *
  * grad_loss       [B] float32: the upstream gradient of each row's loss.
  * grad_logits     [B, grad_stride] elements of `dtype` out, the first V of each row are written, each rounded
