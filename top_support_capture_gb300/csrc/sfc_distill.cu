@@ -386,11 +386,14 @@ cudaError_t choose(DistillParams& p, int64_t B, cudaStream_t stream) {
   const int64_t fill = std::min<int64_t>({kMaxSlices, cut(1024), (304 + B - 1) / B});
   // Rows that one CTA holds, enough of them to fill the GPU: the smaller the CTA the better, since each thread's fixed
   // work and the CTA's barriers weigh less and more CTAs take turns on a SM (2048 rows, loss and gradient: 5000 bf16 12.6
-  // us against 30.9 with two CTAs of 512 a SM, 12000 20.6 : 36.2, 26000 39 : 48, 32000 51 : 57).
+  // us against 30.9 with two CTAs of 512 a SM, 12000 20.6 : 36.2, 26000 39 : 48, 32000 51 : 57; the gradient alone 16.8 :
+  // 32.5, 26.0 : 37.5, 48.5 : 54.2, 54.9 : 59.7; the loss alone 15.1 : 20.0 and 18.4 : 24.7 with CTAs of 128 against 256).
+  // The loss alone stays in CTAs of 256, of which four and not three fit a SM (32000: 34.9, with 384 41.5; 608 rows 12.2 : 17.0).
   if (B >= 304) {
     if (vectors <= kKeepBytes / 8 / 16 - 8 && fits(1)) return start<DT, 128, 8, FWD && BWD, FWD, BWD>(p, B, stream);
     if (vectors <= kKeepBytes / 4 / 16 - 8 && fits(1)) return start<DT, 256, 4, FWD && BWD, FWD, BWD>(p, B, stream);
-    if (vectors <= kKeepBytes / 3 / 16 - 8 && fits(1)) return start<DT, 384, 3, FWD && BWD, FWD, BWD>(p, B, stream);
+    if constexpr (BWD)
+      if (vectors <= kKeepBytes / 3 / 16 - 8 && fits(1)) return start<DT, 384, 3, FWD, FWD, true>(p, B, stream);
   }
   if constexpr (FWD && BWD) {  // a slice, in whole 128-byte lines, within its CTA's shared memory
     if (fits(std::max(fill, cut(kKeepBytes / 2 / 16 - 8)))) return start<DT, 512, 2, true, true, true>(p, B, stream);
