@@ -292,7 +292,7 @@ __global__ void __launch_bounds__(NT, MINB) distill_kernel(const __grid_constant
         // gradient's own call the ids may be others than those that the forward call checked
         const int32_t i = b.id[e];
         const bool body_entry = static_cast<uint32_t>(i - lo) < static_cast<uint32_t>(span);
-        here[e] = body_entry || (rank == 0 && i >= 0 && i < p.V && (i < row.head || i >= tail));
+        here[e] = body_entry || (rank == 0 && i >= 0 && (FWD || i < p.V) && (i < row.head || i >= tail));
         x[e] = !here[e] ? 0.f
                : KEEP && body_entry ? Elem<DT>::load1(reinterpret_cast<const unsigned char*>(kept), i - lo)
                                     : row.at(i);
