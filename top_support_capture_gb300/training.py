@@ -152,7 +152,8 @@ def distill_loss(logits, temperature, teacher_ids, teacher_values, lengths, norm
     if teacher_values is None:
         raise SfcError("teacher_values is required")
     check_packed(logits, temperature, teacher_ids, lengths, teacher_values)
-    check_derivatives(logits, temperature=temperature, teacher_values=teacher_values)
+    if temperature.requires_grad or teacher_values.requires_grad or getattr(forward_ad, "_current_level", 0) >= 0:
+        check_derivatives(logits, temperature=temperature, teacher_values=teacher_values)
     if torch.is_grad_enabled() and logits.requires_grad:
         _, context = _enter(logits.device, stream, logits, temperature, teacher_ids, teacher_values, lengths)
         with context:
