@@ -92,7 +92,7 @@ struct VerifyParams {
   const void* target;
   const void* draft;  // null: every draft is certain
   int64_t V, target_request, target_row, draft_request, draft_row;
-  int32_t B, D;
+  int32_t D;
   bool greedy_t0;
   const float* temperature;
   const float* draft_temperature;
@@ -568,7 +568,7 @@ extern "C" int sfc_verify_drafts(const void* target_logits, const void* draft_lo
     return SFC_EINVAL;
   if (!workspace || workspace_bytes < sfc_verify_workspace_size(B, D, V, dtype)) return SFC_EWORKSPACE;
   const sfc::VerifyParams p{target_logits, draft_logits, V, target_request_stride, target_row_stride,
-                            draft_request_stride, draft_row_stride, static_cast<int32_t>(B), D,
+                            draft_request_stride, draft_row_stride, D,
                             (flags & SFC_FLAG_GREEDY_T0) != 0, temperature,
                             draft_temperature ? draft_temperature : temperature, draft_tokens, num_drafts, uniforms,
                             sfc::RaceKey(seed, step),
