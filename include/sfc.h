@@ -311,7 +311,8 @@ int sfc_distill_backward(const void* logits, int dtype, int64_t B, int64_t V, in
  * Loss and gradient in one call, for callers that know grad_loss beforehand (a mean over the batch): the logits
  * are read from HBM once instead of twice. A bounded wait of the kernel for its own copies that gave up (not expected
  * to happen) makes the row SFC_ROW_TIMEOUT: loss NaN, gradient 0. flags: also SFC_FLAG_TEST_STALL, for tests of that path
- * (the copies are never started, the waits give up after a few polls).
+ * (the copies are never started, the waits give up after a few polls; rows too long to be kept on chip, above 1.7 MB, are read
+ * twice without such copies, and the flag changes nothing there).
  */
 int sfc_distill_forward_backward(const void* logits, int dtype, int64_t B, int64_t V, int64_t row_stride,
                                  const float* temperature, const int32_t* teacher_ids, const float* teacher_values,

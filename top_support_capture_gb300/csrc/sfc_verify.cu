@@ -11,17 +11,20 @@
 // Two launches, no CTA waits for another:
 //  - Statistics: the two rows of every position are cut into slices, one CTA each, ordered by position. A CTA leaves
 //    its slice's softmax statistics in the request's block of the workspace; the last one at a position (an atomic
-//    ticket) merges them and decides on the position's draft. A refusal raises the request's stop mark, and the CTAs
-//    of later positions that have not started yet skip their rows: those do not matter.
+//    ticket) merges them and decides on the position's draft. A refusal raises the request's stop mark; where the CTAs
+//    are more than run at once (a row is one slice then), those of later positions that have not started yet skip their
+//    rows: those do not matter.
 //  - Draw: the vocabulary of each request is cut into slices that race at the position it stopped at (the two rows
 //    come from L2 where they still lie there); the last slice merges, writes the outputs and returns the request's
 //    block to zero.
-// 64 requests x 4 drafts x 151936 bf16: 57 us, 33 of them the statistics (175 MB at 5.2 TB/s: what one wave of
-// streaming CTAs reaches with its start and its end), 28 the draw, which is bound by instructions (Philox and the two
-// exponentials of an element). One request: 13.7 us, two chains of dependent steps (parameters, rows, merge, ticket,
-// decision; decision, rows, race, ticket, outputs). Tried: the statistics in a launch for every two positions, the
-// later ones skipping refused requests: 73 us, each launch adds more than it saves; slices of a third of a row in
-// 2.3 waves: 59 us.
+// 64 requests x 4 drafts x 151936 bf16: 57 us as called. Profiled one by one from cold caches the statistics take 34
+// (175 MB at 5.1 TB/s: what one wave of streaming CTAs reaches with its start and its end; a warp waits for memory in nine
+// cycles of fourteen) and the draw 29. Of the draw's time the SMs have work in 70 % (576 CTAs in 608 places, uneven at the
+// end), and one that has issues in 61 % of its cycles: 64 registers leave it 6.4 warps a scheduler, and of a warp's 10.4
+// cycles an instruction 1.9 pass waiting for the one before (Philox is a chain of products), 1.2 for an arithmetic pipe, 1.1
+// at a barrier. One request: 13.9 us, two chains of dependent steps (parameters, rows, merge, ticket, decision; decision,
+// rows, race, ticket, outputs). Tried: the statistics in a launch for every two positions, the later ones skipping
+// refused requests: 73 us, each launch adds more than it saves; slices of a third of a row in 2.3 waves: 59 us.
 #include <algorithm>
 #include <cfloat>
 #include <cstdint>
@@ -132,8 +135,9 @@ __device__ __forceinline__ RowSpan<DT> draft_row(const VerifyParams& p, int64_t 
   return RowSpan<DT>(p.draft, b * p.draft_request + j * p.draft_row, p.V);
 }
 
-// ln of the probability of token t from its logit x: in 32 bits, and where that has to decide against a number next
-// to it, in 64.
+// ln of the probability of token t from its logit x, given the mass in 32 bits. What is emitted is taken in 32 bits (each of
+// x - m, its quotient, ln s and the difference rounds once: 4e-8 relative in all against 64 bits, where one thread's 64-bit
+// logarithm would cost a microsecond); what has to decide against a number next to it, in 64.
 __device__ __forceinline__ float log_prob(float x, const RowStats& st, float T, int32_t t) {
   if (T == 0.f) return t == st.argmax ? 0.f : -INFINITY;
   return (x - st.m) / T - logf(st.s);
