@@ -25,7 +25,7 @@
  *     candidate subset instead of a full-vocabulary sort).
  *
  * Conventions shared by every entry point:
- *   - Every array argument is a DEVICE pointer, allocated and owned by the caller. The library
+ *   - Every array argument is a DEVICE pointer (unless it is said to be a HOST array), allocated and owned by the caller. The library
  *     allocates nothing and keeps no state between calls other than per-device launch settings
  *     (and what a call leaves in the caller's workspace: see sfc_workspace_size).
  *   - Calls are asynchronous on `stream` (a cudaStream_t; NULL = the legacy default stream): a
@@ -92,6 +92,10 @@ extern "C" {
 
 /* Largest number of drafted tokens per request that the verification calls accept. */
 #define SFC_MAX_DRAFTS 64
+
+/* Largest numbers of given tokens and of top alternatives per row that sfc_token_logprobs accepts. */
+#define SFC_MAX_GIVEN 64
+#define SFC_MAX_TOP 64
 
 /*
  * Bytes of device workspace that sfc_sample_filter_capture needs for these sizes (0: none; workspace
@@ -384,6 +388,103 @@ int sfc_verify_supports(const int32_t* target_ids, const float* target_logprobs,
                         const int32_t* draft_tokens, const int32_t* num_drafts, const float* uniforms, uint64_t seed,
                         uint64_t step, int64_t row_offset, int32_t* accepted, int32_t* tokens, float* token_logprobs,
                         int32_t* row_status, void* stream);
+
+/*
+ * Log-probabilities of given tokens over the whole vocabulary, with each row's entropy and its top alternatives. Per row
+ * r, with z = logits / T:
+ *   ln p = z - ln sum_V exp z,  logprobs[r, i] = ln p at tokens[r, i],  entropy[r] = - sum_V p ln p
+ *   top_ids[r, j], top_logprobs[r, j]: the `top` largest logits, ties to the lowest id, largest first
+ *
+ * logits          [B, row_stride] elements of `dtype`, row-major; aligned to the element size. -inf logits have
+ *                 probability 0 (a given token there has log-probability -inf) and are no alternatives.
+ * temperature     [B] float32, finite and > 0.
+ * tokens          [B, M] int32, 0 <= M <= SFC_MAX_GIVEN; the same token may be given twice; -1: no token in this place
+ *                 (log-probability 0). M = 0: tokens and logprobs may be NULL.
+ * top             0 <= top <= SFC_MAX_TOP. 0: top_ids and top_logprobs may be NULL. Places past the last finite logit:
+ *                 id -1, log-probability -inf.
+ * logprobs        [B, M] float32 out. entropy [B] float32 out. top_ids [B, top] int32, top_logprobs [B, top] float32 out.
+ * row_stats       [B, 4] float32 out (16-byte aligned), or NULL: what sfc_token_logprobs_backward needs of the rows.
+ * row_status      [B] int32 out: SFC_ROW_OK, or SFC_ROW_BADPARAM (every number NaN, ids -1) when T is not finite or <= 0, a
+ *                 token is below -1 or not below V, a logit is NaN or +inf, or no logit is finite.
+ * Every array is a device pointer owned by the caller; nothing is allocated; results are deterministic.
+ * Returns SFC_OK or a negative code (nothing enqueued).
+ */
+int sfc_token_logprobs(const void* logits, int dtype, int64_t B, int64_t V, int64_t row_stride, const float* temperature,
+                       const int32_t* tokens, int32_t M, int32_t top, float* logprobs, float* entropy, int32_t* top_ids,
+                       float* top_logprobs, float* row_stats, int32_t* row_status, void* stream);
+
+/*
+ * The gradient of sfc_token_logprobs with respect to its logits, from the row_stats that the forward call wrote for the
+ * same logits and temperatures:
+ *   grad_logits[r, j] = (sum_i g_i ([tokens[r, i] = j] - p_j) - h p_j (ln p_j + entropy[r])) / T
+ * with g = grad_logprobs[r, :], h = grad_entropy[r]. (For gradients of top alternatives their ids are given as tokens.)
+ *
+ * tokens          [B, M] int32, 0 <= M <= SFC_MAX_GIVEN + SFC_MAX_TOP. Ids outside [0, V) pass no gradient on, nor do tokens
+ *                 whose logit is -inf (their log-probability is a constant).
+ * grad_logprobs   [B, M] float32, or NULL: all 0. grad_entropy [B] float32, or NULL: all 0.
+ * grad_logits     [B, grad_stride] elements of `dtype` out, the first V of each row are written, each rounded once;
+ *                 aligned to the element size. Must not overlap the logits. BADPARAM rows get zeros.
+ */
+int sfc_token_logprobs_backward(const void* logits, int dtype, int64_t B, int64_t V, int64_t row_stride,
+                                const float* temperature, const int32_t* tokens, int32_t M, const float* row_stats,
+                                const float* grad_logprobs, const float* grad_entropy, void* grad_logits,
+                                int64_t grad_stride, void* stream);
+
+/*
+ * The clipped policy loss of each row's sampled token and its gradient in one call: the logits are read from HBM once. With
+ * lp and H the token's log-probability and the row's entropy as sfc_token_logprobs defines them, A = advantages[r] and
+ * rho = exp(lp - old_logprobs[r]):
+ *   loss[r] = - min(rho A, clamp(rho, 1 - clip_low, 1 + clip_high) A) - entropy_weight H,   or
+ *   loss[r] = - A lp - entropy_weight H                                     (old_logprobs NULL: weighted cross-entropy)
+ *   grad_logits[r, j] = grad_loss[r] dloss[r]/dlogits[r, j]
+ * A clipped ratio passes no gradient on; at the border it does.
+ *
+ * tokens          [B] int32; -1: a row of padding (its logits do not matter): loss, outputs and gradient 0.
+ * old_logprobs    [B] float32, finite, or NULL. advantages [B] float32, finite.
+ * clip_low        in [0, 1]; clip_high >= 0, finite; entropy_weight finite (0: the loss has no such term).
+ * flags           0, or SFC_FLAG_TEST_STALL (for tests of the failure path: see sfc_distill_forward_backward).
+ * grad_loss       [B] float32: the upstream gradient of each row's loss (a mean over the batch: 1 / B each).
+ * loss, logprobs, entropy   [B] float32 out; NaN on BADPARAM and TIMEOUT rows.
+ * row_status      [B] int32 out: SFC_ROW_OK; SFC_ROW_BADPARAM when T is not finite or <= 0, the token is below -1 or not
+ *                 below V, an advantage or old log-probability is not finite, or (rows with a token) a logit is NaN or
+ *                 +inf or none is finite; SFC_ROW_TIMEOUT when a bounded wait of the kernel for its own copies gave up
+ *                 (not expected to happen). Such rows' gradients are 0.
+ * A token whose logit is -inf has rho = 0, or without old_logprobs the loss +inf (A > 0), and passes no gradient on. A ratio
+ * above the largest float32 that is not clipped makes the loss +inf; the gradient's slope is then held at that number.
+ * grad_logits     as in sfc_token_logprobs_backward.
+ * Every array is a device pointer owned by the caller; nothing is allocated; results are deterministic.
+ * Returns SFC_OK or a negative code (nothing enqueued).
+ */
+int sfc_policy_forward_backward(const void* logits, int dtype, int64_t B, int64_t V, int64_t row_stride,
+                                const float* temperature, const int32_t* tokens, const float* old_logprobs,
+                                const float* advantages, float clip_low, float clip_high, float entropy_weight,
+                                uint32_t flags, const float* grad_loss, float* loss, float* logprobs, float* entropy,
+                                int32_t* row_status, void* grad_logits, int64_t grad_stride, void* stream);
+
+/*
+ * The global norm of a model's gradients, and their clipping by it:
+ *   norm = sqrt(sum over all tensors and elements of x^2),  scale = min(1, max_norm / (norm + 1e-6)),  out_i = grads_i scale
+ * The sum is held in 64 bits: no element of the types' range overflows it or is lost from it. A norm that is not finite
+ * scales as the formula has it (infinite: finite elements become 0 and infinite ones NaN; NaN: all become NaN).
+ *
+ * grads, counts, dtypes   HOST arrays of n entries, read during the call: the tensors' device addresses (aligned to their
+ *                 element size; NULL where the count is 0), elements and SFC_BF16 / SFC_F32 codes. A tensor is `count`
+ *                 elements in a row. 0 <= n <= 2^20, 2^44 elements in all.
+ * max_norm        >= 0; infinity: nothing is scaled.
+ * out, out_dtypes HOST arrays of n entries: where each clipped tensor is written and its type (rounded once). A tensor's own
+ *                 address and type clips it in place (then nothing is written where scale is 1). No byte of an output may
+ *                 be shared with another output or with another tensor.
+ * norm            float32 device scalar out.
+ * workspace       device scratch of sfc_grad_norm_workspace_size(n) bytes, 8-byte aligned, of any content, used by one
+ *                 call at a time.
+ * Results are deterministic. Returns SFC_OK or a negative code (nothing enqueued on SFC_EINVAL and SFC_EWORKSPACE).
+ */
+size_t sfc_grad_norm_workspace_size(int64_t n);
+int sfc_grad_norm(const void* const* grads, const int64_t* counts, const int32_t* dtypes, int64_t n, float* norm,
+                  void* workspace, size_t workspace_bytes, void* stream);
+int sfc_clip_grad_norm(const void* const* grads, const int64_t* counts, const int32_t* dtypes, int64_t n, float max_norm,
+                       void* const* out, const int32_t* out_dtypes, float* norm, void* workspace, size_t workspace_bytes,
+                       void* stream);
 
 /*
  * Realized-size packing of captured supports ("[Sampling] Stream sampling masks as per-request

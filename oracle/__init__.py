@@ -24,3 +24,13 @@ from .replay import ROW_OUTSIDE, ReplayResult, replay_logprob, replay_row  # noq
 from .pack import pack_supports  # noqa: F401
 from .distill import DistillResult, distill, replay_gradient  # noqa: F401
 from .verify import VerifyResult, verify_drafts, verify_supports  # noqa: F401
+from .policy import (  # noqa: F401
+    GradResult,
+    LogprobsResult,
+    PolicyResult,
+    clip_scale,
+    grad_norm,
+    policy_loss,
+    token_logprobs,
+    token_logprobs_gradient,
+)

@@ -32,6 +32,8 @@ FLAG_TEST_STALL = 8
 FLAG_NORMALISE_TEACHER = 16
 MAX_PACKED_WIDTH = 16384
 MAX_DRAFTS = 64
+MAX_GIVEN = 64
+MAX_TOP = 64
 
 MAX_SLICES = 8
 
@@ -39,7 +41,8 @@ EXPORTED = ("sfc_sample_filter_capture", "sfc_sample_filter_capture_ex", "sfc_wo
             "sfc_workspace_size_ex", "sfc_strerror", "sfc_replay_logprob", "sfc_pack_supports",
             "sfc_sample_filter_capture_noalloc", "sfc_replay_backward", "sfc_distill_forward", "sfc_distill_backward",
             "sfc_distill_forward_backward", "sfc_verify_workspace_size", "sfc_verify_drafts", "sfc_verify_supports",
-            "sfc_capture_id")
+            "sfc_capture_id", "sfc_token_logprobs", "sfc_token_logprobs_backward", "sfc_policy_forward_backward",
+            "sfc_grad_norm_workspace_size", "sfc_grad_norm", "sfc_clip_grad_norm")
 STATIC_SCRATCH_BYTES = 5 * 1024 * 1024
 
 _lib = None
@@ -132,6 +135,33 @@ def load_library() -> ctypes.CDLL:
         c.c_int64, c.c_int32, c.c_void_p, c.c_void_p, c.c_void_p,  # B, D, draft_tokens, num_drafts, uniforms
         c.c_uint64, c.c_uint64, c.c_int64,  # seed, step, row_offset
     ] + outputs + [c.c_void_p]
+    lib.sfc_token_logprobs.restype = c.c_int
+    lib.sfc_token_logprobs.argtypes = rows + [
+        c.c_void_p, c.c_int32, c.c_int32,  # tokens, M, top
+        c.c_void_p, c.c_void_p, c.c_void_p, c.c_void_p,  # logprobs, entropy, top_ids, top_logprobs
+        c.c_void_p, c.c_void_p, c.c_void_p,  # row_stats, row_status, stream
+    ]
+    lib.sfc_token_logprobs_backward.restype = c.c_int
+    lib.sfc_token_logprobs_backward.argtypes = rows + [
+        c.c_void_p, c.c_int32, c.c_void_p, c.c_void_p, c.c_void_p,  # tokens, M, row_stats, grad_logprobs, grad_entropy
+        c.c_void_p, c.c_int64, c.c_void_p,  # grad, stride, stream
+    ]
+    lib.sfc_policy_forward_backward.restype = c.c_int
+    lib.sfc_policy_forward_backward.argtypes = rows + [
+        c.c_void_p, c.c_void_p, c.c_void_p, c.c_float, c.c_float, c.c_float, c.c_uint32,  # tokens, old, advantages, low, high, weight, flags
+        c.c_void_p, c.c_void_p, c.c_void_p, c.c_void_p, c.c_void_p,  # grad_loss, loss, logprobs, entropy, row_status
+        c.c_void_p, c.c_int64, c.c_void_p,  # grad, stride, stream
+    ]
+    tensors = [c.c_void_p, c.c_void_p, c.c_void_p, c.c_int64]  # grads, counts, dtypes, n (host arrays)
+    lib.sfc_grad_norm_workspace_size.restype = c.c_size_t
+    lib.sfc_grad_norm_workspace_size.argtypes = [c.c_int64]
+    lib.sfc_grad_norm.restype = c.c_int
+    lib.sfc_grad_norm.argtypes = tensors + [c.c_void_p, c.c_void_p, c.c_size_t, c.c_void_p]  # norm, workspace, bytes, stream
+    lib.sfc_clip_grad_norm.restype = c.c_int
+    lib.sfc_clip_grad_norm.argtypes = tensors + [
+        c.c_float, c.c_void_p, c.c_void_p,  # max_norm, out, out_dtypes (host arrays)
+        c.c_void_p, c.c_void_p, c.c_size_t, c.c_void_p,  # norm, workspace, bytes, stream
+    ]
     _lib = lib
     return lib
 
@@ -505,9 +535,11 @@ def pack_supports_into(lengths, support_ids, support_logprobs, offsets, ids_out,
         raise SfcError(f"sfc_pack_supports: {strerror(rc)} ({rc})")
 
 
-# The consumers of captured supports live in modules of their own, loaded on first use (they import torch).
+# The consumers of captured supports and of whole rows live in modules of their own, loaded on first use (they import torch).
 _MODULES = {
     "training": ("DistillOutput", "DistillGradOutput", "distill_loss", "distill_loss_and_grad", "replay_logprob_backward"),
+    "policy": ("TokenLogprobs", "PolicyGradOutput", "token_logprobs", "token_logprobs_backward", "policy_loss_and_grad"),
+    "gradients": ("grad_norm", "clip_grad_norm"),
     "speculative": ("VerifyOutput", "verify_drafts", "verify_supports", "verify_workspace_size"),
 }
 

@@ -1,0 +1,156 @@
+// Softmax statistics of a row together with what its entropy needs, and the gradient that log-probabilities and the
+// entropy pass to the logits. With d = (x - m) c, c = log2(e) / T, m the row's maximum:
+//
+//   s = sum 2^d,  w = sum 2^d d,  ln p = ln2 d - ln s,  H = -sum p ln p = ln s - ln2 w / s   (both parts are >= 0)
+//   sum_i g_i dlnp_i/dx_j + h dH/dx_j = (g_j - p_j (G + h (ln p_j + H))) / T,   G = sum_i g_i
+//
+// A masked logit has d = -inf and p = 0; its products p d and p ln p are 0 because d is held above kFar there, where 2^d is
+// 0 in 32 bits. The exponential itself takes the d that was not held, so that NaN and +inf logits reach s as in SoftmaxAcc.
+#pragma once
+
+#include "sfc_rows.cuh"
+
+namespace sfc {
+
+constexpr float kFar = -200.f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// Statistics of what one thread has seen, in two lanes each. m is the true maximum (see SoftmaxAcc).
+struct EntropyAcc {
+  float m = -FLT_MAX;
+  uint64_t s2 = 0, w2 = 0;
+
+  __device__ __forceinline__ void raise(float x, float c) {
+    if (x > m) {
+      const float d = fmaxf((m - x) * c, kFar), f = ex2_approx(d);
+      const uint64_t f2 = pack_f2(f, f);
+      w2 = fmul_f2(ffma_f2(pack_f2(d, d), s2, w2), f2);
+      s2 = fmul_f2(s2, f2);
+      m = x;
+    }
+  }
+  template <int N>
+  __device__ __forceinline__ void add_below(const float (&x)[N], float c) {  // none of x is above m
+    const uint64_t minus_m = pack_f2(-m, -m), c2 = pack_f2(c, c);
+    uint64_t e[N / 2];
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+      float a, b;
+      unpack_f2(fmul_f2(fadd_f2(pack_f2(x[2 * i], x[2 * i + 1]), minus_m), c2), a, b);
+      e[i] = pack_f2(ex2_approx(a), ex2_approx(b));
+      w2 = ffma_f2(e[i], pack_f2(fmaxf(a, kFar), fmaxf(b, kFar)), w2);
+    }
+#pragma unroll
+    for (int w = N / 4; w > 0; w /= 2)  // a fixed tree
+#pragma unroll
+      for (int i = 0; i < w; ++i) e[i] = fadd_f2(e[i], e[i + w]);
+    s2 = fadd_f2(s2, e[0]);
+  }
+  __device__ __forceinline__ void add(float x, float c) {
+    raise(x, c);
+    const float d = (x - m) * c, e = ex2_approx(d);
+    s2 = fadd_f2(s2, pack_f2(e, 0.f));
+    w2 = fadd_f2(w2, pack_f2(e * fmaxf(d, kFar), 0.f));
+  }
+  template <int DT>
+  __device__ __forceinline__ void add(const uint4& v, float c) {
+    raise(Elem<DT>::vmax(v), c);
+    float x[Elem<DT>::kVec];
+    Elem<DT>::unpack(v, x);
+    add_below(x, c);
+  }
+  // U vectors; bf16: one maximum of all of them (see SoftmaxAcc::add).
+  template <int DT, int U>
+  __device__ __forceinline__ void add(const uint4 (&v)[U], float c) {
+    constexpr int G = DT == 0 ? U : 1;
+#pragma unroll
+    for (int g = 0; g < U; g += G) {
+      uint4 top = v[g];
+#pragma unroll
+      for (int u = 1; u < G; ++u) top = larger<DT>(top, v[g + u]);
+      raise(Elem<DT>::vmax(top), c);
+#pragma unroll
+      for (int u = 0; u < G; ++u) {
+        float x[Elem<DT>::kVec];
+        Elem<DT>::unpack(v[g + u], x);
+        add_below(x, c);
+      }
+    }
+  }
+};
+
+struct EntropyStats {
+  float m, s, w;
+
+  __device__ __forceinline__ float log_sum() const { return logf(s); }
+  __device__ __forceinline__ float entropy() const { return fmaxf(logf(s) - kLn2 * (w / s), 0.f); }
+};
+
+// The statistics that the lanes of a warp hold, merged: the same bits in every lane.
+__device__ __forceinline__ EntropyStats merge_lanes(const EntropyStats& v, float c) {
+  const float m = warp_max(v.m), d = fmaxf((v.m - m) * c, kFar), f = ex2_approx(d);
+  return EntropyStats{m, warp_total(v.s * f), warp_total((v.w + d * v.s) * f)};
+}
+__device__ __forceinline__ EntropyStats merge_lanes(const EntropyAcc& a, float c) {
+  float s, t, w, u;
+  unpack_f2(a.s2, s, t);
+  unpack_f2(a.w2, w, u);
+  return merge_lanes(EntropyStats{a.m, s + t, w + u}, c);
+}
+// n <= 32 statistics in shared memory, merged by a whole warp (the lanes past them repeat the first with no mass).
+__device__ __forceinline__ EntropyStats merge_shared(const float4* part, int n, float c) {
+  const int lane = threadIdx.x & 31;
+  const float4 v = part[lane < n ? lane : 0];
+  return merge_lanes(EntropyStats{v.x, lane < n ? v.y : 0.f, lane < n ? v.z : 0.f}, c);
+}
+
+__device__ __forceinline__ float held(float x) {  // an overflow is held at the largest number; NaN stays
+  return fabsf(x) == INFINITY ? copysignf(FLT_MAX, x) : x;
+}
+
+// The dense part of a row's gradient: 2^d (a + b d) = -p (G + h (ln p + H)) scale.
+struct RowGradient {
+  float m, c, a, b;
+
+  // G and h with the factor that is common to the row (an upstream gradient over T) multiplied in already.
+  __device__ __forceinline__ RowGradient(float m_, float s, float H, float G, float h, float c_) : m(m_), c(c_) {
+    a = held(-(G + h * (H - logf(s))) / s);
+    b = held(-h * kLn2 / s);
+  }
+  __device__ __forceinline__ float at(float x) const {
+    const float d = (x - m) * c;
+    return ex2_approx(d) * fmaf(fmaxf(d, kFar), b, a);
+  }
+  template <int DT>
+  __device__ __forceinline__ uint4 vector(const uint4& v) const {
+    constexpr int N = Elem<DT>::kVec;
+    const uint64_t minus_m = pack_f2(-m, -m), c2 = pack_f2(c, c), a2 = pack_f2(a, a), b2 = pack_f2(b, b);
+    float x[N];
+    Elem<DT>::unpack(v, x);
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      float d, e;
+      unpack_f2(fmul_f2(fadd_f2(pack_f2(x[i], x[i + 1]), minus_m), c2), d, e);
+      const uint64_t t = ffma_f2(pack_f2(fmaxf(d, kFar), fmaxf(e, kFar)), b2, a2);
+      unpack_f2(fmul_f2(pack_f2(ex2_approx(d), ex2_approx(e)), t), x[i], x[i + 1]);
+    }
+    return Out<DT>::pack(x);
+  }
+};
+
+// One vector of a gradient row to `to`, which lies `shift` bytes past a 16-byte boundary; by whole warps (see store_shifted).
+template <int DT>
+__device__ __forceinline__ void store_vector(unsigned char* to, const uint4& w, int shift, bool active) {
+  if (DT == 0 && shift != 0) {
+    store_shifted(to, w, shift, active);
+  } else if (active) {
+    if (shift == 0) {
+      *reinterpret_cast<uint4*>(to) = w;
+    } else {
+      uint32_t* four = reinterpret_cast<uint32_t*>(to);
+      four[0] = w.x, four[1] = w.y, four[2] = w.z, four[3] = w.w;
+    }
+  }
+}
+
+}  // namespace sfc

@@ -1,0 +1,402 @@
+// Log-probabilities of given tokens over the whole vocabulary, with the row's entropy and its top alternatives, and their
+// gradient (sfc_entropy.cuh has the formulas).
+//
+// The forward call reads the logits once. A row is cut into slices of 16-byte vectors, one CTA each, which form a cluster
+// and exchange their statistics through distributed shared memory, merged in slice order.
+//
+// Top alternatives without a second pass: each thread already keeps the maximum of what it has seen. The K-th largest of
+// the maxima of K or more disjoint groups of threads is a lower bound on the K-th largest logit, since each group has an
+// element at least that large, and a tight one: with 128 groups of randomly spread logits about K + K^2 / 256 elements
+// reach it. Only the threads whose own maximum reaches the bound have such elements; their warps read those threads'
+// vectors again (from L2) and put what reaches the bound into a pool in shared memory, from which the K largest are
+// ranked by counting. Of S slices each gives two bounds, the largest of the slices' K-th and the smallest of their
+// ceil(K / S)-th; the larger one holds for the row. Where ties or a regular pattern overfill the pool, the row's first CTA
+// finds the K largest one by one instead (every thread holds its best, the winner's warp looks for its next): exact for
+// any row.
+#include <algorithm>
+#include <climits>
+#include <cstdint>
+
+#include "../../include/sfc.h"
+#include "sfc_entropy.cuh"
+#include "sfc_host.cuh"
+
+namespace sfc {
+namespace {
+
+constexpr int kMaxSlices = 8;  // the portable cluster size
+constexpr int kGroups = 128;   // of threads; not fewer than SFC_MAX_TOP, not more than the smallest CTA
+constexpr uint32_t kPool = 1024;
+static_assert(SFC_MAX_TOP <= kGroups && SFC_MAX_GIVEN <= kGroups, "");
+
+struct ScoreParams {
+  const void* logits;
+  int64_t row_stride, V;
+  const float* temperature;
+  const int32_t* tokens;
+  int32_t M, K;
+  float* logprobs;
+  float* entropy;
+  int32_t* top_ids;
+  float* top_logprobs;
+  float4* stats;  // (m, s, H, 0) for the gradient, or null
+  int32_t* row_status;
+  int32_t slices, per;  // CTAs a row, vectors a slice
+};
+
+__device__ __forceinline__ uint32_t dsmem_count(uint32_t addr) {  // the counter's old value
+  uint32_t v;
+  asm volatile("atom.relaxed.cluster.shared::cluster.add.u32 %0, [%1], 1;" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+template <int DT>
+__device__ __forceinline__ uint64_t ckey_of(float x, int64_t id) {  // 0: not an alternative (-inf)
+  return x > -INFINITY ? make_ckey(Keys<DT>::key(x), static_cast<uint32_t>(id)) : 0ull;
+}
+
+__device__ __forceinline__ uint64_t warp_max_key(uint64_t k) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) k = max(k, __shfl_xor_sync(kFull, k, o));
+  return k;
+}
+
+// The largest key below `limit` among the vectors first, first + step, ... below v1 (this lane's share of the work).
+template <int DT>
+__device__ __forceinline__ uint64_t best_below(const RowSpan<DT>& row, int first, int step, int v1, uint64_t limit) {
+  constexpr int VEC = Elem<DT>::kVec;
+  uint64_t best = 0;
+  for (int k = first; k < v1; k += step) {
+    float x[VEC];
+    Elem<DT>::unpack(__ldg(row.body() + k), x);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      const uint64_t key = ckey_of<DT>(x[e], row.head + static_cast<int64_t>(k) * VEC + e);
+      if (key < limit && key > best) best = key;
+    }
+  }
+  return best;
+}
+
+template <int DT, int NT, int MINB>
+__global__ void __launch_bounds__(NT, MINB) score_kernel(const __grid_constant__ ScoreParams p) {
+  constexpr int NW = NT / 32, VEC = Elem<DT>::kVec;
+  constexpr int U = 4;  // vectors in flight per thread (and as many again)
+  __shared__ float4 red[NW];
+  __shared__ float4 table[kMaxSlices];   // (m, s, w) of the slices
+  __shared__ float2 bounds[kMaxSlices];  // their K-th and ceil(K / S)-th group maxima
+  __shared__ float tops[NT], groups[kGroups], cut[2];
+  __shared__ uint64_t pool[kPool], winners[NW];
+  __shared__ uint32_t count;
+  const int tid = threadIdx.x, lane = tid & 31, wp = tid >> 5, S = p.slices, rank = blockIdx.y, K = p.K;
+  const int64_t r = blockIdx.x;
+  const RowSpan<DT> row(p.logits, r * p.row_stride, p.V);
+  const int nvec = static_cast<int>(row.nvec), v0 = min(rank * p.per, nvec), v1 = min(v0 + p.per, nvec);
+  RowStream<DT, NT, U> stream(row, v0, v1);
+  if (S > 1) cluster_arrive();  // the cluster's CTAs have started: waited for before the first store into another
+  const float T = p.temperature[r];
+  const bool scalar = rank == 0 && tid < row.scalars();
+  const float xs = scalar ? row.at(row.scalar_index(tid)) : -INFINITY;
+  const int32_t token = rank == 0 && tid < p.M ? p.tokens[r * p.M + tid] : -1;
+  const bool given = token >= 0 && token < p.V;
+  const float xt = given ? row.at(token) : 0.f;
+  if (tid == 0) count = 0;
+  const float c = exponent_scale(T);
+  EntropyAcc a;
+  stream.batches([&](const uint4(&v)[U]) { a.template add<DT, U>(v, c); });
+  if (scalar) a.add(xs, c);
+  const EntropyStats mine = merge_lanes(a, c);
+  if (lane == 0) red[wp] = make_float4(mine.m, mine.s, mine.w, 0.f);
+  tops[tid] = a.m;
+  const bool wrong = __syncthreads_or(token < -1 || token >= p.V) || !temperature_valid(T);
+  EntropyStats all = merge_shared(red, NW, c);
+  float bound = -FLT_MAX;
+  if (K > 0) {
+    if (tid < kGroups) {
+      float g = tops[tid];
+#pragma unroll
+      for (int i = kGroups; i < NT; i += kGroups) g = fmaxf(g, tops[tid + i]);
+      groups[tid] = g;
+    }
+    __syncthreads();
+    if (tid < kGroups) {
+      const float g = groups[tid];
+      int larger = 0;
+#pragma unroll 8
+      for (int i = 0; i < kGroups; ++i) larger += groups[i] > g || (groups[i] == g && i < tid);
+      if (larger == K - 1) cut[0] = g;
+      if (larger == (K + S - 1) / S - 1) cut[1] = g;
+    }
+    __syncthreads();
+    bound = cut[0];
+  }
+  if (S > 1) {
+    cluster_wait();
+    if (tid < S) {
+      const uint32_t to = dsmem_addr(&table[rank], tid);
+      dsmem_st64(to, pack_f2(all.m, all.s));
+      dsmem_st32(to + 8, __float_as_uint(all.w));
+      if (K > 0) dsmem_st64(dsmem_addr(&bounds[rank], tid), pack_f2(cut[0], cut[1]));
+    }
+    cluster_sync_all();
+    all = merge_shared(table, S, c);
+    if (K > 0) {
+      float low = bounds[0].y;
+      bound = bounds[0].x;
+      for (int i = 1; i < S; ++i) {
+        bound = fmaxf(bound, bounds[i].x);
+        low = fminf(low, bounds[i].y);
+      }
+      bound = fmaxf(bound, low);
+    }
+  }
+  const bool valid = stats_valid(all.m, all.s);  // uniform over the cluster
+  uint32_t n = 0;  // keys in the pool of rank 0
+  if (K > 0 && valid) {
+    const uint32_t counter = S > 1 ? dsmem_addr(&count, 0) : smem_addr(&count);
+    const uint32_t places = S > 1 ? dsmem_addr(pool, 0) : smem_addr(pool);
+    auto push = [&](float x, int64_t id) {
+      const uint32_t at = dsmem_count(counter);
+      if (at < kPool) dsmem_st64(places + at * 8, ckey_of<DT>(x, id));
+    };
+    for (unsigned who = __ballot_sync(kFull, a.m >= bound); who; who &= who - 1) {
+      const int src = wp * 32 + __ffs(who) - 1;
+      for (int k = v0 + src + lane * NT; k < v1; k += 32 * NT) {
+        const uint4 v = __ldg(row.body() + k);
+        if (Elem<DT>::vmax(v) < bound) continue;
+        float x[VEC];
+        Elem<DT>::unpack(v, x);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+          if (x[e] >= bound) push(x[e], row.head + static_cast<int64_t>(k) * VEC + e);
+      }
+    }
+    if (scalar && xs >= bound) push(xs, row.scalar_index(tid));
+    if (S > 1) cluster_sync_all();  // no CTA touches another's memory after it
+    else __syncthreads();
+  }
+  if (rank != 0) return;
+  if (K > 0 && valid) {
+    n = count;
+    if (n > kPool) {
+      n = static_cast<uint32_t>(K);
+      auto next = [&](int of, uint64_t limit) {  // the largest key of thread `of` (of the whole row's) below the limit, by its warp
+        uint64_t key = best_below<DT>(row, of + lane * NT, 32 * NT, nvec, limit);
+        if (scalar && tid == of) {
+          const uint64_t k = ckey_of<DT>(xs, row.scalar_index(tid));
+          if (k < limit && k > key) key = k;
+        }
+        return warp_max_key(key);
+      };
+      uint64_t best = 0;
+      for (int l = 0; l < 32; ++l) {
+        const uint64_t k = next(wp * 32 + l, ~0ull);
+        if (lane == l) best = k;
+      }
+      for (int j = 0; j < K; ++j) {
+        const uint64_t w = warp_max_key(best);
+        if (lane == 0) winners[wp] = w;
+        __syncthreads();
+        uint64_t top = winners[0];
+#pragma unroll
+        for (int i = 1; i < NW; ++i) top = max(top, winners[i]);
+        __syncthreads();
+        if (tid == 0) pool[j] = top;
+        if (top != 0 && w == top) {  // the winner's warp: uniform
+          const int l = __ffs(__ballot_sync(kFull, best == top)) - 1;
+          const uint64_t k = next(wp * 32 + l, top);
+          if (lane == l) best = k;
+        }
+      }
+    }
+  }
+  if (rank != 0) return;
+  const bool ok = valid && !wrong;
+  const float nan = __int_as_float(0x7fc00000), ln_s = all.log_sum();
+  auto logprob = [&](float x) { return (x - all.m) / T - ln_s; };
+  if (tid < p.M) p.logprobs[r * p.M + tid] = !ok ? nan : given ? logprob(xt) : 0.f;
+  if (tid == 0) {
+    const float H = all.entropy();
+    p.entropy[r] = ok ? H : nan;
+    p.row_status[r] = ok ? SFC_ROW_OK : SFC_ROW_BADPARAM;
+    if (p.stats) p.stats[r] = make_float4(ok ? all.m : nan, all.s, H, 0.f);
+  }
+  if (K == 0) return;
+  if (tid < K) {  // places without an alternative
+    p.top_ids[r * K + tid] = -1;
+    p.top_logprobs[r * K + tid] = ok ? -INFINITY : nan;
+  }
+  __syncthreads();  // before the others are written
+  if (!ok) return;
+  for (uint32_t i = tid; i < n; i += NT) {
+    const uint64_t key = pool[i];
+    if (key == 0) continue;
+    int above = 0;
+    for (uint32_t j = 0; j < n; ++j) above += pool[j] > key;
+    if (above >= K) continue;
+    p.top_ids[r * K + above] = static_cast<int32_t>(ckey_id(key));
+    p.top_logprobs[r * K + above] = logprob(Keys<DT>::value(ckey_key(key)));
+  }
+}
+
+struct ScoreGradParams {
+  const void* logits;
+  int64_t row_stride, V;
+  const float* temperature;
+  const int32_t* tokens;
+  int32_t M;
+  const float4* stats;
+  const float* grad_logprobs;
+  const float* grad_entropy;
+  unsigned char* grad;
+  int64_t grad_stride;
+  int32_t per;  // vectors a slice
+};
+
+constexpr int kMaxEntries = SFC_MAX_GIVEN + SFC_MAX_TOP;
+
+// Every CTA takes the row's tokens (few) and one slice of its logits. The dense part is written first; after the CTA's
+// barrier the first place of each token that lies in the slice overwrites its entry with the whole gradient, rounded once.
+template <int DT, int NT, int MINB>
+__global__ void __launch_bounds__(NT, MINB) score_backward_kernel(const __grid_constant__ ScoreGradParams p) {
+  constexpr int VEC = Elem<DT>::kVec;
+  constexpr int U = 4;
+  __shared__ int32_t ids[kMaxEntries];
+  __shared__ float gs[kMaxEntries];
+  const int tid = threadIdx.x, lane = tid & 31, rank = blockIdx.y;
+  const int64_t r = blockIdx.x;
+  const RowSpan<DT> row(p.logits, r * p.row_stride, p.V);
+  const int nvec = static_cast<int>(row.nvec), v0 = min(rank * p.per, nvec), v1 = min(v0 + p.per, nvec);
+  RowStream<DT, NT, U> stream(row, v0, v1);
+  const bool scalar = rank == 0 && tid < row.scalars();
+  const float4 st = p.stats[r];
+  const float T = p.temperature[r], c = exponent_scale(T), inv_T = fminf(1.f / T, FLT_MAX);
+  const bool live = st.x == st.x;  // rows without a log-probability pass no gradient on
+  const float h = p.grad_entropy ? p.grad_entropy[r] * inv_T : 0.f;
+  float own_x = 0.f;
+  if (tid < p.M) {  // a masked token's log-probability is the constant -inf
+    const int32_t id = p.tokens[r * p.M + tid];
+    const bool in = id >= 0 && id < p.V;
+    own_x = in ? row.at(id) : -INFINITY;
+    ids[tid] = own_x > -INFINITY ? id : -1;
+    gs[tid] = own_x > -INFINITY && p.grad_logprobs ? p.grad_logprobs[r * p.M + tid] * inv_T : 0.f;
+  }
+  __syncthreads();
+  float G = 0.f;
+  for (int j = lane; j < p.M; j += 32) G += gs[j];
+  G = warp_total(G);
+  const RowGradient dense(st.x, st.y, st.z, G, h, c);
+  unsigned char* grad = p.grad + r * p.grad_stride * Elem<DT>::kBytes;
+  unsigned char* out = grad + static_cast<int64_t>(row.head) * Elem<DT>::kBytes;
+  const int shift = static_cast<int>(reinterpret_cast<uintptr_t>(out) & 15);
+  if (!live) {
+    for (int i = v0 + tid; i - lane < v1; i += NT)
+      store_vector<DT>(out + static_cast<int64_t>(i) * 16, make_uint4(0u, 0u, 0u, 0u), shift, i < v1);
+  } else {
+    stream.each([&](const uint4& w, int i) {
+      store_vector<DT>(out + static_cast<int64_t>(i) * 16, dense.template vector<DT>(w), shift, i < v1);
+    });
+  }
+  if (scalar) {
+    const int64_t i = row.scalar_index(tid);
+    Out<DT>::store1(grad, i, live ? dense.at(row.at(i)) : 0.f);
+  }
+  if (!live) return;
+  __syncthreads();  // the dense values are written before the tokens' overwrite theirs
+  if (tid >= p.M || ids[tid] < 0) return;
+  const int64_t id = ids[tid], lo = row.head + static_cast<int64_t>(v0) * VEC, hi = row.head + static_cast<int64_t>(v1) * VEC;
+  if (!(id >= lo && id < hi) && !(rank == 0 && (id < row.head || id >= row.tail()))) return;
+  float g = 0.f;
+  for (int j = 0; j < p.M; ++j) {
+    if (ids[j] != id) continue;
+    if (j < tid) return;  // an earlier place of the same token writes it
+    g += gs[j];
+  }
+  Out<DT>::store1(grad, id, dense.at(own_x) + g);
+}
+
+int check_rows(const void* logits, int dtype, int64_t B, int64_t V, int64_t row_stride, const float* temperature) {
+  if (!logits || !temperature) return SFC_EINVAL;
+  if (dtype != SFC_BF16 && dtype != SFC_F32) return SFC_EINVAL;
+  if (B < 1 || B > INT32_MAX || V < 1 || V > INT32_MAX || row_stride < V) return SFC_EINVAL;
+  if (reinterpret_cast<uintptr_t>(logits) % (dtype == SFC_BF16 ? 2 : 4)) return SFC_EINVAL;
+  return SFC_OK;
+}
+
+int32_t slice_of(int64_t vectors, int64_t slices) {  // in whole 128-byte lines
+  return static_cast<int32_t>((vectors + slices - 1) / slices + 7) & ~7;
+}
+
+template <int DT, int NT, int MINB>
+cudaError_t start(ScoreParams p, int64_t B, cudaStream_t stream) {
+  p.per = slice_of(p.V / Elem<DT>::kVec, p.slices);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(B), static_cast<unsigned>(p.slices));
+  cfg.blockDim = dim3(NT);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim = {1, static_cast<unsigned>(p.slices), 1};
+  cfg.attrs = attr;
+  cfg.numAttrs = p.slices > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, score_kernel<DT, NT, MINB>, p);
+}
+
+template <int DT>
+cudaError_t choose(ScoreParams& p, int64_t B, cudaStream_t stream) {
+  const int64_t vectors = p.V / Elem<DT>::kVec;
+  // few rows: enough slices to fill the GPU's 304 CTA slots, of at least two vectors per thread
+  p.slices = static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>({kMaxSlices, (vectors + 1023) / 1024, (304 + B - 1) / B})));
+  if (B * p.slices > 152) return start<DT, 256, 4>(p, B, stream);
+  return start<DT, 512, 2>(p, B, stream);
+}
+
+template <int DT>
+cudaError_t start_backward(ScoreGradParams p, int64_t B, cudaStream_t stream) {
+  const int64_t vectors = p.V / Elem<DT>::kVec;
+  const int64_t slices = std::max<int64_t>(1, std::max((vectors + 20479) / 20480, std::min<int64_t>({8, (vectors + 1023) / 1024, (304 + B - 1) / B})));
+  p.per = slice_of(vectors, slices);
+  score_backward_kernel<DT, 512, 2><<<dim3(static_cast<unsigned>(B), static_cast<unsigned>(slices)), 512, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+int result(cudaError_t err) {
+  if (err == cudaSuccess) return SFC_OK;
+  (void)cudaGetLastError();
+  return SFC_ECUDA;
+}
+
+}  // namespace
+}  // namespace sfc
+
+extern "C" int sfc_token_logprobs(const void* logits, int dtype, int64_t B, int64_t V, int64_t row_stride,
+                                  const float* temperature, const int32_t* tokens, int32_t M, int32_t top, float* logprobs,
+                                  float* entropy, int32_t* top_ids, float* top_logprobs, float* row_stats, int32_t* row_status,
+                                  void* stream) {
+  const int rc = sfc::check_rows(logits, dtype, B, V, row_stride, temperature);
+  if (rc != SFC_OK) return rc;
+  if (M < 0 || M > SFC_MAX_GIVEN || (M > 0 && (!tokens || !logprobs))) return SFC_EINVAL;
+  if (top < 0 || top > SFC_MAX_TOP || (top > 0 && (!top_ids || !top_logprobs))) return SFC_EINVAL;
+  if (!entropy || !row_status || reinterpret_cast<uintptr_t>(row_stats) % 16) return SFC_EINVAL;
+  sfc::ScoreParams p{logits, row_stride, V, temperature, tokens, M, top, logprobs, entropy, top_ids, top_logprobs,
+                     reinterpret_cast<float4*>(row_stats), row_status, 1, 0};
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return sfc::result(dtype == SFC_BF16 ? sfc::choose<0>(p, B, st) : sfc::choose<1>(p, B, st));
+}
+
+extern "C" int sfc_token_logprobs_backward(const void* logits, int dtype, int64_t B, int64_t V, int64_t row_stride,
+                                           const float* temperature, const int32_t* tokens, int32_t M, const float* row_stats,
+                                           const float* grad_logprobs, const float* grad_entropy, void* grad_logits,
+                                           int64_t grad_stride, void* stream) {
+  const int rc = sfc::check_rows(logits, dtype, B, V, row_stride, temperature);
+  if (rc != SFC_OK) return rc;
+  if (M < 0 || M > sfc::kMaxEntries || (M > 0 && !tokens) || !row_stats || !grad_logits || grad_stride < V) return SFC_EINVAL;
+  const int64_t elt = dtype == SFC_BF16 ? 2 : 4;
+  const uintptr_t g = reinterpret_cast<uintptr_t>(grad_logits), l = reinterpret_cast<uintptr_t>(logits);
+  if (g % elt || reinterpret_cast<uintptr_t>(row_stats) % 16) return SFC_EINVAL;
+  if (g < l + ((B - 1) * row_stride + V) * elt && l < g + ((B - 1) * grad_stride + V) * elt) return SFC_EINVAL;
+  const sfc::ScoreGradParams p{logits, row_stride, V, temperature, tokens, M, reinterpret_cast<const float4*>(row_stats), grad_logprobs,
+                               grad_entropy, static_cast<unsigned char*>(grad_logits), grad_stride, 0};
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return sfc::result(dtype == SFC_BF16 ? sfc::start_backward<0>(p, B, st) : sfc::start_backward<1>(p, B, st));
+}
