@@ -143,6 +143,15 @@ def test_layouts_and_lists():
     check_norm(float(s), sfc.grad_norm(s))
 
 
+def test_inference_tensors():
+    import top_support_capture_gb300 as sfc
+
+    with torch.inference_mode():
+        t = torch.full((16,), 3.0, device="cuda")
+        assert float(sfc.clip_grad_norm([t], 6.0)) == 12.0 and abs(float(t[0]) - 1.5) < 1e-6
+    assert float(sfc.clip_grad_norm([t, torch.zeros(3, device="cuda")], 3.0)) == pytest.approx(6.0, abs=1e-5) and abs(float(t[0]) - 0.75) < 1e-6
+
+
 def test_refused():
     import top_support_capture_gb300 as sfc
 

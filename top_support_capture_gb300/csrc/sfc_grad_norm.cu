@@ -3,12 +3,14 @@
 //   norm = sqrt(sum over all tensors of x^2),  scale = min(1, max_norm / (norm + 1e-6)),  out = x scale
 //
 // The tensors' addresses travel in the launch's parameters (up to kMany of them; longer lists take several launches), so
-// nothing is copied to the device and a captured call holds all it needs. Each tensor is cut into chunks of kChunk 16-byte
-// vectors; the CTAs take equal runs of the list of all chunks.
+// nothing is copied to the device and a captured call holds all it needs. Each tensor is cut into chunks of 32 KB; the CTAs
+// take equal runs of the list of all chunks.
 //
-// A batch of 16 to 32 squares is summed in 32 bits and added to a 64-bit sum of its thread; the CTAs' sums lie in the
-// workspace, and whoever needs the norm adds them up in the same fixed order. A batch whose 32-bit sum overflowed, or lies
-// so low that squares were flushed, is summed again in 64 bits: the norm holds over the whole range of its elements.
+// A batch of 32 or 16 squares is summed in 32 bits, the batches of a thread with a compensated sum in 32 bits (one 64-bit
+// addition a batch took more than the memory's time: 534 M bf16 elements 396 us, so 150, 7.1 TB/s), the threads in 64. The CTAs' sums lie in
+// the workspace, and whoever needs the norm adds them up in the same fixed order. A batch whose sum lies outside
+// [2^-100, 2^100], where squares may overflow or lose bits, is summed in 64 bits by itself: the norm holds over the whole
+// range of its elements.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -22,9 +24,10 @@
 namespace sfc {
 namespace {
 
-constexpr int kThreads = 512, kCtas = 4 * 152;  // a wave of CTAs
-constexpr int kChunk = 4 * kThreads;            // vectors: four loads in flight per thread
-constexpr int kFew = 16, kMany = 1000;          // tensors of a launch: parameters of 0.6 KB, of 32 KB
+constexpr int kThreads = 256, kCtas = 4 * 152, kClipCtas = 3 * 152;  // a wave of CTAs
+constexpr int kInFlight = 8;                    // 16-byte vectors of a thread
+constexpr int kChunk = kInFlight * kThreads;    // vectors
+constexpr int kFew = 16, kMany = 1000;          // tensors of a launch: parameters of 0.7 KB, of 32 KB
 
 struct Tensor {
   const void* in;
@@ -45,7 +48,12 @@ struct Tensors {
 };
 static_assert(sizeof(Tensors<kMany>) <= 32764, "a launch's parameters");
 
-// The part of a chunk in its tensor: vectors [v0, v1) of the tensor's body; the first chunk has the scalars beside it too.
+// A launch may start while the one before it in the stream still runs (programmatic dependent launch): until the wait it
+// touches nothing that the other writes.
+__device__ __forceinline__ void allow_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_last() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// use(tensor, its chunk) for the chunks [c0, c1) of the list.
 template <int CAP, class F>
 __device__ __forceinline__ void each_chunk(const Tensors<CAP>& p, int c0, int c1, bool descending, F use) {
   if (c0 >= c1) return;
@@ -69,41 +77,57 @@ __device__ __forceinline__ void each_chunk(const Tensors<CAP>& p, int c0, int c1
   }
 }
 
-// The sum of a batch's squares.
-template <int DT, int U>
-__device__ __forceinline__ double squares(const uint4 (&v)[U]) {
-  constexpr int N = Elem<DT>::kVec;
-  uint64_t s2 = 0;
+// A batch's squares in 64 bits (out of line: batches of zeros apart, few need it).
+template <int DT>
+__device__ __noinline__ double exact_squares(uint4 a, uint4 b, uint4 c, uint4 d) {
+  constexpr uint32_t kMagnitude = DT == 0 ? 0x7FFF7FFFu : 0x7FFFFFFFu;
+  auto bits = [](const uint4& v) { return v.x | v.y | v.z | v.w; };
+  double sum = 0.0;
+  if (((bits(a) | bits(b) | bits(c) | bits(d)) & kMagnitude) == 0) return sum;
+#pragma unroll 1
+  for (int u = 0; u < 4; ++u) {
+    float x[Elem<DT>::kVec];
+    Elem<DT>::unpack(a, x);
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    float x[N];
-    Elem<DT>::unpack(v[u], x);
+    for (int i = 0; i < Elem<DT>::kVec; ++i) sum += static_cast<double>(x[i]) * x[i];
+    a = b, b = c, c = d;
+  }
+  return sum;
+}
+
+// The squares that a thread has summed.
+struct SquareAcc {
+  float sum = 0.f, lost = 0.f;  // of the batches in range, compensated
+  double rest = 0.0;            // of the others
+
+  template <int DT>
+  __device__ __forceinline__ void add(const uint4 (&v)[4]) {
+    constexpr int N = Elem<DT>::kVec;
+    uint64_t s2 = 0, t2 = 0;
 #pragma unroll
-    for (int i = 0; i < N; i += 2) {
-      const uint64_t x2 = pack_f2(x[i], x[i + 1]);
-      s2 = ffma_f2(x2, x2, s2);
+    for (int u = 0; u < 4; ++u) {
+      float x[N];
+      Elem<DT>::unpack(v[u], x);
+#pragma unroll
+      for (int i = 0; i < N; i += 4) {
+        const uint64_t a = pack_f2(x[i], x[i + 1]), b = pack_f2(x[i + 2], x[i + 3]);
+        s2 = ffma_f2(a, a, s2);
+        t2 = ffma_f2(b, b, t2);
+      }
+    }
+    float a, b;
+    unpack_f2(fadd_f2(s2, t2), a, b);
+    const float s = a + b;
+    if (s >= 0x1p-100f && s <= 0x1p100f) {
+      const float y = s - lost, t = sum + y;
+      lost = (t - sum) - y;
+      sum = t;
+    } else {
+      rest += exact_squares<DT>(v[0], v[1], v[2], v[3]);
     }
   }
-  float a, b;
-  unpack_f2(s2, a, b);
-  const float s = a + b;
-  if (s >= 0x1p-120f && s < INFINITY) return s;
-  // overflow, NaN, or nothing but numbers below 2^-60, whose squares lose bits or are 0
-  uint32_t any = 0;
-  constexpr uint32_t kMagnitude = DT == 0 ? 0x7FFF7FFFu : 0x7FFFFFFFu;
-#pragma unroll
-  for (int u = 0; u < U; ++u) any |= (v[u].x | v[u].y | v[u].z | v[u].w) & kMagnitude;
-  double d = 0.0;
-  if (any == 0) return d;
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    float x[N];
-    Elem<DT>::unpack(v[u], x);
-#pragma unroll
-    for (int i = 0; i < N; ++i) d += static_cast<double>(x[i]) * x[i];
-  }
-  return d;
-}
+  __device__ __forceinline__ double total() const { return rest + (static_cast<double>(sum) - lost); }
+};
 
 __device__ __forceinline__ double block_total(double x, double* red) {  // in thread 0
 #pragma unroll
@@ -111,7 +135,7 @@ __device__ __forceinline__ double block_total(double x, double* red) {  // in th
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
   __syncthreads();
   if (threadIdx.x < 32) {
-    x = threadIdx.x < blockDim.x / 32 ? red[threadIdx.x] : 0.0;
+    x = threadIdx.x < kThreads / 32 ? red[threadIdx.x] : 0.0;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(kFull, x, o);
   }
@@ -119,30 +143,35 @@ __device__ __forceinline__ double block_total(double x, double* red) {  // in th
 }
 
 template <int DT>
-__device__ __forceinline__ void square_chunk(const Tensor& t, int chunk, double& sum) {
+__device__ __forceinline__ void square_chunk(const Tensor& t, int chunk, SquareAcc& acc) {
   const RowSpan<DT> x(t.in, 0, t.count);
   const int64_t v0 = static_cast<int64_t>(chunk) * kChunk + threadIdx.x;
-  uint4 v[4];
+  const uint4* body = x.body() + v0;
+  static_assert(kInFlight == 8, "two batches");
+  uint4 v[2][4];
 #pragma unroll
-  for (int u = 0; u < 4; ++u) v[u] = v0 + u * kThreads < x.nvec ? ld_stream(x.body() + v0 + u * kThreads) : make_uint4(0u, 0u, 0u, 0u);
+  for (int u = 0; u < kInFlight; ++u)
+    v[u / 4][u % 4] = v0 + u * kThreads < x.nvec ? ld_stream(body + u * kThreads) : make_uint4(0u, 0u, 0u, 0u);
   if (chunk == 0 && threadIdx.x < x.scalars()) {
     const double s = x.at(x.scalar_index(threadIdx.x));
-    sum += s * s;
+    acc.rest += s * s;
   }
-  sum += squares<DT>(v);
+  acc.template add<DT>(v[0]);
+  acc.template add<DT>(v[1]);
 }
 
 template <int CAP>
 __global__ void __launch_bounds__(kThreads, 4) grad_norm_kernel(const __grid_constant__ Tensors<CAP> p) {
   __shared__ double red[kThreads / 32];
+  allow_next();
   const int64_t b = blockIdx.x;
-  double sum = 0.0;
+  SquareAcc acc;
   each_chunk(p, static_cast<int>(b * p.chunks / gridDim.x), static_cast<int>((b + 1) * p.chunks / gridDim.x), false,
              [&](const Tensor& t, int chunk) {
-               if (t.dtype == SFC_BF16) square_chunk<0>(t, chunk, sum);
-               else square_chunk<1>(t, chunk, sum);
+               if (t.dtype == SFC_BF16) square_chunk<0>(t, chunk, acc);
+               else square_chunk<1>(t, chunk, acc);
              });
-  sum = block_total(sum, red);
+  const double sum = block_total(acc.total(), red);
   if (threadIdx.x == 0) p.partial[p.slot + b] = sum;
 }
 
@@ -159,68 +188,92 @@ __device__ __forceinline__ double total_norm(const double* partial, int slots) {
 }
 
 __global__ void __launch_bounds__(kThreads) finish_norm_kernel(const double* partial, int slots, float* norm) {
+  wait_for_last();
   const double n = total_norm(partial, slots);
   if (threadIdx.x == 0) *norm = static_cast<float>(n);
 }
 
-template <int N>
-__device__ __forceinline__ void store_elements(float* to, const float (&x)[N]) {
-  if (reinterpret_cast<uintptr_t>(to) % 16 == 0) {
-#pragma unroll
-    for (int i = 0; i < N; i += 4) __stcs(reinterpret_cast<float4*>(to + i), make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]));
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i) to[i] = x[i];
+// Eight elements at once: 16 bytes of bf16, 32 of f32 in one access, so that whichever side is wider, a warp's
+// instruction covers a run of memory without holes (bf16 to f32 in two stores of 16 bytes: 534 M elements 638 us).
+template <class T>
+struct Eight;
+template <>
+struct Eight<float> {
+  uint32_t w[8];
+  __device__ __forceinline__ void load(const float* from) {
+    // (not volatile: each address is loaded once, and stored only from what was loaded there)
+    asm("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+        : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+        : "l"(from));
   }
-}
-template <int N>
-__device__ __forceinline__ void store_elements(__nv_bfloat16* to, const float (&x)[N]) {
-  if (reinterpret_cast<uintptr_t>(to) % (2 * N) == 0) {
-    uint32_t w[N / 2];
+  __device__ __forceinline__ void unpack(float (&x)[8]) const {
 #pragma unroll
-    for (int i = 0; i < N / 2; ++i) {
-      const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-      w[i] = *reinterpret_cast<const uint32_t*>(&h);
-    }
-    if constexpr (N == 8) __stcs(reinterpret_cast<uint4*>(to), make_uint4(w[0], w[1], w[2], w[3]));
-    else __stcs(reinterpret_cast<uint2*>(to), make_uint2(w[0], w[1]));
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i) to[i] = __float2bfloat16_rn(x[i]);
+    for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(w[i]);
   }
-}
+  __device__ __forceinline__ static void store(float* to, const float (&x)[8]) {
+    asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(to), "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]),
+                 "f"(x[5]), "f"(x[6]), "f"(x[7])
+                 : "memory");
+  }
+};
+template <>
+struct Eight<__nv_bfloat16> {
+  uint4 v;
+  __device__ __forceinline__ void load(const __nv_bfloat16* from) { v = *reinterpret_cast<const uint4*>(from); }
+  __device__ __forceinline__ void unpack(float (&x)[8]) const { Elem<0>::unpack(v, x); }
+  __device__ __forceinline__ static void store(__nv_bfloat16* to, const float (&x)[8]) { *reinterpret_cast<uint4*>(to) = Out<0>::pack(x); }
+};
 
-template <int DT, class OutT>
+__device__ __forceinline__ void put(float* to, float x) { *to = x; }
+__device__ __forceinline__ void put(__nv_bfloat16* to, float x) { *to = __float2bfloat16_rn(x); }
+__device__ __forceinline__ float get(const float* from) { return *from; }
+__device__ __forceinline__ float get(const __nv_bfloat16* from) { return __bfloat162float(*from); }
+
+template <class InT, class OutT>
 __device__ __forceinline__ void scale_chunk(const Tensor& t, int chunk, float scale) {
-  constexpr int N = Elem<DT>::kVec;
-  const RowSpan<DT> x(t.in, 0, t.count);
+  constexpr int U = 64 / (8 * sizeof(InT));  // eights of a thread in flight: 64 bytes, half of its share
+  const InT* in = static_cast<const InT*>(t.in);
   OutT* out = static_cast<OutT*>(t.out);
-  const int64_t v0 = static_cast<int64_t>(chunk) * kChunk + threadIdx.x;
-  uint4 v[4];
-#pragma unroll
-  for (int u = 0; u < 4; ++u)
-    if (v0 + u * kThreads < x.nvec) v[u] = x.body()[v0 + u * kThreads];
-  if (chunk == 0 && threadIdx.x < x.scalars()) {
-    const int64_t i = x.scalar_index(threadIdx.x);
-    const float y[1] = {x.at(i) * scale};
-    if constexpr (sizeof(OutT) == 4) out[i] = y[0];
-    else out[i] = __float2bfloat16_rn(y[0]);
+  const int per = static_cast<int>(16 / sizeof(InT)) * kChunk;  // elements of a chunk
+  const int64_t first = static_cast<int64_t>(chunk) * per;
+  // elements before the first eight whose memory is aligned on both sides; where there is none, all go one by one
+  const int head = static_cast<int>((-reinterpret_cast<uintptr_t>(in) & (8 * sizeof(InT) - 1)) / sizeof(InT));
+  if ((reinterpret_cast<uintptr_t>(out + head) & (8 * sizeof(OutT) - 1)) != 0) {
+    const int64_t end = min(first + per, t.count);
+#pragma unroll 8
+    for (int64_t i = first + threadIdx.x; i < end; i += kThreads) put(out + i, get(in + i) * scale);
+    return;
   }
+  const int64_t eights = t.count > head ? (t.count - head) / 8 : 0;
+  int64_t k0 = first / 8 + threadIdx.x;
+  if (chunk == 0) {  // the scalars beside the eights
+    const int64_t tail = head + eights * 8, before = min(static_cast<int64_t>(head), t.count);
+    const int64_t i = threadIdx.x < before ? threadIdx.x : tail + (threadIdx.x - before);
+    if (i < t.count && (threadIdx.x < before || t.count > head)) put(out + i, get(in + i) * scale);
+  }
+#pragma unroll 1
+  for (int half = 0; half < 2; ++half, k0 += U * kThreads) {
+    Eight<InT> v[U];
 #pragma unroll
-  for (int u = 0; u < 4; ++u) {
-    const int64_t k = v0 + u * kThreads;
-    if (k >= x.nvec) break;
-    float y[N];
-    Elem<DT>::unpack(v[u], y);
+    for (int u = 0; u < U; ++u)
+      if (k0 + u * kThreads < eights) v[u].load(in + head + (k0 + u * kThreads) * 8);
 #pragma unroll
-    for (int i = 0; i < N; ++i) y[i] *= scale;
-    store_elements<N>(out + x.head + k * N, y);
+    for (int u = 0; u < U; ++u) {
+      if (k0 + u * kThreads >= eights) break;
+      float x[8];
+      v[u].unpack(x);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] *= scale;
+      Eight<OutT>::store(out + head + (k0 + u * kThreads) * 8, x);
+    }
   }
 }
 
-// The same runs of chunks backwards: what the norm's pass read last is still in L2.
+// The chunks backwards: what the norm's pass read last is still in L2. Three CTAs a SM: with four, the registers spill
+// (534 M elements f32 to bf16, both calls: 785 us, with four 1046; f32 to f32 954 : 1013; bf16 to f32 669 : 671).
 template <int CAP>
-__global__ void __launch_bounds__(kThreads, 2) clip_kernel(const __grid_constant__ Tensors<CAP> p) {
+__global__ void __launch_bounds__(kThreads, 3) clip_kernel(const __grid_constant__ Tensors<CAP> p) {
+  wait_for_last();
   const double norm = total_norm(p.partial, p.slots);
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.norm = static_cast<float>(norm);
   const double ratio = p.max_norm / (norm + 1e-6);
@@ -230,11 +283,11 @@ __global__ void __launch_bounds__(kThreads, 2) clip_kernel(const __grid_constant
              [&](const Tensor& t, int chunk) {
                if (scale == 1.f && t.in == t.out) return;  // in place: nothing to do
                if (t.dtype == SFC_BF16) {
-                 if (t.out_dtype == SFC_BF16) scale_chunk<0, __nv_bfloat16>(t, chunk, scale);
-                 else scale_chunk<0, float>(t, chunk, scale);
+                 if (t.out_dtype == SFC_BF16) scale_chunk<__nv_bfloat16, __nv_bfloat16>(t, chunk, scale);
+                 else scale_chunk<__nv_bfloat16, float>(t, chunk, scale);
                } else {
-                 if (t.out_dtype == SFC_BF16) scale_chunk<1, __nv_bfloat16>(t, chunk, scale);
-                 else scale_chunk<1, float>(t, chunk, scale);
+                 if (t.out_dtype == SFC_BF16) scale_chunk<float, __nv_bfloat16>(t, chunk, scale);
+                 else scale_chunk<float, float>(t, chunk, scale);
                }
              });
 }
@@ -249,8 +302,8 @@ struct List {
 };
 
 int64_t chunks_of(const List& l, int64_t i) {
-  const int64_t vectors = l.counts[i] / (l.dtypes[i] == SFC_BF16 ? 8 : 4);  // not fewer than its body has
-  return l.counts[i] > 0 ? std::max<int64_t>(1, (vectors + kChunk - 1) / kChunk) : 0;
+  const int64_t per = kChunk * (l.dtypes[i] == SFC_BF16 ? 8 : 4);
+  return (l.counts[i] + per - 1) / per;
 }
 
 // The table of one launch over the tensors from i: as many as fit, those without elements left out. Returns the next.
@@ -268,8 +321,23 @@ int64_t fill(const List& l, int64_t i, Tensors<CAP>& p) {
 }
 
 template <int CAP>
-unsigned ctas(const Tensors<CAP>& p) {
-  return static_cast<unsigned>(std::min(p.chunks, kCtas));
+unsigned ctas(const Tensors<CAP>& p, int most) {
+  return static_cast<unsigned>(std::min(p.chunks, most));
+}
+
+// Behind the launch before it, which it may overtake up to its wait.
+template <class P, class... Args>
+cudaError_t launch_behind(void (*kernel)(P, Args...), unsigned grid, cudaStream_t stream, const P& p, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p, args...);
 }
 
 template <int CAP>
@@ -283,20 +351,16 @@ cudaError_t run(const List& l, float max_norm, float* norm, double* partial, cud
     i = fill(l, i, p);
     if (p.n == 0) break;
     p.slot = p.slots;
-    p.slots += static_cast<int32_t>(ctas(p));
-    grad_norm_kernel<CAP><<<ctas(p), kThreads, 0, stream>>>(p);
+    p.slots += static_cast<int32_t>(ctas(p, kCtas));
+    grad_norm_kernel<CAP><<<ctas(p, kCtas), kThreads, 0, stream>>>(p);
     const cudaError_t err = cudaGetLastError();
     if (err != cudaSuccess) return err;
   }
-  if (!l.out || p.slots == 0) {
-    finish_norm_kernel<<<1, kThreads, 0, stream>>>(partial, p.slots, norm);
-    return cudaGetLastError();
-  }
+  if (!l.out || p.slots == 0) return launch_behind(finish_norm_kernel, 1, stream, static_cast<const double*>(partial), p.slots, norm);
   for (int64_t i = 0; i < l.n;) {
     i = fill(l, i, p);
     if (p.n == 0) break;
-    clip_kernel<CAP><<<ctas(p), kThreads, 0, stream>>>(p);
-    const cudaError_t err = cudaGetLastError();
+    const cudaError_t err = launch_behind(clip_kernel<CAP>, ctas(p, kClipCtas), stream, p);
     if (err != cudaSuccess) return err;
   }
   return cudaSuccess;

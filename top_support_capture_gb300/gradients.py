@@ -3,13 +3,18 @@
 Like the rest of the binding this only checks and marshals arguments (include/sfc.h has the formulas)."""
 from __future__ import annotations
 
-import ctypes
+from array import array
+from operator import attrgetter
 
 import torch
 from torch.autograd import forward_ad
 
-from . import SFC_OK, SfcError, _dtype_code, _enter, load_library
+from . import SFC_BF16, SFC_F32, SFC_OK, SfcError, _dtype_code, _enter, load_library
 from .training import _raise
+
+_CODES = {torch.bfloat16: SFC_BF16, torch.float32: SFC_F32}
+_dtype, _requires_grad = attrgetter("dtype"), attrgetter("requires_grad")
+_Tensor = torch.Tensor
 
 
 def _dense(t):
@@ -27,11 +32,23 @@ def check_tensors(name, tensors):
     tensors = [t for t in ([tensors] if isinstance(tensors, torch.Tensor) else tensors) if t is not None]
     if not tensors:
         raise SfcError(f"{name} holds no tensor")
-    device = tensors[0].device
-    if device.type != "cuda":
-        raise SfcError(f"{name} must be CUDA tensors, got {device}")
-    check_layouts(name, tensors, device)
+    if not _all_plain(tensors):
+        device = tensors[0].device
+        if device.type != "cuda":
+            raise SfcError(f"{name} must be CUDA tensors, got {device}")
+        check_layouts(name, tensors, device)
     return tensors
+
+
+def _all_plain(tensors):
+    """Whether there is nothing to look at one by one. The calls over many small tensors take as long as their Python: what
+    is asked of every tensor is asked by one map."""
+    try:
+        devices = set(map(_Tensor.get_device, tensors))
+        return (len(devices) == 1 and devices.pop() >= 0 and all(map(_Tensor.is_contiguous, tensors))
+                and not (torch.is_grad_enabled() and any(map(_requires_grad, tensors))) and getattr(forward_ad, "_current_level", 0) < 0)
+    except RuntimeError:  # (a tensor without strides)
+        return False
 
 
 def check_layouts(name, tensors, device):
@@ -50,9 +67,14 @@ def check_layouts(name, tensors, device):
 
 
 def _arrays(tensors):
-    n = len(tensors)
-    return ((ctypes.c_void_p * n)(*[t.data_ptr() for t in tensors]), (ctypes.c_int64 * n)(*[t.numel() for t in tensors]),
-            (ctypes.c_int32 * n)(*[_dtype_code(t) for t in tensors]))
+    """(addresses, counts, dtype codes) as the library reads them."""
+    try:
+        codes = array("i", map(_CODES.__getitem__, map(_dtype, tensors)))
+    except KeyError:
+        for t in tensors:
+            _dtype_code(t)
+        raise
+    return array("Q", map(_Tensor.data_ptr, tensors)), array("q", map(_Tensor.numel, tensors)), codes
 
 
 def grad_norm(grads, stream=None):
@@ -86,23 +108,20 @@ def check_out(grads, out):
 
 def _run(grads, out, max_norm, stream):
     lib, dev, n = load_library(), grads[0].device, len(grads)
-    addresses, counts, dtypes = _arrays(grads)
+    lists = _arrays(grads)
+    to = () if out is None else lists[::2] if out is grads else _arrays(out)[::2]
     stream, context = _enter(dev, stream, *grads, *(out if out is not None and out is not grads else ()))
     with context:
+        nbytes = lib.sfc_grad_norm_workspace_size(n)
         norm = torch.empty((), dtype=torch.float32, device=dev)
         # the CTAs' sums: memory of this call alone, so calls and captured graphs that run side by side share none
-        nbytes = lib.sfc_grad_norm_workspace_size(n)
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-        if out is None:
-            rc = lib.sfc_grad_norm(addresses, counts, dtypes, n, norm.data_ptr(), workspace.data_ptr(), nbytes, stream)
-        else:
-            to, _, to_dtypes = (addresses, counts, dtypes) if out is grads else _arrays(out)
-            rc = lib.sfc_clip_grad_norm(addresses, counts, dtypes, n, max_norm, to, to_dtypes, norm.data_ptr(), workspace.data_ptr(),
-                                        nbytes, stream)
+        address = lambda a: a.buffer_info()[0]  # (the arrays live until the call is over)
+        tail = norm.data_ptr(), workspace.data_ptr(), nbytes, stream
+        rc = (lib.sfc_grad_norm(*map(address, lists), n, *tail) if out is None else
+              lib.sfc_clip_grad_norm(*map(address, lists), n, max_norm, *map(address, to), *tail))
     if rc != SFC_OK:
         _raise("sfc_grad_norm" if out is None else "sfc_clip_grad_norm (tensors that overlap?)", rc)
     if out is not None:  # autograd's view of what was written
-        for t in out:
-            if not t.is_inference():
-                torch.autograd.graph.increment_version(t)
+        torch.autograd.graph.increment_version(out)
     return norm
