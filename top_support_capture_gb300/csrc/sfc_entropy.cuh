@@ -59,16 +59,19 @@ struct EntropyAcc {
     Elem<DT>::unpack(v, x);
     add_below(x, c);
   }
-  // U vectors; bf16: one maximum of all of them (see SoftmaxAcc::add).
+  // U vectors; bf16: one maximum of all of them (see SoftmaxAcc::add). Returns their maximum.
   template <int DT, int U>
-  __device__ __forceinline__ void add(const uint4 (&v)[U], float c) {
+  __device__ __forceinline__ float add(const uint4 (&v)[U], float c) {
     constexpr int G = DT == 0 ? U : 1;
+    float most = -FLT_MAX;
 #pragma unroll
     for (int g = 0; g < U; g += G) {
       uint4 top = v[g];
 #pragma unroll
       for (int u = 1; u < G; ++u) top = larger<DT>(top, v[g + u]);
-      raise(Elem<DT>::vmax(top), c);
+      const float x_top = Elem<DT>::vmax(top);
+      most = fmaxf(most, x_top);
+      raise(x_top, c);
 #pragma unroll
       for (int u = 0; u < G; ++u) {
         float x[Elem<DT>::kVec];
@@ -76,6 +79,7 @@ struct EntropyAcc {
         add_below(x, c);
       }
     }
+    return most;
   }
 };
 

@@ -106,6 +106,7 @@ __global__ void __launch_bounds__(NT, MINB) policy_kernel(const __grid_constant_
         dsmem_st64(to, pack_f2(all.m, all.s));
         dsmem_st32(to + 8, __float_as_uint(all.w));
       }
+      __syncwarp();  // the barrier's halves want whole warps
       cluster_sync_all();
       late = __any_sync(kFull, table[lane < S ? lane : 0].y == kLate);
       all = merge_shared(table, S, c);
@@ -203,8 +204,14 @@ cudaError_t choose(PolicyParams& p, int64_t B, cudaStream_t stream) {
     p.slices = static_cast<int32_t>(std::min<int64_t>(S, kMaxSlices));
     return S <= kMaxSlices;
   };
-  // few rows: enough slices to fill the GPU's 304 CTA slots, of at least two vectors per thread
-  const int64_t fill = std::min<int64_t>({kMaxSlices, cut(1024), (304 + B - 1) / B});
+  // rows that one CTA holds, enough of them to fill the GPU: the smaller the CTA the more of them take turns on a SM
+  if (B >= 304) {
+    if (vectors <= kKeepBytes / 8 / 16 - 8 && fits(1)) return start<DT, 128, 8, true>(p, B, stream);
+    if (vectors <= kKeepBytes / 4 / 16 - 8 && fits(1)) return start<DT, 256, 4, true>(p, B, stream);
+    if (vectors <= kKeepBytes / 3 / 16 - 8 && fits(1)) return start<DT, 384, 3, true>(p, B, stream);
+  }
+  // few rows: slices for the GPU's 304 CTA slots, of at least two vectors per thread
+  const int64_t fill = std::max<int64_t>(1, std::min<int64_t>({kMaxSlices, vectors / 1024, 304 / B}));
   // a slice, in whole 128-byte lines, within its CTA's shared memory
   if (fits(std::max(fill, cut(kKeepBytes / 2 / 16 - 8)))) return start<DT, 512, 2, true>(p, B, stream);
   if (fits(cut(kKeepBytes / 16 - 8))) return start<DT, 1024, 1, true>(p, B, stream);

@@ -4,15 +4,15 @@
 // The forward call reads the logits once. A row is cut into slices of 16-byte vectors, one CTA each, which form a cluster
 // and exchange their statistics through distributed shared memory, merged in slice order.
 //
-// Top alternatives without a second pass: each thread already keeps the maximum of what it has seen. The K-th largest of
-// the maxima of K or more disjoint groups of threads is a lower bound on the K-th largest logit, since each group has an
-// element at least that large, and a tight one: with 128 groups of randomly spread logits about K + K^2 / 256 elements
-// reach it. Only the threads whose own maximum reaches the bound have such elements; their warps read those threads'
-// vectors again (from L2) and put what reaches the bound into a pool in shared memory, from which the K largest are
-// ranked by counting. Of S slices each gives two bounds, the largest of the slices' K-th and the smallest of their
-// ceil(K / S)-th; the larger one holds for the row. Where ties or a regular pattern overfill the pool, the row's first CTA
-// finds the K largest one by one instead (every thread holds its best, the winner's warp looks for its next): exact for
-// any row.
+// Top alternatives without a second pass: each thread already knows the maximum of what it has seen, and keeps those of its
+// cells (32 elements or more) in shared memory. The K-th largest of the maxima of K or more disjoint groups of threads is a
+// lower bound on the K-th largest logit, since each group has an element at least that large, and a tight one: with 128
+// groups of randomly spread logits about K + K^2 / 256 elements reach it. Only the cells whose maximum reaches the bound
+// have such elements: their vectors are read again (from L2, all at once over their warp's lanes), and what reaches the
+// bound goes into a pool in shared memory, from which the K largest are ranked by counting. Of S slices each gives two
+// bounds, the largest of the slices' K-th and the smallest of their ceil(K / S)-th; the larger one holds for the row. Where
+// ties or a regular pattern overfill the pool or a warp's list of cells, the row's first CTA finds the K largest one by one
+// instead (every thread holds its best, the winner's warp looks for its next): exact for any row.
 #include <algorithm>
 #include <climits>
 #include <cstdint>
@@ -27,6 +27,8 @@ namespace {
 constexpr int kMaxSlices = 8;  // the portable cluster size
 constexpr int kGroups = 128;   // of threads; not fewer than SFC_MAX_TOP, not more than the smallest CTA
 constexpr uint32_t kPool = 1024;
+constexpr int kListed = 64;  // cells of a warp
+constexpr int kCells = 24, kCellBytes = 32768;  // most of a thread, of a CTA
 static_assert(SFC_MAX_TOP <= kGroups && SFC_MAX_GIVEN <= kGroups, "");
 
 struct ScoreParams {
@@ -42,11 +44,12 @@ struct ScoreParams {
   float4* stats;  // (m, s, H, 0) for the gradient, or null
   int32_t* row_status;
   int32_t slices, per;  // CTAs a row, vectors a slice
+  int32_t shift;        // a cell holds 2^shift batches of a thread
 };
 
-__device__ __forceinline__ uint32_t dsmem_count(uint32_t addr) {  // the counter's old value
+__device__ __forceinline__ uint32_t dsmem_add(uint32_t addr, uint32_t n) {  // the counter's old value
   uint32_t v;
-  asm volatile("atom.relaxed.cluster.shared::cluster.add.u32 %0, [%1], 1;" : "=r"(v) : "r"(addr) : "memory");
+  asm volatile("atom.relaxed.cluster.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(v) : "r"(addr), "r"(n) : "memory");
   return v;
 }
 
@@ -84,10 +87,12 @@ __global__ void __launch_bounds__(NT, MINB) score_kernel(const __grid_constant__
   constexpr int U = 4;  // vectors in flight per thread (and as many again)
   __shared__ float4 red[NW];
   __shared__ float4 table[kMaxSlices];   // (m, s, w) of the slices
-  __shared__ float2 bounds[kMaxSlices];  // their K-th and ceil(K / S)-th group maxima
-  __shared__ float tops[NT], groups[kGroups], cut[2];
+  __shared__ float2 bounds[kMaxSlices];  // of the slices' K-th and ceil(K / S)-th group maxima
+  __shared__ __align__(16) uint32_t groups[kGroups];  // keys of the groups' maxima, made different by their low bits
+  __shared__ float cut[2];
   __shared__ uint64_t pool[kPool], winners[NW];
-  __shared__ uint32_t count;
+  __shared__ uint32_t list[NW][kListed], count;
+  extern __shared__ float cells[];  // [cell][thread], where there are alternatives
   const int tid = threadIdx.x, lane = tid & 31, wp = tid >> 5, S = p.slices, rank = blockIdx.y, K = p.K;
   const int64_t r = blockIdx.x;
   const RowSpan<DT> row(p.logits, r * p.row_stride, p.V);
@@ -103,41 +108,57 @@ __global__ void __launch_bounds__(NT, MINB) score_kernel(const __grid_constant__
   if (tid == 0) count = 0;
   const float c = exponent_scale(T);
   EntropyAcc a;
-  stream.batches([&](const uint4(&v)[U]) { a.template add<DT, U>(v, c); });
+  int batches = 0;
+  const int of_cell = (1 << p.shift) - 1;
+  float cell = -FLT_MAX;
+  stream.batches([&](const uint4(&v)[U]) {
+    cell = fmaxf(cell, a.template add<DT, U>(v, c));
+    if (K > 0 && (batches & of_cell) == of_cell) {
+      cells[(batches >> p.shift) * NT + tid] = cell;
+      cell = -FLT_MAX;
+    }
+    ++batches;
+  });
+  if (K > 0 && (batches & of_cell) != 0) cells[(batches >> p.shift) * NT + tid] = cell;
   if (scalar) a.add(xs, c);
   const EntropyStats mine = merge_lanes(a, c);
   if (lane == 0) red[wp] = make_float4(mine.m, mine.s, mine.w, 0.f);
-  tops[tid] = a.m;
+  constexpr int Q = NT / kGroups;  // neighbouring threads of a group
+  if (K > 0) {
+    float g = a.m;
+#pragma unroll
+    for (int o = Q / 2; o > 0; o >>= 1) g = fmaxf(g, __shfl_xor_sync(kFull, g, o));
+    if (tid % Q == 0) groups[tid / Q] = (Keys<DT>::key(g) & ~(kGroups - 1u)) | (tid / Q);
+  }
   const bool wrong = __syncthreads_or(token < -1 || token >= p.V) || !temperature_valid(T);
   EntropyStats all = merge_shared(red, NW, c);
-  float bound = -FLT_MAX;
-  if (K > 0) {
-    if (tid < kGroups) {
-      float g = tops[tid];
+  float2 own = make_float2(-FLT_MAX, -FLT_MAX);
+  if (K > 0) {  // the group below K - 1 others has the K-th largest maximum; each of a group's threads compares a share
+    const uint32_t key = groups[tid / Q];
+    int above = 0;
 #pragma unroll
-      for (int i = kGroups; i < NT; i += kGroups) g = fmaxf(g, tops[tid + i]);
-      groups[tid] = g;
+    for (int i = 0; i < kGroups / 4 / Q; ++i) {
+      const uint4 k = reinterpret_cast<const uint4*>(groups)[i * Q + tid % Q];
+      above += (k.x > key) + (k.y > key) + (k.z > key) + (k.w > key);
     }
+#pragma unroll
+    for (int o = Q / 2; o > 0; o >>= 1) above += __shfl_xor_sync(kFull, above, o);
+    const float value = Keys<DT>::value(key & ~(kGroups - 1u));
+    if (above == K - 1) cut[0] = value;
+    if (above == (K + S - 1) / S - 1) cut[1] = value;
     __syncthreads();
-    if (tid < kGroups) {
-      const float g = groups[tid];
-      int larger = 0;
-#pragma unroll 8
-      for (int i = 0; i < kGroups; ++i) larger += groups[i] > g || (groups[i] == g && i < tid);
-      if (larger == K - 1) cut[0] = g;
-      if (larger == (K + S - 1) / S - 1) cut[1] = g;
-    }
-    __syncthreads();
-    bound = cut[0];
+    own = make_float2(cut[0], cut[1]);
   }
+  float bound = own.x;
   if (S > 1) {
     cluster_wait();
     if (tid < S) {
       const uint32_t to = dsmem_addr(&table[rank], tid);
       dsmem_st64(to, pack_f2(all.m, all.s));
       dsmem_st32(to + 8, __float_as_uint(all.w));
-      if (K > 0) dsmem_st64(dsmem_addr(&bounds[rank], tid), pack_f2(cut[0], cut[1]));
+      dsmem_st64(dsmem_addr(&bounds[rank], tid), pack_f2(own.x, own.y));
     }
+    __syncwarp();  // the barrier's halves want whole warps
     cluster_sync_all();
     all = merge_shared(table, S, c);
     if (K > 0) {
@@ -151,64 +172,55 @@ __global__ void __launch_bounds__(NT, MINB) score_kernel(const __grid_constant__
     }
   }
   const bool valid = stats_valid(all.m, all.s);  // uniform over the cluster
-  uint32_t n = 0;  // keys in the pool of rank 0
   if (K > 0 && valid) {
     const uint32_t counter = S > 1 ? dsmem_addr(&count, 0) : smem_addr(&count);
     const uint32_t places = S > 1 ? dsmem_addr(pool, 0) : smem_addr(pool);
-    auto push = [&](float x, int64_t id) {
-      const uint32_t at = dsmem_count(counter);
+    auto add = [&](uint32_t n) { return S > 1 ? dsmem_add(counter, n) : atomicAdd(&count, n); };
+    auto place = [&](uint32_t at, float x, int64_t id) {
       if (at < kPool) dsmem_st64(places + at * 8, ckey_of<DT>(x, id));
     };
-    for (unsigned who = __ballot_sync(kFull, a.m >= bound); who; who &= who - 1) {
-      const int src = wp * 32 + __ffs(who) - 1;
-      for (int k = v0 + src + lane * NT; k < v1; k += 32 * NT) {
-        const uint4 v = __ldg(row.body() + k);
-        if (Elem<DT>::vmax(v) < bound) continue;
-        float x[VEC];
-        Elem<DT>::unpack(v, x);
+    // the warp's cells that reach the bound, then their vectors, one for each lane
+    int listed = 0;
+    if (__any_sync(kFull, a.m >= bound)) {
+      for (int i = 0; i << p.shift < batches; ++i) {
+        const bool in = cells[i * NT + tid] >= bound;
+        const unsigned who = __ballot_sync(kFull, in);
+        const int at = listed + __popc(who & ((1u << lane) - 1));
+        if (in && at < kListed) list[wp][at] = i * NT + tid;
+        listed += __popc(who);
+      }
+      __syncwarp();
+    }
+    if (listed > kListed) {
+      if (lane == 0) add(kPool + 1);
+      listed = 0;
+    }
+    const int vectors = listed << (p.shift + 2);
+    static_assert(U == 4, "vectors of a batch");
+    for (int i = lane; i - lane < vectors; i += 32) {
+      const int of = list[wp][min(i, vectors - 1) >> (p.shift + 2)];
+      const int at = v0 + of % NT + ((of / NT << (p.shift + 2)) + (i & ((4 << p.shift) - 1))) * NT;
+      const uint4 v = i < vectors && at < v1 ? __ldg(row.body() + at) : Elem<DT>::neg_inf_vec();
+      uint32_t in = Elem<DT>::ge_mask(v, bound);
+      const int n = __popc(in);
+      int upto = n;  // of the lanes up to this one
 #pragma unroll
-        for (int e = 0; e < VEC; ++e)
-          if (x[e] >= bound) push(x[e], row.head + static_cast<int64_t>(k) * VEC + e);
+      for (int o = 1; o < 32; o *= 2) {
+        const int before = __shfl_up_sync(kFull, upto, o);
+        if (lane >= o) upto += before;
+      }
+      uint32_t to = 0;
+      if (lane == 31 && upto > 0) to = add(upto);
+      to = __shfl_sync(kFull, to, 31) + upto - n;
+      for (; in; in &= in - 1) {
+        const int e = __ffs(in) - 1;
+        place(to++, Elem<DT>::get_dyn(v, e), row.head + static_cast<int64_t>(at) * VEC + e);
       }
     }
-    if (scalar && xs >= bound) push(xs, row.scalar_index(tid));
+    if (scalar && xs >= bound) place(add(1), xs, row.scalar_index(tid));
+    __syncwarp();
     if (S > 1) cluster_sync_all();  // no CTA touches another's memory after it
     else __syncthreads();
-  }
-  if (rank != 0) return;
-  if (K > 0 && valid) {
-    n = count;
-    if (n > kPool) {
-      n = static_cast<uint32_t>(K);
-      auto next = [&](int of, uint64_t limit) {  // the largest key of thread `of` (of the whole row's) below the limit, by its warp
-        uint64_t key = best_below<DT>(row, of + lane * NT, 32 * NT, nvec, limit);
-        if (scalar && tid == of) {
-          const uint64_t k = ckey_of<DT>(xs, row.scalar_index(tid));
-          if (k < limit && k > key) key = k;
-        }
-        return warp_max_key(key);
-      };
-      uint64_t best = 0;
-      for (int l = 0; l < 32; ++l) {
-        const uint64_t k = next(wp * 32 + l, ~0ull);
-        if (lane == l) best = k;
-      }
-      for (int j = 0; j < K; ++j) {
-        const uint64_t w = warp_max_key(best);
-        if (lane == 0) winners[wp] = w;
-        __syncthreads();
-        uint64_t top = winners[0];
-#pragma unroll
-        for (int i = 1; i < NW; ++i) top = max(top, winners[i]);
-        __syncthreads();
-        if (tid == 0) pool[j] = top;
-        if (top != 0 && w == top) {  // the winner's warp: uniform
-          const int l = __ffs(__ballot_sync(kFull, best == top)) - 1;
-          const uint64_t k = next(wp * 32 + l, top);
-          if (lane == l) best = k;
-        }
-      }
-    }
   }
   if (rank != 0) return;
   const bool ok = valid && !wrong;
@@ -222,20 +234,51 @@ __global__ void __launch_bounds__(NT, MINB) score_kernel(const __grid_constant__
     if (p.stats) p.stats[r] = make_float4(ok ? all.m : nan, all.s, H, 0.f);
   }
   if (K == 0) return;
-  if (tid < K) {  // places without an alternative
-    p.top_ids[r * K + tid] = -1;
-    p.top_logprobs[r * K + tid] = ok ? -INFINITY : nan;
+  auto put = [&](int j, uint64_t key) {  // 0: no alternative in this place
+    p.top_ids[r * K + j] = key ? static_cast<int32_t>(ckey_id(key)) : -1;
+    p.top_logprobs[r * K + j] = key ? logprob(Keys<DT>::value(ckey_key(key))) : ok ? -INFINITY : nan;
+  };
+  const int n = ok ? count : 0;
+  if (n <= static_cast<int>(kPool)) {
+    if (tid < K && tid >= n) put(tid, 0ull);
+    for (int i0 = 0; i0 < n; i0 += NT / 4) {  // four lanes count the keys above one
+      const int i = i0 + tid / 4;
+      const uint64_t key = pool[min(i, n - 1)];
+      int above = 0;
+      for (int j = tid & 3; j < n; j += 4) above += pool[j] > key;
+      above += __shfl_xor_sync(kFull, above, 1);
+      above += __shfl_xor_sync(kFull, above, 2);
+      if (i < n && above < K && (tid & 3) == 0) put(above, key);
+    }
+    return;
   }
-  __syncthreads();  // before the others are written
-  if (!ok) return;
-  for (uint32_t i = tid; i < n; i += NT) {
-    const uint64_t key = pool[i];
-    if (key == 0) continue;
-    int above = 0;
-    for (uint32_t j = 0; j < n; ++j) above += pool[j] > key;
-    if (above >= K) continue;
-    p.top_ids[r * K + above] = static_cast<int32_t>(ckey_id(key));
-    p.top_logprobs[r * K + above] = logprob(Keys<DT>::value(ckey_key(key)));
+  auto next = [&](int of, uint64_t limit) {  // the largest key of thread `of` (of the whole row's) below the limit, by its warp
+    uint64_t key = best_below<DT>(row, of + lane * NT, 32 * NT, nvec, limit);
+    if (scalar && tid == of) {
+      const uint64_t k = ckey_of<DT>(xs, row.scalar_index(tid));
+      if (k < limit && k > key) key = k;
+    }
+    return warp_max_key(key);
+  };
+  uint64_t best = 0;
+  for (int l = 0; l < 32; ++l) {
+    const uint64_t k = next(wp * 32 + l, ~0ull);
+    if (lane == l) best = k;
+  }
+  for (int j = 0; j < K; ++j) {
+    const uint64_t w = warp_max_key(best);
+    if (lane == 0) winners[wp] = w;
+    __syncthreads();
+    uint64_t top = winners[0];
+#pragma unroll
+    for (int i = 1; i < NW; ++i) top = max(top, winners[i]);
+    __syncthreads();
+    if (tid == 0) put(j, top);
+    if (top != 0 && w == top) {  // the winner's warp: uniform
+      const int l = __ffs(__ballot_sync(kFull, best == top)) - 1;
+      const uint64_t k = next(wp * 32 + l, top);
+      if (lane == l) best = k;
+    }
   }
 }
 
@@ -331,6 +374,12 @@ template <int DT, int NT, int MINB>
 cudaError_t start(ScoreParams p, int64_t B, cudaStream_t stream) {
   p.per = slice_of(p.V / Elem<DT>::kVec, p.slices);
   cudaLaunchConfig_t cfg = {};
+  p.shift = DT == 0 ? 0 : 1;  // cells of 32 elements, larger where a thread has too many
+  if (p.K > 0) {
+    const int most = std::min(kCells, kCellBytes / 4 / NT), batches = (p.per + 4 * NT - 1) / (4 * NT);
+    while ((batches >> p.shift) + 1 > most) ++p.shift;
+    cfg.dynamicSmemBytes = static_cast<size_t>((batches >> p.shift) + 1) * NT * sizeof(float);
+  }
   cfg.gridDim = dim3(static_cast<unsigned>(B), static_cast<unsigned>(p.slices));
   cfg.blockDim = dim3(NT);
   cfg.stream = stream;
@@ -345,19 +394,35 @@ cudaError_t start(ScoreParams p, int64_t B, cudaStream_t stream) {
 template <int DT>
 cudaError_t choose(ScoreParams& p, int64_t B, cudaStream_t stream) {
   const int64_t vectors = p.V / Elem<DT>::kVec;
-  // few rows: enough slices to fill the GPU's 304 CTA slots, of at least two vectors per thread
-  p.slices = static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>({kMaxSlices, (vectors + 1023) / 1024, (304 + B - 1) / B})));
-  if (B * p.slices > 152) return start<DT, 256, 4>(p, B, stream);
+  // Few rows: slices for every SM (two or four or eight: clusters of other sizes leave SMs out; 24 x 151936 bf16 with six 6.3
+  // us, four 5.7), and CTAs as large as keeps some vectors for each thread (1 x 151936: of 256 4.0 us, of 512 4.4; 64 x 151936
+  // 10.4 : 7.9). Many rows: one CTA each, of a size of which several take turns on a SM (2048 x 32000: of 128 25.7 us, of
+  // 256 26.4, of 512 32.8; 2048 x 151936 103.9, 100.6, 108.1). Groups of a CTA's threads need vectors to look at: rows
+  // below 1024 have CTAs of 128.
+  p.slices = 1;
+  while (p.slices < kMaxSlices && 2 * p.slices * B <= 152 && vectors >= 4096 * p.slices) p.slices *= 2;
+  if (B > 304) return vectors <= 7000 ? start<DT, 128, 8>(p, B, stream) : start<DT, 256, 4>(p, B, stream);
+  if (vectors <= 1024) return start<DT, 128, 8>(p, B, stream);
+  if (vectors / p.slices <= 3200) return start<DT, 256, 4>(p, B, stream);
   return start<DT, 512, 2>(p, B, stream);
 }
 
-template <int DT>
-cudaError_t start_backward(ScoreGradParams p, int64_t B, cudaStream_t stream) {
-  const int64_t vectors = p.V / Elem<DT>::kVec;
-  const int64_t slices = std::max<int64_t>(1, std::max((vectors + 20479) / 20480, std::min<int64_t>({8, (vectors + 1023) / 1024, (304 + B - 1) / B})));
-  p.per = slice_of(vectors, slices);
-  score_backward_kernel<DT, 512, 2><<<dim3(static_cast<unsigned>(B), static_cast<unsigned>(slices)), 512, 0, stream>>>(p);
+template <int DT, int NT, int MINB>
+cudaError_t start_backward(ScoreGradParams p, int64_t B, int64_t slices, cudaStream_t stream) {
+  p.per = slice_of(p.V / Elem<DT>::kVec, slices);
+  score_backward_kernel<DT, NT, MINB><<<dim3(static_cast<unsigned>(B), static_cast<unsigned>(slices)), NT, 0, stream>>>(p);
   return cudaGetLastError();
+}
+
+template <int DT>
+cudaError_t choose_backward(const ScoreGradParams& p, int64_t B, cudaStream_t stream) {
+  const int64_t vectors = p.V / Elem<DT>::kVec;
+  // many short rows: several small CTAs take turns on a SM
+  if (B >= 304 && vectors <= 1656) return start_backward<DT, 128, 8>(p, B, 1, stream);
+  if (B >= 304 && vectors <= 3320) return start_backward<DT, 256, 4>(p, B, 1, stream);
+  // slices of 320 KB at most; few rows: enough to fill the GPU's 304 CTA slots, of at least two vectors per thread
+  const int64_t fill = std::min<int64_t>({8, (vectors + 1023) / 1024, (304 + B - 1) / B});
+  return start_backward<DT, 512, 2>(p, B, std::max<int64_t>({1, (vectors + 20479) / 20480, fill}), stream);
 }
 
 int result(cudaError_t err) {
@@ -379,7 +444,7 @@ extern "C" int sfc_token_logprobs(const void* logits, int dtype, int64_t B, int6
   if (top < 0 || top > SFC_MAX_TOP || (top > 0 && (!top_ids || !top_logprobs))) return SFC_EINVAL;
   if (!entropy || !row_status || reinterpret_cast<uintptr_t>(row_stats) % 16) return SFC_EINVAL;
   sfc::ScoreParams p{logits, row_stride, V, temperature, tokens, M, top, logprobs, entropy, top_ids, top_logprobs,
-                     reinterpret_cast<float4*>(row_stats), row_status, 1, 0};
+                     reinterpret_cast<float4*>(row_stats), row_status, 1, 0, 0};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return sfc::result(dtype == SFC_BF16 ? sfc::choose<0>(p, B, st) : sfc::choose<1>(p, B, st));
 }
@@ -398,5 +463,5 @@ extern "C" int sfc_token_logprobs_backward(const void* logits, int dtype, int64_
   const sfc::ScoreGradParams p{logits, row_stride, V, temperature, tokens, M, reinterpret_cast<const float4*>(row_stats), grad_logprobs,
                                grad_entropy, static_cast<unsigned char*>(grad_logits), grad_stride, 0};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return sfc::result(dtype == SFC_BF16 ? sfc::start_backward<0>(p, B, st) : sfc::start_backward<1>(p, B, st));
+  return sfc::result(dtype == SFC_BF16 ? sfc::choose_backward<0>(p, B, st) : sfc::choose_backward<1>(p, B, st));
 }
