@@ -83,11 +83,69 @@ struct EntropyAcc {
   }
 };
 
+// The sums of vectors whose logits are known to be near: |x c| <= kNear for all of them, and none above m. The exponent is one
+// fused step then, d' = x c - M with M = m c rounded: against another reference, which `finish` takes out again, and every
+// d' is a number, so that none is held.
+constexpr float kNear = 1e18f;
+
+struct NearAcc {
+  uint64_t c2, minus_M2, s2 = 0, w2 = 0;
+
+  __device__ __forceinline__ NearAcc(float m, float c) : c2(pack_f2(c, c)), minus_M2(pack_f2(-(m * c), -(m * c))) {}
+  template <int DT>
+  __device__ __forceinline__ void add(const uint4& v) {
+    constexpr int N = Elem<DT>::kVec;
+    float x[N];
+    Elem<DT>::unpack(v, x);
+    uint64_t e[N / 2];
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+      const uint64_t d = ffma_f2(pack_f2(x[2 * i], x[2 * i + 1]), c2, minus_M2);
+      float a, b;
+      unpack_f2(d, a, b);
+      e[i] = pack_f2(ex2_approx(a), ex2_approx(b));
+      w2 = ffma_f2(e[i], d, w2);
+    }
+#pragma unroll
+    for (int w = N / 4; w > 0; w /= 2)  // a fixed tree
+#pragma unroll
+      for (int i = 0; i < w; ++i) e[i] = fadd_f2(e[i], e[i + w]);
+    s2 = fadd_f2(s2, e[0]);
+  }
+  __device__ __forceinline__ void finish(EntropyAcc& a, float m, float c) const {  // a has seen nothing before
+    const float rho = fmaf(m, c, -(m * c)), f = ex2_approx(-rho);
+    a.m = m;
+    a.s2 = fmul_f2(s2, pack_f2(f, f));
+    a.w2 = fmul_f2(ffma_f2(pack_f2(-rho, -rho), s2, w2), pack_f2(f, f));
+  }
+};
+
+template <int DT>
+__device__ __forceinline__ uint4 smaller(const uint4& a, const uint4& b) {  // element by element
+  auto word = [](uint32_t x, uint32_t y) {
+    if constexpr (DT == 0) {
+      const __nv_bfloat162 h = __hmin2(*reinterpret_cast<const __nv_bfloat162*>(&x), *reinterpret_cast<const __nv_bfloat162*>(&y));
+      return *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+      return __float_as_uint(fminf(__uint_as_float(x), __uint_as_float(y)));
+    }
+  };
+  return make_uint4(word(a.x, b.x), word(a.y, b.y), word(a.z, b.z), word(a.w, b.w));
+}
+template <int DT>
+__device__ __forceinline__ float vmin(const uint4& v) {
+  float x[Elem<DT>::kVec];
+  Elem<DT>::unpack(v, x);
+#pragma unroll
+  for (int i = 1; i < Elem<DT>::kVec; ++i) x[0] = fminf(x[0], x[i]);
+  return x[0];
+}
+
 struct EntropyStats {
   float m, s, w;
 
   __device__ __forceinline__ float log_sum() const { return logf(s); }
-  __device__ __forceinline__ float entropy() const { return fmaxf(logf(s) - kLn2 * (w / s), 0.f); }
+  __device__ __forceinline__ float entropy(float ln_s) const { return fmaxf(ln_s - kLn2 * (w / s), 0.f); }
 };
 
 // The statistics that the lanes of a warp hold, merged: the same bits in every lane.
@@ -117,9 +175,10 @@ struct RowGradient {
   float m, c, a, b;
 
   // G and h with the factor that is common to the row (an upstream gradient over T) multiplied in already.
-  __device__ __forceinline__ RowGradient(float m_, float s, float H, float G, float h, float c_) : m(m_), c(c_) {
-    a = held(-(G + h * (H - logf(s))) / s);
-    b = held(-h * kLn2 / s);
+  __device__ __forceinline__ RowGradient(float m_, float s, float ln_s, float H, float G, float h, float c_) : m(m_), c(c_) {
+    const float inv_s = 1.f / s;
+    a = held(-(G + h * (H - ln_s)) * inv_s);
+    b = held(-h * kLn2 * inv_s);
   }
   __device__ __forceinline__ float at(float x) const {
     const float d = (x - m) * c;
@@ -140,6 +199,31 @@ struct RowGradient {
     }
     return Out<DT>::pack(x);
   }
+  // The same for logits that are near (see NearAcc), and moderate factors.
+  struct Near {
+    uint64_t c2, minus_M2, a2, b2;
+
+    __device__ __forceinline__ explicit Near(const RowGradient& g) {
+      // 2^d (a + b d) with d = d' - rho
+      const float M = g.m * g.c, rho = fmaf(g.m, g.c, -M), f = ex2_approx(-rho), a = f * fmaf(-g.b, rho, g.a), b = f * g.b;
+      c2 = pack_f2(g.c, g.c), minus_M2 = pack_f2(-M, -M), a2 = pack_f2(a, a), b2 = pack_f2(b, b);
+    }
+    template <int DT>
+    __device__ __forceinline__ uint4 vector(const uint4& v) const {
+      constexpr int N = Elem<DT>::kVec;
+      float x[N];
+      Elem<DT>::unpack(v, x);
+#pragma unroll
+      for (int i = 0; i < N; i += 2) {
+        const uint64_t d = ffma_f2(pack_f2(x[i], x[i + 1]), c2, minus_M2);
+        float p, q;
+        unpack_f2(d, p, q);
+        unpack_f2(fmul_f2(pack_f2(ex2_approx(p), ex2_approx(q)), ffma_f2(d, b2, a2)), x[i], x[i + 1]);
+      }
+      return Out<DT>::pack(x);
+    }
+  };
+  __device__ __forceinline__ bool moderate() const { return fabsf(m * c) <= kNear && fabsf(a) <= kNear && fabsf(b) <= kNear; }
 };
 
 // One vector of a gradient row to `to`, which lies `shift` bytes past a 16-byte boundary; by whole warps (see store_shifted).

@@ -45,11 +45,16 @@ constexpr int kKeepBytes = 212992;  // shared memory of one SM that keeps logits
 constexpr uint32_t kStallPolls = 16;
 constexpr float kLate = -1.f;  // in place of a mass: a copy did not arrive
 
+__device__ __forceinline__ void prefetch_l2(const void* from, uint32_t bytes) {  // 16-byte aligned, a multiple of 16
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(from), "r"(bytes) : "memory");
+}
+
 // KEEP: the slice's vectors lie in dynamic shared memory (16 bytes for each).
 template <int DT, int NT, int MINB, bool KEEP>
 __global__ void __launch_bounds__(NT, MINB) policy_kernel(const __grid_constant__ PolicyParams p) {
   constexpr int NW = NT / 32, VEC = Elem<DT>::kVec;
   constexpr int U = 4;  // vectors in flight per thread where they are not kept (and as many again)
+  constexpr int kAhead = 76 * MINB;  // CTAs that a prefetch runs ahead: half of what runs at once
   extern __shared__ __align__(128) uint4 kept[];
   __shared__ uint64_t full;
   __shared__ float4 red[NW];
@@ -79,14 +84,43 @@ __global__ void __launch_bounds__(NT, MINB) policy_kernel(const __grid_constant_
   const bool sound = temperature_valid(T) && token >= -1 && token < p.V && fabsf(A) < INFINITY && fabsf(old) < INFINITY;
   int status = sound ? SFC_ROW_OK : SFC_ROW_BADPARAM;
   bool live = sound && token >= 0, late = false;  // uniform over the row's CTAs
+  bool near = false;  // this thread's kept logits are
+  uint4 top = Elem<DT>::neg_inf_vec(), low = top;
   EntropyStats all{-FLT_MAX, 0.f, 0.f};
   if (live) {
     EntropyAcc a;
     if (KEEP) {
       late = !__all_sync(kFull, mbar_wait(&full, 0, p.stall ? kStallPolls : kWaitPolls));
+      if (tid == 0 && r + kAhead / S < gridDim.x) {  // a later CTA's slice on its way to L2 while HBM would idle
+        const RowSpan<DT> later(p.logits, (r + kAhead / S) * p.row_stride, p.V);
+        const int vecs = static_cast<int>(later.nvec), at = min(rank * p.per, vecs), bytes = (min(at + p.per, vecs) - at) * 16;
+        if (bytes > 0) prefetch_l2(later.body() + at, bytes);
+      }
       if (!late) {
+        // the extremes first: the sums then have no rescaling and no step that waits for the one before
+        if (mine > tid) top = low = kept[tid];
+#pragma unroll 4
+        for (int k = tid + NT; k < mine; k += NT) {
+          const uint4 v = kept[k];
+          top = larger<DT>(top, v);
+          low = smaller<DT>(low, v);
+        }
+        const float most = Elem<DT>::vmax(top);
+        near = mine <= tid || fmaxf(fabsf(most * c), fabsf(vmin<DT>(low) * c)) <= kNear;
+        if (mine > tid && near) {
+          NearAcc n(most, c);
+#pragma unroll 4
+          for (int k = tid; k < mine; k += NT) n.template add<DT>(kept[k]);
+          n.finish(a, most, c);
+        } else {
+          a.raise(most, c);
 #pragma unroll 2
-        for (int k = tid; k < mine; k += NT) a.template add<DT>(kept[k], c);
+          for (int k = tid; k < mine; k += NT) {
+            float x[VEC];
+            Elem<DT>::unpack(kept[k], x);
+            a.add_below(x, c);
+          }
+        }
       }
     } else {
       RowStream<DT, NT, U> stream(row, v0, v1);
@@ -119,14 +153,16 @@ __global__ void __launch_bounds__(NT, MINB) policy_kernel(const __grid_constant_
   }
   // nothing of the CTA's is still in flight when it ends
   if (KEEP && !live && tid == 0 && !p.stall) mbar_wait(&full, 0);
-  float H = 0.f, lp = 0.f, loss = status < 0 ? nan : 0.f, slope = 0.f;  // slope: dloss/dlp
+  const float inv_T = fminf(1.f / T, FLT_MAX);
+  float H = 0.f, lp = 0.f, ln_s = 0.f, loss = status < 0 ? nan : 0.f, slope = 0.f;  // slope: dloss/dlp
   if (live) {
-    const float ln_s = all.log_sum(), z = (xt - all.m) / T;
-    H = all.entropy();
+    ln_s = all.log_sum();
+    H = all.entropy(ln_s);
+    const float z = (xt - all.m) * inv_T;
     lp = z - ln_s;
     if (p.old_logprobs) {
-      // lp - old with the division's remainder, and the near numbers subtracted first: rho is as exact as its exponent
-      const float rest = z > -INFINITY ? fmaf(-z, T, xt - all.m) / T : 0.f;
+      // lp - old with the quotient's remainder, and the near numbers subtracted first: rho is as exact as its exponent
+      const float rest = z > -INFINITY ? fmaf(-z, T, xt - all.m) * inv_T : 0.f;
       const float rho = expf((z - old) - ln_s + rest), plain = rho * A;
       const float low = 1.f - p.clip_low, high = 1.f + p.clip_high;
       const bool active = A >= 0.f ? rho <= high : rho >= low;
@@ -138,16 +174,20 @@ __global__ void __launch_bounds__(NT, MINB) policy_kernel(const __grid_constant_
     }
     if (p.entropy_weight != 0.f) loss -= p.entropy_weight * H;
   }
-  const float scale = live ? up * fminf(1.f / T, FLT_MAX) : 0.f, g = held(slope * scale);
+  const float scale = live ? up * inv_T : 0.f, g = held(slope * scale);
   unsigned char* grad = p.grad + r * p.grad_stride * Elem<DT>::kBytes;
   unsigned char* out = grad + static_cast<int64_t>(row.head) * Elem<DT>::kBytes;
   const int shift = static_cast<int>(reinterpret_cast<uintptr_t>(out) & 15);
-  const RowGradient dense(all.m, live ? all.s : 1.f, H, g, -p.entropy_weight * scale, c);
+  const RowGradient dense(all.m, live ? all.s : 1.f, ln_s, H, g, -p.entropy_weight * scale, c);
   auto put = [&](int at, const uint4& w) { store_vector<DT>(out + static_cast<int64_t>(at) * 16, w, shift, at < v1); };
   if (!live) {
     for (int i = v0 + tid; i - lane < v1; i += NT) put(i, make_uint4(0u, 0u, 0u, 0u));
   } else if (KEEP && DT == 0 && shift != 0) {
     for (int i = tid; i - lane < mine; i += NT) put(v0 + i, dense.template vector<DT>(kept[min(i, mine - 1)]));
+  } else if (KEEP && near && dense.moderate()) {
+    const RowGradient::Near n(dense);
+#pragma unroll 4
+    for (int i = tid; i < mine; i += NT) put(v0 + i, n.template vector<DT>(kept[i]));
   } else if (KEEP) {
 #pragma unroll 2
     for (int i = tid; i < mine; i += NT) put(v0 + i, dense.template vector<DT>(kept[i]));

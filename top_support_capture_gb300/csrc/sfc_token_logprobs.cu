@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(NT, MINB) score_kernel(const __grid_constant__
   auto logprob = [&](float x) { return (x - all.m) / T - ln_s; };
   if (tid < p.M) p.logprobs[r * p.M + tid] = !ok ? nan : given ? logprob(xt) : 0.f;
   if (tid == 0) {
-    const float H = all.entropy();
+    const float H = all.entropy(ln_s);
     p.entropy[r] = ok ? H : nan;
     p.row_status[r] = ok ? SFC_ROW_OK : SFC_ROW_BADPARAM;
     if (p.stats) p.stats[r] = make_float4(ok ? all.m : nan, all.s, H, 0.f);
@@ -328,7 +328,7 @@ __global__ void __launch_bounds__(NT, MINB) score_backward_kernel(const __grid_c
   float G = 0.f;
   for (int j = lane; j < p.M; j += 32) G += gs[j];
   G = warp_total(G);
-  const RowGradient dense(st.x, st.y, st.z, G, h, c);
+  const RowGradient dense(st.x, st.y, logf(st.y), st.z, G, h, c);
   unsigned char* grad = p.grad + r * p.grad_stride * Elem<DT>::kBytes;
   unsigned char* out = grad + static_cast<int64_t>(row.head) * Elem<DT>::kBytes;
   const int shift = static_cast<int>(reinterpret_cast<uintptr_t>(out) & 15);
