@@ -27,7 +27,7 @@ namespace {
 constexpr int kThreads = 256, kCtas = 4 * 152, kClipCtas = 3 * 152;  // a wave of CTAs
 constexpr int kInFlight = 8;                    // 16-byte vectors of a thread
 constexpr int kChunk = kInFlight * kThreads;    // vectors
-constexpr int kFew = 16, kMany = 1000;          // tensors of a launch: parameters of 0.7 KB, of 32 KB
+constexpr int kFew = 16, kSome = 250, kMany = 1000;  // tensors of a launch: parameters of 0.6, 8 and 32 KB
 
 struct Tensor {
   const void* in;
@@ -421,7 +421,9 @@ int enqueue(const List& l, float max_norm, float* norm, void* workspace, size_t 
   if (!workspace || workspace_bytes < workspace_bytes_of(l.n)) return SFC_EWORKSPACE;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   double* partial = static_cast<double*>(workspace);
-  if ((l.n <= kFew ? run<kFew>(l, max_norm, norm, partial, st) : run<kMany>(l, max_norm, norm, partial, st)) != cudaSuccess) {
+  const cudaError_t err = l.n <= kFew ? run<kFew>(l, max_norm, norm, partial, st)
+                          : l.n <= kSome ? run<kSome>(l, max_norm, norm, partial, st) : run<kMany>(l, max_norm, norm, partial, st);
+  if (err != cudaSuccess) {
     (void)cudaGetLastError();
     return SFC_ECUDA;
   }

@@ -9,10 +9,9 @@ from operator import attrgetter
 import torch
 from torch.autograd import forward_ad
 
-from . import SFC_BF16, SFC_F32, SFC_OK, SfcError, _dtype_code, _enter, load_library
+from . import SFC_OK, SfcError, _dtype_code, _enter, load_library
 from .training import _raise
 
-_CODES = {torch.bfloat16: SFC_BF16, torch.float32: SFC_F32}
 _dtype, _requires_grad = attrgetter("dtype"), attrgetter("requires_grad")
 _Tensor = torch.Tensor
 
@@ -28,16 +27,17 @@ def _dense(t):
 
 
 def check_tensors(name, tensors):
-    """The tensors as a list (entries None left out), each on one CUDA device and dense."""
+    """The tensors as a list (entries None left out), each on one CUDA device and dense; and whether all are contiguous."""
     tensors = [t for t in ([tensors] if isinstance(tensors, torch.Tensor) else tensors) if t is not None]
     if not tensors:
         raise SfcError(f"{name} holds no tensor")
-    if not _all_plain(tensors):
+    plain = _all_plain(tensors)
+    if not plain:
         device = tensors[0].device
         if device.type != "cuda":
             raise SfcError(f"{name} must be CUDA tensors, got {device}")
         check_layouts(name, tensors, device)
-    return tensors
+    return tensors, plain
 
 
 def _all_plain(tensors):
@@ -68,48 +68,52 @@ def check_layouts(name, tensors, device):
 
 def _arrays(tensors):
     """(addresses, counts, dtype codes) as the library reads them."""
-    try:
-        codes = array("i", map(_CODES.__getitem__, map(_dtype, tensors)))
-    except KeyError:
-        for t in tensors:
-            _dtype_code(t)
-        raise
+    dtypes = list(map(_dtype, tensors))
+    if dtypes.count(dtypes[0]) == len(dtypes):
+        codes = array("i", [_dtype_code(tensors[0])]) * len(dtypes)
+    else:
+        codes = array("i", map(_dtype_code, tensors))
     return array("Q", map(_Tensor.data_ptr, tensors)), array("q", map(_Tensor.numel, tensors)), codes
 
 
 def grad_norm(grads, stream=None):
     """The global norm of ``grads`` (an iterable of bf16/f32 CUDA tensors of one device, entries None left out): a float32
     scalar tensor. See include/sfc.h."""
-    grads = check_tensors("grads", grads)
-    return _run(grads, None, 0.0, stream)
+    grads, _ = check_tensors("grads", grads)
+    return _run(grads, _arrays(grads), None, None, 0.0, stream)
 
 
 def clip_grad_norm(grads, max_norm: float, out=None, stream=None):
-    """Scales ``grads`` so that their global norm is at most ``max_norm``, in place, or into the tensors of ``out`` (as many,
-    of the same shapes; bf16 or f32 each, as the optimizer wants them). Returns the norm before clipping, a float32 scalar
+    """Scales ``grads`` so that their global norm is at most ``max_norm``, in place, or into the tensors of ``out`` (as many, of
+    as many elements; bf16 or f32 each, as the optimizer wants them). Returns the norm before clipping, a float32 scalar
     tensor. No host synchronisation. See include/sfc.h."""
     max_norm = float(max_norm)
     if not max_norm >= 0.0:
         raise SfcError(f"max_norm must be >= 0, got {max_norm}")
-    grads = check_tensors("grads", grads)
-    if out is not None:
-        out = check_tensors("out", out)
+    grads, plain = check_tensors("grads", grads)
+    lists = _arrays(grads)
+    if out is None:
+        return _run(grads, lists, grads, lists, max_norm, stream)
+    out, out_plain = check_tensors("out", out)
+    to = _arrays(out)
+    if len(out) != len(grads) or to[1] != lists[1] or out[0].device != grads[0].device or not (plain and out_plain):
         check_out(grads, out)
-    return _run(grads, grads if out is None else out, max_norm, stream)
+    return _run(grads, lists, out, to, max_norm, stream)
 
 
 def check_out(grads, out):
+    """Each of ``out`` beside its gradient: of as many elements in the same order (contiguous both, or the same layout)."""
     if len(out) != len(grads):
         raise SfcError(f"out must hold {len(grads)} tensors, got {len(out)}")
     for i, (g, o) in enumerate(zip(grads, out)):
-        if o.device != g.device or o.shape != g.shape or (o.stride() != g.stride() and not (o.is_contiguous() and g.is_contiguous())):
-            raise SfcError(f"out[{i}] must have grads[{i}]'s device, shape and strides")
+        if o.device != g.device or o.numel() != g.numel():
+            raise SfcError(f"out[{i}] must be on grads[{i}]'s device and have its shape")
+        if not (o.is_contiguous() and g.is_contiguous()) and (o.shape != g.shape or o.stride() != g.stride()):
+            raise SfcError(f"out[{i}] must have grads[{i}]'s shape and strides (or both be contiguous)")
 
 
-def _run(grads, out, max_norm, stream):
+def _run(grads, lists, out, to, max_norm, stream):
     lib, dev, n = load_library(), grads[0].device, len(grads)
-    lists = _arrays(grads)
-    to = () if out is None else lists[::2] if out is grads else _arrays(out)[::2]
     stream, context = _enter(dev, stream, *grads, *(out if out is not None and out is not grads else ()))
     with context:
         nbytes = lib.sfc_grad_norm_workspace_size(n)
@@ -119,7 +123,7 @@ def _run(grads, out, max_norm, stream):
         address = lambda a: a.buffer_info()[0]  # (the arrays live until the call is over)
         tail = norm.data_ptr(), workspace.data_ptr(), nbytes, stream
         rc = (lib.sfc_grad_norm(*map(address, lists), n, *tail) if out is None else
-              lib.sfc_clip_grad_norm(*map(address, lists), n, max_norm, *map(address, to), *tail))
+              lib.sfc_clip_grad_norm(*map(address, lists), n, max_norm, address(to[0]), address(to[2]), *tail))
     if rc != SFC_OK:
         _raise("sfc_grad_norm" if out is None else "sfc_clip_grad_norm (tensors that overlap?)", rc)
     if out is not None:  # autograd's view of what was written

@@ -11,7 +11,7 @@ from typing import NamedTuple
 import torch
 from torch.autograd import forward_ad
 
-from . import FLAG_TEST_STALL, MAX_GIVEN, MAX_TOP, SFC_OK, SfcError, _enter, _expect, _ptr, load_library
+from . import FLAG_TEST_STALL, MAX_GIVEN, MAX_TOP, SFC_OK, SfcError, _dtype_code, _enter, _expect, _ptr, load_library
 from .training import _check_grad, _raise, _rows_args, check_derivatives, check_rows
 
 
@@ -65,31 +65,46 @@ def _forward(logits, stride, temperature, tokens, M, top, stream, keep_stats):
 
 
 class _TokenLogprobs(torch.autograd.Function):
+    """Makes the float outputs of a call that has been made already functions of its logits. (What goes through `apply` costs
+    a few microseconds for each tensor: the whole numbers do not.)"""
+
     @staticmethod
-    def forward(ctx, logits, stride, temperature, tokens, M, top):
-        out = _forward(logits, stride, temperature, tokens, M, top, None, True)
-        ctx.save_for_backward(logits, temperature, tokens, out.top_ids, out.row_stats)
+    def forward(ctx, logits, stride, temperature, tokens, out):
+        ctx.save_for_backward(logits, temperature, tokens, out.row_stats, out.top_ids)
+        ctx.stride, ctx.has = stride, (out.logprobs is not None, out.top_logprobs is not None)
         ctx.set_materialize_grads(False)  # none is made for what takes no part in a loss
-        ctx.mark_non_differentiable(*(t for t in (out.top_ids, out.row_status) if t is not None))
-        return out[:5]
+        return tuple(t for t in (out.entropy, out.logprobs, out.top_logprobs) if t is not None)
 
     @staticmethod
     @torch.autograd.function.once_differentiable
-    def backward(ctx, grad_logprobs, grad_entropy, _ids, grad_top, _status):
-        if grad_logprobs is None and grad_entropy is None and grad_top is None:
-            return (None,) * 6
-        logits, temperature, tokens, top_ids, stats = ctx.saved_tensors
-        B, given = logits.shape[0], []
-        with torch.cuda.device(logits.device):  # autograd runs a backward on its forward's stream
-            if grad_logprobs is not None:
-                given.append((tokens.view(B, -1), grad_logprobs.reshape(B, -1)))
-            if grad_top is not None:
-                given.append((top_ids, grad_top))
-            tokens, up = (torch.cat(part, 1) if len(part) > 1 else part[0] for part in zip(*given)) if given else (None, None)
-            up = None if up is None else up.to(torch.float32).contiguous()
-            grad_entropy = None if grad_entropy is None else grad_entropy.to(torch.float32).contiguous()
-        grad = token_logprobs_backward(logits.detach(), temperature, tokens, stats, up, grad_entropy)
-        return grad, None, None, None, None, None
+    def backward(ctx, grad_entropy, *grads):
+        grads = iter(grads)
+        grad_logprobs, grad_top = (next(grads) if has else None for has in ctx.has)
+        if grad_logprobs is None and grad_top is None and grad_entropy is None:
+            return (None,) * 5
+        logits, temperature, tokens, stats, top_ids = ctx.saved_tensors
+        dev, (B, V) = logits.device, logits.shape
+        stream, context = _enter(dev, None)  # autograd runs a backward on its forward's stream
+        with context:
+            if grad_top is not None:  # the alternatives are tokens like the others
+                if grad_logprobs is None:
+                    tokens, grad_logprobs = top_ids, grad_top
+                else:
+                    tokens = torch.cat((tokens.view(B, -1), top_ids), 1)
+                    grad_logprobs = torch.cat((grad_logprobs.reshape(B, -1), grad_top), 1)
+            elif grad_logprobs is None:
+                tokens = None
+            if grad_logprobs is not None and not (grad_logprobs.dtype is torch.float32 and grad_logprobs.is_contiguous()):
+                grad_logprobs = grad_logprobs.to(torch.float32).contiguous()
+            if grad_entropy is not None and not (grad_entropy.dtype is torch.float32 and grad_entropy.is_contiguous()):
+                grad_entropy = grad_entropy.to(torch.float32).contiguous()
+            grad = torch.empty((B, V), dtype=logits.dtype, device=dev)
+            rc = load_library().sfc_token_logprobs_backward(
+                logits.data_ptr(), _dtype_code(logits), B, V, ctx.stride, temperature.data_ptr(), _ptr(tokens),
+                0 if tokens is None else tokens.numel() // B, stats.data_ptr(), _ptr(grad_logprobs), _ptr(grad_entropy), grad.data_ptr(), V, stream)
+        if rc != SFC_OK:
+            _raise("sfc_token_logprobs_backward", rc)
+        return grad, None, None, None, None
 
 
 def token_logprobs(logits, temperature, tokens=None, top: int = 0, keep_stats: bool = False, stream=None) -> TokenLogprobs:
@@ -109,7 +124,10 @@ def token_logprobs(logits, temperature, tokens=None, top: int = 0, keep_stats: b
             raise SfcError("keep_stats is for calls outside autograd: detach the logits")
         _, context = _enter(logits.device, stream, logits, temperature, tokens)
         with context:
-            return TokenLogprobs(*_TokenLogprobs.apply(logits, row, temperature, tokens, M, top))
+            out = _forward(logits, row, temperature, tokens, M, top, None, True)
+            floats = iter(_TokenLogprobs.apply(logits, row, temperature, tokens, out))
+            entropy = next(floats)
+            return TokenLogprobs(next(floats) if M else None, entropy, out.top_ids, next(floats) if top else None, out.row_status)
     return _forward(logits, row, temperature, tokens, M, top, stream, keep_stats)
 
 
