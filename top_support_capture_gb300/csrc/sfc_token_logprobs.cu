@@ -260,10 +260,19 @@ __global__ void __launch_bounds__(NT, MINB) score_kernel(const __grid_constant__
     }
     return warp_max_key(key);
   };
-  uint64_t best = 0;
-  for (int l = 0; l < 32; ++l) {
-    const uint64_t k = next(wp * 32 + l, ~0ull);
-    if (lane == l) best = k;
+  uint64_t best = scalar ? ckey_of<DT>(xs, row.scalar_index(tid)) : 0ull;
+  float most = -INFINITY;  // in the vectors: ties keep the first
+  for (int k = tid; k < nvec; k += NT) {
+    const uint4 v = __ldg(row.body() + k);
+    if (!(Elem<DT>::vmax(v) > most)) continue;
+    most = Elem<DT>::vmax(v);
+    float x[VEC];
+    Elem<DT>::unpack(v, x);
+    int first = 0;
+#pragma unroll
+    for (int e = VEC - 1; e >= 0; --e)
+      if (x[e] == most) first = e;
+    best = max(best, ckey_of<DT>(most, row.head + static_cast<int64_t>(k) * VEC + first));
   }
   for (int j = 0; j < K; ++j) {
     const uint64_t w = warp_max_key(best);

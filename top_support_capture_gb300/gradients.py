@@ -72,7 +72,8 @@ def _arrays(tensors):
     if dtypes.count(dtypes[0]) == len(dtypes):
         codes = array("i", [_dtype_code(tensors[0])]) * len(dtypes)
     else:
-        codes = array("i", map(_dtype_code, tensors))
+        of = {t.dtype: _dtype_code(t) for t in map(tensors.__getitem__, map(dtypes.index, set(dtypes)))}
+        codes = array("i", map(of.__getitem__, dtypes))
     return array("Q", map(_Tensor.data_ptr, tensors)), array("q", map(_Tensor.numel, tensors)), codes
 
 
