@@ -28,7 +28,7 @@ constexpr int kMaxSlices = 8;  // the portable cluster size
 constexpr int kGroups = 128;   // of threads; not fewer than SFC_MAX_TOP, not more than the smallest CTA
 constexpr uint32_t kPool = 1024;
 constexpr int kListed = 64;  // cells of a warp
-constexpr int kCells = 24, kCellBytes = 32768;  // most of a thread, of a CTA
+constexpr int kCells = 24, kCellBytes = 32768;  // most of a thread (a mask's bits), of a CTA
 static_assert(SFC_MAX_TOP <= kGroups && SFC_MAX_GIVEN <= kGroups, "");
 
 struct ScoreParams {
@@ -62,6 +62,18 @@ __device__ __forceinline__ uint64_t warp_max_key(uint64_t k) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) k = max(k, __shfl_xor_sync(kFull, k, o));
   return k;
+}
+
+// The sum of n over the lanes before this one, and over all.
+__device__ __forceinline__ int warp_before(int n, int& total) {
+  int upto = n;
+#pragma unroll
+  for (int o = 1; o < 32; o *= 2) {
+    const int before = __shfl_up_sync(kFull, upto, o);
+    if (static_cast<int>(threadIdx.x & 31) >= o) upto += before;
+  }
+  total = __shfl_sync(kFull, upto, 31);
+  return upto - n;
 }
 
 // The largest key below `limit` among the vectors first, first + step, ... below v1 (this lane's share of the work).
@@ -182,13 +194,12 @@ __global__ void __launch_bounds__(NT, MINB) score_kernel(const __grid_constant__
     // the warp's cells that reach the bound, then their vectors, one for each lane
     int listed = 0;
     if (__any_sync(kFull, a.m >= bound)) {
-      for (int i = 0; i << p.shift < batches; ++i) {
-        const bool in = cells[i * NT + tid] >= bound;
-        const unsigned who = __ballot_sync(kFull, in);
-        const int at = listed + __popc(who & ((1u << lane) - 1));
-        if (in && at < kListed) list[wp][at] = i * NT + tid;
-        listed += __popc(who);
-      }
+      uint32_t in = 0;
+      const int of_thread = (batches + of_cell) >> p.shift;
+#pragma unroll 8
+      for (int i = 0; i < of_thread; ++i) in |= static_cast<uint32_t>(cells[i * NT + tid] >= bound) << i;
+      int at = warp_before(__popc(in), listed);
+      for (; in && at < kListed; in &= in - 1) list[wp][at++] = (__ffs(in) - 1) * NT + tid;
       __syncwarp();
     }
     if (listed > kListed) {
@@ -202,16 +213,11 @@ __global__ void __launch_bounds__(NT, MINB) score_kernel(const __grid_constant__
       const int at = v0 + of % NT + ((of / NT << (p.shift + 2)) + (i & ((4 << p.shift) - 1))) * NT;
       const uint4 v = i < vectors && at < v1 ? __ldg(row.body() + at) : Elem<DT>::neg_inf_vec();
       uint32_t in = Elem<DT>::ge_mask(v, bound);
-      const int n = __popc(in);
-      int upto = n;  // of the lanes up to this one
-#pragma unroll
-      for (int o = 1; o < 32; o *= 2) {
-        const int before = __shfl_up_sync(kFull, upto, o);
-        if (lane >= o) upto += before;
-      }
+      int total;
+      const int before = warp_before(__popc(in), total);
       uint32_t to = 0;
-      if (lane == 31 && upto > 0) to = add(upto);
-      to = __shfl_sync(kFull, to, 31) + upto - n;
+      if (lane == 0 && total > 0) to = add(total);
+      to = __shfl_sync(kFull, to, 0) + before;
       for (; in; in &= in - 1) {
         const int e = __ffs(in) - 1;
         place(to++, Elem<DT>::get_dyn(v, e), row.head + static_cast<int64_t>(at) * VEC + e);
