@@ -6,7 +6,9 @@ has for such a pair:
   1. the target decodes with top-k / top-p and captures each position's support     sample_filter_capture
   2. the draft is trained on those supports                                         distill_loss_and_grad
   3. the draft is tuned on its own samples, over their supports                     replay_logprob (differentiable)
+     with the target's log-probabilities as reward                                  token_logprobs
   4. the draft drafts, the target verifies                                          verify_supports, verify_drafts
+  5. the draft is tuned over its whole vocabulary, a few updates per sample         policy_loss_and_grad, clip_grad_norm
 
 and prints how many tokens each call of the target yields before and after. `python examples/draft_and_verify.py`
 """
@@ -70,12 +72,35 @@ def tune(draft, table, steps=20, batch=512):
         context = torch.randint(0, V, (batch,), device=table.device)
         with torch.no_grad():
             own = capture(draft(context), 13, step)
-            reward = table[context].log_softmax(1).gather(1, own.tokens.long()[:, None])[:, 0]
+            reward = sfc.token_logprobs(table[context], ones, own.tokens).logprobs
         replay = sfc.replay_logprob(draft(context), ones, own.support_ids, own.lengths, own.tokens)
         loss = -((reward - reward.mean()) * replay.token_logprob).mean()
         opt.zero_grad()
         loss.backward()
         opt.step()
+
+
+def tune_clipped(draft, table, steps=10, epochs=3, batch=512):
+    """Towards the target's distribution by unfiltered samples (the reward is how much likelier the target finds them): clipped
+    policy updates and clipped gradients. Returns the gradients' norms."""
+    opt = torch.optim.Adam(draft.parameters(), lr=0.0005)
+    ones, norms = torch.ones(batch, device=table.device), []
+    for step in range(steps):
+        context = torch.randint(0, V, (batch,), device=table.device)
+        with torch.no_grad():
+            logits = draft(context)
+            tokens = torch.multinomial(logits.softmax(1), 1)[:, 0].int()
+            old = sfc.token_logprobs(logits, ones, tokens).logprobs
+            reward = sfc.token_logprobs(table[context], ones, tokens).logprobs - old
+            advantages = (reward - reward.mean()) / (reward.std() + 1e-6)
+        for _ in range(epochs):
+            logits = draft(context)
+            out = sfc.policy_loss_and_grad(logits.detach(), ones, tokens, advantages, ones / batch, old_logprobs=old)
+            opt.zero_grad()
+            logits.backward(out.grad_logits)
+            norms.append(sfc.clip_grad_norm([p.grad for p in draft.parameters()], 1.0))
+            opt.step()
+    return torch.stack(norms)
 
 
 @torch.no_grad()
@@ -120,8 +145,11 @@ def main():
     after = speculate(draft, table)
     tune(draft, table)
     tuned, dense = speculate(draft, table), speculate(draft, table, filtered=False)
+    norms = tune_clipped(draft, table)
+    clipped = speculate(draft, table, filtered=False)
     print(f"distillation loss {float(losses[0]):.3f} -> {float(losses[-1]):.3f}")
     print(f"tokens per call of the target: untrained {before:.2f}, distilled {after:.2f}, tuned {tuned:.2f}, unfiltered {dense:.2f}")
+    print(f"clipped updates over the whole vocabulary: gradient norm {float(norms[0]):.3f} -> {float(norms[-1]):.3f}, unfiltered {clipped:.2f}")
     return losses, before, after, tuned, dense
 
 
