@@ -159,6 +159,16 @@ __device__ __forceinline__ EntropyStats merge_lanes(const EntropyAcc& a, float c
   unpack_f2(a.w2, w, u);
   return merge_lanes(EntropyStats{a.m, s + t, w + u}, c);
 }
+// One thread's 16 bytes into another CTA's shared memory, counted by that CTA's barrier: the exchange of a cluster's
+// statistics without the barrier of the whole cluster, whose release waits for all that its warps have in flight.
+__device__ __forceinline__ void dsmem_send(uint32_t addr, const float4& v, uint32_t bar) {
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(addr), "f"(v.x),
+               "f"(v.y), "f"(v.z), "f"(v.w), "r"(bar)
+               : "memory");
+}
+// The arrival of a cluster barrier that orders nothing but the start of its CTAs.
+__device__ __forceinline__ void cluster_arrive_started() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+
 // n <= 32 statistics in shared memory, merged by a whole warp (the lanes past them repeat the first with no mass).
 __device__ __forceinline__ EntropyStats merge_shared(const float4* part, int n, float c) {
   const int lane = threadIdx.x & 31;
@@ -174,6 +184,7 @@ __device__ __forceinline__ float held(float x) {  // an overflow is held at the 
 struct RowGradient {
   float m, c, a, b;
 
+  __device__ __forceinline__ RowGradient(const float4& v) : m(v.x), c(v.y), a(v.z), b(v.w) {}
   // G and h with the factor that is common to the row (an upstream gradient over T) multiplied in already.
   __device__ __forceinline__ RowGradient(float m_, float s, float ln_s, float H, float G, float h, float c_) : m(m_), c(c_) {
     const float inv_s = 1.f / s;

@@ -62,37 +62,39 @@ __global__ void __launch_bounds__(NT, MINB) policy_kernel(const __grid_constant_
   constexpr int U = 4;  // vectors in flight per thread where they are not kept (and as many again)
   constexpr int kAhead = 76 * MINB;  // CTAs that a prefetch runs ahead: half of what runs at once
   extern __shared__ __align__(128) uint4 kept[];
-  __shared__ uint64_t full;
+  __shared__ uint64_t full, joined;  // the copy's arrival, that of the slices' statistics
   __shared__ float4 red[NW];
   __shared__ float4 table[kMaxSlices];  // (m, s, w) of the slices
+  __shared__ float4 gradient;           // (m, c, a, b) of the row's
+  __shared__ float slope_at_token;
+  __shared__ int outcome;
   const int tid = threadIdx.x, lane = tid & 31, wp = tid >> 5, S = p.slices, rank = blockIdx.y;
   const int64_t r = blockIdx.x;
   const RowSpan<DT> row(p.logits, r * p.row_stride, p.V);
   const uint4* body = row.body();
   const int nvec = static_cast<int>(row.nvec), v0 = min(rank * p.per, nvec), v1 = min(v0 + p.per, nvec), mine = v1 - v0;
   const bool scalar = rank == 0 && tid < row.scalars();
-  if (KEEP) {  // on their way while the row's parameters load
-    if (tid == 0) {
-      mbar_init(&full, 1);
-      mbar_init_fence();
-      if (!p.stall) {
-        mbar_arrive_expect_tx(&full, mine * 16);
-        if (mine > 0) bulk_load(kept, body + v0, mine * 16, &full);
-      }
+  if (tid == 0) {
+    mbar_init(&full, 1);
+    mbar_init(&joined, 1);
+    mbar_init_fence();
+    if (KEEP && !p.stall) {  // on its way while the row's parameters load
+      mbar_arrive_expect_tx(&full, mine * 16);
+      if (mine > 0) bulk_load(kept, body + v0, mine * 16, &full);
     }
-    __syncthreads();  // the barrier exists
+    mbar_arrive_expect_tx(&joined, S * sizeof(float4));
   }
-  if (S > 1) cluster_arrive();  // the cluster's CTAs have started: waited for before the first store into another
+  __syncthreads();                       // the barriers exist
+  if (S > 1) cluster_arrive_started();  // waited for before the first store into another CTA
   const float T = p.temperature[r], A = p.advantages[r], old = p.old_logprobs ? p.old_logprobs[r] : 0.f, up = p.grad_loss[r];
   const int32_t token = p.tokens[r];
-  const float c = exponent_scale(T), nan = __int_as_float(0x7fc00000);
+  const float c = exponent_scale(T);
   const float xt = token >= 0 && token < p.V ? row.at(token) : 0.f;
   const bool sound = temperature_valid(T) && token >= -1 && token < p.V && fabsf(A) < INFINITY && fabsf(old) < INFINITY;
   int status = sound ? SFC_ROW_OK : SFC_ROW_BADPARAM;
   bool live = sound && token >= 0, late = false;  // uniform over the row's CTAs
   bool near = false;  // this thread's kept logits are
   uint4 top = Elem<DT>::neg_inf_vec(), low = top;
-  EntropyStats all{-FLT_MAX, 0.f, 0.f};
   if (live) {
     EntropyAcc a;
     if (KEEP) {
@@ -137,54 +139,69 @@ __global__ void __launch_bounds__(NT, MINB) policy_kernel(const __grid_constant_
     if (lane == 0) red[wp] = make_float4(w.m, w.s, w.w, 0.f);
     if (KEEP) late = __syncthreads_or(late);
     else __syncthreads();
-    all = merge_shared(red, NW, c);
-    if (KEEP && late) all = EntropyStats{-FLT_MAX, kLate, 0.f};
-    if (S > 1) {
-      cluster_wait();
-      if (tid < S) {
-        const uint32_t to = dsmem_addr(&table[rank], tid);
-        dsmem_st64(to, pack_f2(all.m, all.s));
-        dsmem_st32(to + 8, __float_as_uint(all.w));
-      }
-      __syncwarp();  // the barrier's halves want whole warps
-      cluster_sync_all();
-      late = __any_sync(kFull, table[lane < S ? lane : 0].y == kLate);
-      all = merge_shared(table, S, c);
-    }
-    live = stats_valid(all.m, all.s) && !late;
-    if (!live) status = KEEP && late ? SFC_ROW_TIMEOUT : SFC_ROW_BADPARAM;
-  } else if (S > 1) {
-    cluster_wait();
-    cluster_sync_all();
   }
+  if (S > 1) cluster_wait();
+  // the row's scalars, by one warp of each of its CTAs
+  if (wp == 0) {
+    const float nan = __int_as_float(0x7fc00000), inv_T = fminf(1.f / T, FLT_MAX);
+    EntropyStats all{-FLT_MAX, kLate, 0.f};
+    if (live) {
+      if (!(KEEP && late)) all = merge_shared(red, NW, c);
+      if (S > 1) {
+        if (tid < S) dsmem_send(dsmem_addr(&table[rank], tid), make_float4(all.m, all.s, all.w, 0.f), dsmem_addr(&joined, tid));
+        __syncwarp();
+        late = !__all_sync(kFull, mbar_wait(&joined, 0));
+        if (late) mbar_wait(&joined, 0);  // nothing is on its way to a CTA that has ended
+        late = late || __any_sync(kFull, table[lane < S ? lane : 0].y == kLate);
+        all = merge_shared(table, S, c);
+      }
+      live = stats_valid(all.m, all.s) && !late;
+      if (!live) status = late ? SFC_ROW_TIMEOUT : SFC_ROW_BADPARAM;
+    }
+    float H = 0.f, lp = 0.f, ln_s = 0.f, loss = status < 0 ? nan : 0.f, slope = 0.f;  // slope: dloss/dlp
+    if (live) {
+      ln_s = all.log_sum();
+      H = all.entropy(ln_s);
+      const float z = (xt - all.m) * inv_T;
+      lp = z - ln_s;
+      if (p.old_logprobs) {
+        // lp - old with the quotient's remainder, and the near numbers subtracted first: rho is as exact as its exponent
+        const float rest = z > -INFINITY ? fmaf(-z, T, xt - all.m) * inv_T : 0.f;
+        const float rho = expf((z - old) - ln_s + rest), plain = rho * A;
+        const float low = 1.f - p.clip_low, high = 1.f + p.clip_high;
+        const bool active = A >= 0.f ? rho <= high : rho >= low;
+        loss = active ? -plain : -(A >= 0.f ? high : low) * A;
+        slope = active ? held(-plain) : 0.f;
+      } else {
+        loss = A == 0.f ? 0.f : -A * lp;
+        slope = xt > -INFINITY ? -A : 0.f;  // a masked token's log-probability is the constant -inf
+      }
+      if (p.entropy_weight != 0.f) loss -= p.entropy_weight * H;
+    }
+    if (lane == 0) {
+      const float scale = up * inv_T, g = held(slope * scale);
+      if (live) {
+        const RowGradient dense(all.m, all.s, ln_s, H, g, -p.entropy_weight * scale, c);
+        gradient = make_float4(dense.m, dense.c, dense.a, dense.b);
+        slope_at_token = g;
+      }
+      outcome = live;
+      if (rank == 0) {
+        p.loss[r] = loss;
+        p.logprobs[r] = status < 0 ? nan : lp;
+        p.entropy[r] = status < 0 ? nan : H;
+        p.row_status[r] = status;
+      }
+    }
+  }
+  __syncthreads();
+  live = outcome;
   // nothing of the CTA's is still in flight when it ends
   if (KEEP && !live && tid == 0 && !p.stall) mbar_wait(&full, 0);
-  const float inv_T = fminf(1.f / T, FLT_MAX);
-  float H = 0.f, lp = 0.f, ln_s = 0.f, loss = status < 0 ? nan : 0.f, slope = 0.f;  // slope: dloss/dlp
-  if (live) {
-    ln_s = all.log_sum();
-    H = all.entropy(ln_s);
-    const float z = (xt - all.m) * inv_T;
-    lp = z - ln_s;
-    if (p.old_logprobs) {
-      // lp - old with the quotient's remainder, and the near numbers subtracted first: rho is as exact as its exponent
-      const float rest = z > -INFINITY ? fmaf(-z, T, xt - all.m) * inv_T : 0.f;
-      const float rho = expf((z - old) - ln_s + rest), plain = rho * A;
-      const float low = 1.f - p.clip_low, high = 1.f + p.clip_high;
-      const bool active = A >= 0.f ? rho <= high : rho >= low;
-      loss = active ? -plain : -(A >= 0.f ? high : low) * A;
-      slope = active ? held(-plain) : 0.f;
-    } else {
-      loss = A == 0.f ? 0.f : -A * lp;
-      slope = xt > -INFINITY ? -A : 0.f;  // a masked token's log-probability is the constant -inf
-    }
-    if (p.entropy_weight != 0.f) loss -= p.entropy_weight * H;
-  }
-  const float scale = live ? up * inv_T : 0.f, g = held(slope * scale);
+  const RowGradient dense(gradient);
   unsigned char* grad = p.grad + r * p.grad_stride * Elem<DT>::kBytes;
   unsigned char* out = grad + static_cast<int64_t>(row.head) * Elem<DT>::kBytes;
   const int shift = static_cast<int>(reinterpret_cast<uintptr_t>(out) & 15);
-  const RowGradient dense(all.m, live ? all.s : 1.f, ln_s, H, g, -p.entropy_weight * scale, c);
   auto put = [&](int at, const uint4& w) { store_vector<DT>(out + static_cast<int64_t>(at) * 16, w, shift, at < v1); };
   if (!live) {
     for (int i = v0 + tid; i - lane < v1; i += NT) put(i, make_uint4(0u, 0u, 0u, 0u));
@@ -209,13 +226,7 @@ __global__ void __launch_bounds__(NT, MINB) policy_kernel(const __grid_constant_
     __syncthreads();  // the dense values are written before the token's overwrites its own
     const int64_t lo = row.head + static_cast<int64_t>(v0) * VEC, hi = row.head + static_cast<int64_t>(v1) * VEC;
     if (tid == 0 && ((token >= lo && token < hi) || (rank == 0 && (token < row.head || token >= row.tail()))))
-      Out<DT>::store1(grad, token, dense.at(xt) + g);
-  }
-  if (rank == 0 && tid == 0) {
-    p.loss[r] = loss;
-    p.logprobs[r] = status < 0 ? nan : lp;
-    p.entropy[r] = status < 0 ? nan : H;
-    p.row_status[r] = status;
+      Out<DT>::store1(grad, token, dense.at(xt) + slope_at_token);
   }
 }
 
