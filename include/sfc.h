@@ -405,7 +405,8 @@ int sfc_verify_supports(const int32_t* target_ids, const float* target_logprobs,
  * logprobs        [B, M] float32 out. entropy [B] float32 out. top_ids [B, top] int32, top_logprobs [B, top] float32 out.
  * row_stats       [B, 4] float32 out (16-byte aligned), or NULL: what sfc_token_logprobs_backward needs of the rows.
  * row_status      [B] int32 out: SFC_ROW_OK, or SFC_ROW_BADPARAM (every number NaN, ids -1) when T is not finite or <= 0, a
- *                 token is below -1 or not below V, a logit is NaN or +inf, or no logit is finite.
+ *                 token is below -1 or not below V, a logit is NaN or +inf, or no logit is finite; SFC_ROW_TIMEOUT (the same)
+ *                 when a bounded wait of the kernel for its own stores gave up (not expected to happen).
  * Every array is a device pointer owned by the caller; nothing is allocated; results are deterministic.
  * Returns SFC_OK or a negative code (nothing enqueued).
  */

@@ -11,11 +11,12 @@
 // the gradient is written first, the token's entry over it after the CTA's barrier. Rows longer than a cluster's shared
 // memory are read again.
 //
-// 2048 x 151936 bf16: 230 us, 0.80 of the measured copy rate (2 x 622 MB). The CTAs of a SM read, compute and write in turns, so
-// what they issue counts as much as the bytes: with sums that were rescaled as each vector raised the maximum, exponents in two
-// steps and products held above -200 one by one it took 264 us (a CTA's fold 9200 cycles of 23300); a later slice on its way to
-// L2 meanwhile 260; the extremes of a thread's vectors first, so that the sums have no such step, 252; one fused step per
-// exponent and no holding where the extremes allow it 230 (fold 4000 of 20000).
+// 2048 x 151936 bf16: 180 us, 1.02 of the measured copy rate (2 x 622 MB). The CTAs of a SM read, compute and write in turns, so
+// what they issue and wait for counts as much as the bytes. The steps: sums that were rescaled as each vector raised the
+// maximum, exponents in two steps and products held above -200 one by one 264 us; a later slice on its way to L2 meanwhile 260;
+// the extremes of a thread's vectors first, so that the sums have no such step, 252; one fused step per exponent and no holding
+// where the extremes allow it 230; the slices' statistics sent by stores that the receiver's barrier counts 180: a
+// cluster barrier's release had every warp wait for all that it had in flight (a quarter of the warps' time).
 #include <algorithm>
 #include <climits>
 #include <cstdint>
@@ -261,19 +262,12 @@ cudaError_t choose(PolicyParams& p, int64_t B, cudaStream_t stream) {
     p.slices = static_cast<int32_t>(std::min<int64_t>(S, kMaxSlices));
     return S <= kMaxSlices;
   };
-  // rows that one CTA holds, enough of them to fill the GPU: the smaller the CTA the more of them take turns on a SM
-  if (B >= 304) {
-    if (vectors <= kKeepBytes / 8 / 16 - 8 && fits(1)) return start<DT, 128, 8, true>(p, B, stream);
-    if (vectors <= kKeepBytes / 4 / 16 - 8 && fits(1)) return start<DT, 256, 4, true>(p, B, stream);
-    if (vectors <= kKeepBytes / 3 / 16 - 8 && fits(1)) return start<DT, 384, 3, true>(p, B, stream);
-    if (vectors <= kKeepBytes / 2 / 16 - 8 && fits(1)) return start<DT, 512, 2, true>(p, B, stream);
-  }
-  // Otherwise slices within their CTA's shared memory (in whole 128-byte lines), for few rows as many (two, four or eight) as
-  // there are places. Large CTAs where each has a SM to itself (1 x 151936 bf16: eight of 512 5.5 us, of 256 6.0), else small
-  // ones, which take turns (64 x 151936: four of 512 13.6, six of 256 13.0; 256 x 151936 39.4 : 36.1; 2048 x 151936 231 : 230).
+  // Slices within their CTA's shared memory (in whole 128-byte lines): the smaller the CTAs the better, as long as a row fits a
+  // cluster, since more of them take turns on a SM (2048 x 151936 bf16: six slices of 256 threads 180 us, three of 512 199;
+  // 2048 x 50000: four of 128 63, two of 256 64, one of 512 70). Few rows: as many slices (two, four or eight) as there are places.
   int64_t fill = 1;
   while (fill < kMaxSlices && vectors >= 4096 * fill && 2 * fill * B <= 304) fill *= 2;
-  if (fill * B <= 152 && fits(std::max(fill, cut(kKeepBytes / 2 / 16 - 8)))) return start<DT, 512, 2, true>(p, B, stream);
+  if (fits(std::max(fill, cut(kKeepBytes / 8 / 16 - 8)))) return start<DT, 128, 8, true>(p, B, stream);
   if (fits(std::max(fill, cut(kKeepBytes / 4 / 16 - 8)))) return start<DT, 256, 4, true>(p, B, stream);
   if (fits(cut(kKeepBytes / 2 / 16 - 8))) return start<DT, 512, 2, true>(p, B, stream);
   if (fits(cut(kKeepBytes / 16 - 8))) return start<DT, 1024, 1, true>(p, B, stream);

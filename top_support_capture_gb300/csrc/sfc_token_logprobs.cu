@@ -25,6 +25,7 @@ namespace sfc {
 namespace {
 
 constexpr int kMaxSlices = 8;  // the portable cluster size
+constexpr float kLate = -1.f;  // in place of a mass: a bounded wait gave up
 constexpr int kGroups = 128;   // of threads; not fewer than SFC_MAX_TOP, not more than the smallest CTA
 constexpr uint32_t kPool = 1024;
 constexpr int kListed = 64;  // cells of a warp
@@ -99,7 +100,9 @@ __global__ void __launch_bounds__(NT, MINB) score_kernel(const __grid_constant__
   constexpr int U = 4;  // vectors in flight per thread (and as many again)
   __shared__ float4 red[NW];
   __shared__ float4 table[kMaxSlices];   // (m, s, w) of the slices
-  __shared__ float2 bounds[kMaxSlices];  // of the slices' K-th and ceil(K / S)-th group maxima
+  __shared__ float4 bounds[kMaxSlices];  // their K-th and ceil(K / S)-th group maxima
+  __shared__ float4 joint;               // (m, s, w) of the row, the bound
+  __shared__ uint64_t joined;            // the arrival of the slices' statistics
   __shared__ __align__(16) uint32_t groups[kGroups];  // keys of the groups' maxima, made different by their low bits
   __shared__ float cut[2];
   __shared__ uint64_t pool[kPool], winners[NW];
@@ -110,7 +113,15 @@ __global__ void __launch_bounds__(NT, MINB) score_kernel(const __grid_constant__
   const RowSpan<DT> row(p.logits, r * p.row_stride, p.V);
   const int nvec = static_cast<int>(row.nvec), v0 = min(rank * p.per, nvec), v1 = min(v0 + p.per, nvec);
   RowStream<DT, NT, U> stream(row, v0, v1);
-  if (S > 1) cluster_arrive();  // the cluster's CTAs have started: waited for before the first store into another
+  if (S > 1) {
+    if (tid == 0) {
+      mbar_init(&joined, 1);
+      mbar_init_fence();
+      mbar_arrive_expect_tx(&joined, 2 * S * sizeof(float4));
+    }
+    __syncthreads();
+    cluster_arrive_started();  // waited for before the first store into another CTA
+  }
   const float T = p.temperature[r];
   const bool scalar = rank == 0 && tid < row.scalars();
   const float xs = scalar ? row.at(row.scalar_index(tid)) : -INFINITY;
@@ -162,28 +173,33 @@ __global__ void __launch_bounds__(NT, MINB) score_kernel(const __grid_constant__
     own = make_float2(cut[0], cut[1]);
   }
   float bound = own.x;
+  bool late = false;
   if (S > 1) {
     cluster_wait();
-    if (tid < S) {
-      const uint32_t to = dsmem_addr(&table[rank], tid);
-      dsmem_st64(to, pack_f2(all.m, all.s));
-      dsmem_st32(to + 8, __float_as_uint(all.w));
-      dsmem_st64(dsmem_addr(&bounds[rank], tid), pack_f2(own.x, own.y));
-    }
-    __syncwarp();  // the barrier's halves want whole warps
-    cluster_sync_all();
-    all = merge_shared(table, S, c);
-    if (K > 0) {
+    if (wp == 0) {
+      if (tid < S) {
+        const uint32_t bar = dsmem_addr(&joined, tid);
+        dsmem_send(dsmem_addr(&table[rank], tid), make_float4(all.m, all.s, all.w, 0.f), bar);
+        dsmem_send(dsmem_addr(&bounds[rank], tid), make_float4(own.x, own.y, 0.f, 0.f), bar);
+      }
+      __syncwarp();
+      late = !__all_sync(kFull, mbar_wait(&joined, 0));
+      if (late) mbar_wait(&joined, 0);  // nothing is on its way to a CTA that has ended
+      all = merge_shared(table, S, c);
       float low = bounds[0].y;
       bound = bounds[0].x;
       for (int i = 1; i < S; ++i) {
         bound = fmaxf(bound, bounds[i].x);
         low = fminf(low, bounds[i].y);
       }
-      bound = fmaxf(bound, low);
+      if (lane == 0) joint = make_float4(all.m, late ? kLate : all.s, all.w, fmaxf(bound, low));
     }
+    __syncthreads();
+    all = EntropyStats{joint.x, joint.y, joint.z};
+    bound = joint.w;
+    late = all.s == kLate;
   }
-  const bool valid = stats_valid(all.m, all.s);  // uniform over the cluster
+  const bool valid = stats_valid(all.m, all.s);  // uniform over the cluster (but for waits that gave up)
   if (K > 0 && valid) {
     const uint32_t counter = S > 1 ? dsmem_addr(&count, 0) : smem_addr(&count);
     const uint32_t places = S > 1 ? dsmem_addr(pool, 0) : smem_addr(pool);
@@ -224,7 +240,9 @@ __global__ void __launch_bounds__(NT, MINB) score_kernel(const __grid_constant__
       }
     }
     if (scalar && xs >= bound) place(add(1), xs, row.scalar_index(tid));
-    __syncwarp();
+  }
+  if (K > 0) {
+    __syncwarp();  // the barrier's halves want whole warps
     if (S > 1) cluster_sync_all();  // no CTA touches another's memory after it
     else __syncthreads();
   }
@@ -236,7 +254,7 @@ __global__ void __launch_bounds__(NT, MINB) score_kernel(const __grid_constant__
   if (tid == 0) {
     const float H = all.entropy(ln_s);
     p.entropy[r] = ok ? H : nan;
-    p.row_status[r] = ok ? SFC_ROW_OK : SFC_ROW_BADPARAM;
+    p.row_status[r] = ok ? SFC_ROW_OK : late ? SFC_ROW_TIMEOUT : SFC_ROW_BADPARAM;
     if (p.stats) p.stats[r] = make_float4(ok ? all.m : nan, all.s, H, 0.f);
   }
   if (K == 0) return;
