@@ -343,3 +343,28 @@ def test_rows_past_32_bit_offsets():
     grad = sfc.token_logprobs_backward(big, T, tokens, out.row_stats, g)
     check_grad(c, ref, oracle.token_logprobs_gradient(c["l"], wl.DT_BF16, c["T"], c["tokens"], c["g"]), grad[-last:])
     assert not grad[:-last].any()
+
+
+# Rows in one CTA of 128 or 256 threads, up to the longest of each and above it.
+@pytest.mark.parametrize("dtype", [wl.DT_BF16, wl.DT_F32])
+@pytest.mark.parametrize("B,vectors", [(320, 60), (320, 1369), (320, 4000), (310, 7000), (310, 7001), (306, 18992), (306, 54721)])
+def test_many_rows(dtype, B, vectors):
+    import top_support_capture_gb300 as sfc
+
+    V, K = vectors * (8 if dtype == wl.DT_BF16 else 4) + 3, 30
+    gen = torch.Generator("cuda").manual_seed(vectors)
+    x = torch.randn((B, V), generator=gen, device="cuda").mul_(3).to(torch.bfloat16 if dtype == wl.DT_BF16 else torch.float32)
+    x[1, 1000:] = -float("inf")
+    x[2, ::2] = -float("inf")
+    x[3] = x[3].round()  # ties
+    rng = np.random.default_rng(vectors)
+    T, tokens = rng.uniform(0.5, 1.7, B).astype(np.float32), rng.integers(-1, V, (B, 2)).astype(np.int32)
+    out = sfc.token_logprobs(x, cuda(T, np.float32), cuda(tokens, np.int32), top=K)
+    assert not out.row_status.any() and torch.isfinite(out.entropy).all()
+    rows = np.unique(np.r_[0, 1, 2, 3, B - 1, rng.integers(0, B, 4)])
+    at = torch.from_numpy(rows).cuda()
+    l = x[at].view(torch.int16).cpu().numpy().view(np.uint16) if dtype == wl.DT_BF16 else x[at].cpu().numpy()
+    some = dict(l=l, dtype=dtype, T=T[rows], tokens=tokens[rows])
+    check_values(some, reference(some, K), type(out)(*(t if t is None else t[at] for t in out)), K)
+    again = sfc.token_logprobs(x, cuda(T, np.float32), cuda(tokens, np.int32), top=K)
+    assert all(torch.equal(p, q) for p, q in zip(out[:5], again[:5]))  # whatever the order in which the slices' arrive

@@ -141,6 +141,42 @@ __device__ __forceinline__ float vmin(const uint4& v) {
   return x[0];
 }
 
+// One thread's share (every NT-th) of n vectors in shared memory. The extremes come first: the sums then have no rescaling and
+// no step that waits for the one before. Returns whether the thread's logits are near.
+template <int DT, int NT>
+__device__ __forceinline__ bool add_kept(EntropyAcc& a, const uint4* kept, int n, float c) {
+  const int tid = threadIdx.x;
+  if (tid >= n) return true;
+  uint4 top = kept[tid], low = top;
+#pragma unroll 4
+  for (int k = tid + NT; k < n; k += NT) {
+    const uint4 v = kept[k];
+    top = larger<DT>(top, v);
+    low = smaller<DT>(low, v);
+  }
+  const float most = Elem<DT>::vmax(top);
+  const bool near = fmaxf(fabsf(most * c), fabsf(vmin<DT>(low) * c)) <= kNear;
+  if (near) {
+    NearAcc sums(most, c);
+#pragma unroll 4
+    for (int k = tid; k < n; k += NT) sums.template add<DT>(kept[k]);
+    sums.finish(a, most, c);
+  } else {
+    a.raise(most, c);
+#pragma unroll 2
+    for (int k = tid; k < n; k += NT) {
+      float x[Elem<DT>::kVec];
+      Elem<DT>::unpack(kept[k], x);
+      a.add_below(x, c);
+    }
+  }
+  return near;
+}
+
+__device__ __forceinline__ void prefetch_l2(const void* from, uint32_t bytes) {  // 16-byte aligned, a multiple of 16
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(from), "r"(bytes) : "memory");
+}
+
 struct EntropyStats {
   float m, s, w;
 

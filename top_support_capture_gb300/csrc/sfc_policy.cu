@@ -52,10 +52,6 @@ constexpr int kKeepBytes = 212992;  // shared memory of one SM that keeps logits
 constexpr uint32_t kStallPolls = 16;
 constexpr float kLate = -1.f;  // in place of a mass: a copy did not arrive
 
-__device__ __forceinline__ void prefetch_l2(const void* from, uint32_t bytes) {  // 16-byte aligned, a multiple of 16
-  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(from), "r"(bytes) : "memory");
-}
-
 // KEEP: the slice's vectors lie in dynamic shared memory (16 bytes for each).
 template <int DT, int NT, int MINB, bool KEEP>
 __global__ void __launch_bounds__(NT, MINB) policy_kernel(const __grid_constant__ PolicyParams p) {
@@ -95,7 +91,6 @@ __global__ void __launch_bounds__(NT, MINB) policy_kernel(const __grid_constant_
   int status = sound ? SFC_ROW_OK : SFC_ROW_BADPARAM;
   bool live = sound && token >= 0, late = false;  // uniform over the row's CTAs
   bool near = false;  // this thread's kept logits are
-  uint4 top = Elem<DT>::neg_inf_vec(), low = top;
   if (live) {
     EntropyAcc a;
     if (KEEP) {
@@ -105,32 +100,7 @@ __global__ void __launch_bounds__(NT, MINB) policy_kernel(const __grid_constant_
         const int vecs = static_cast<int>(later.nvec), at = min(rank * p.per, vecs), bytes = (min(at + p.per, vecs) - at) * 16;
         if (bytes > 0) prefetch_l2(later.body() + at, bytes);
       }
-      if (!late) {
-        // the extremes first: the sums then have no rescaling and no step that waits for the one before
-        if (mine > tid) top = low = kept[tid];
-#pragma unroll 4
-        for (int k = tid + NT; k < mine; k += NT) {
-          const uint4 v = kept[k];
-          top = larger<DT>(top, v);
-          low = smaller<DT>(low, v);
-        }
-        const float most = Elem<DT>::vmax(top);
-        near = mine <= tid || fmaxf(fabsf(most * c), fabsf(vmin<DT>(low) * c)) <= kNear;
-        if (mine > tid && near) {
-          NearAcc n(most, c);
-#pragma unroll 4
-          for (int k = tid; k < mine; k += NT) n.template add<DT>(kept[k]);
-          n.finish(a, most, c);
-        } else {
-          a.raise(most, c);
-#pragma unroll 2
-          for (int k = tid; k < mine; k += NT) {
-            float x[VEC];
-            Elem<DT>::unpack(kept[k], x);
-            a.add_below(x, c);
-          }
-        }
-      }
+      if (!late) near = add_kept<DT, NT>(a, kept, mine, c);
     } else {
       RowStream<DT, NT, U> stream(row, v0, v1);
       stream.batches([&](const uint4(&v)[U]) { a.template add<DT, U>(v, c); });
