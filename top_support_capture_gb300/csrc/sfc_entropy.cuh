@@ -52,18 +52,11 @@ struct EntropyAcc {
     s2 = fadd_f2(s2, pack_f2(e, 0.f));
     w2 = fadd_f2(w2, pack_f2(e * fmaxf(d, kFar), 0.f));
   }
-  template <int DT>
-  __device__ __forceinline__ void add(const uint4& v, float c) {
-    raise(Elem<DT>::vmax(v), c);
-    float x[Elem<DT>::kVec];
-    Elem<DT>::unpack(v, x);
-    add_below(x, c);
-  }
   // U vectors; bf16: one maximum of all of them (see SoftmaxAcc::add). Returns their maximum.
   template <int DT, int U>
   __device__ __forceinline__ float add(const uint4 (&v)[U], float c) {
     constexpr int G = DT == 0 ? U : 1;
-    float most = -FLT_MAX;
+    float most = -INFINITY;
 #pragma unroll
     for (int g = 0; g < U; g += G) {
       uint4 top = v[g];

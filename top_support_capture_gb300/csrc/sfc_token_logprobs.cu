@@ -133,12 +133,12 @@ __global__ void __launch_bounds__(NT, MINB) score_kernel(const __grid_constant__
   EntropyAcc a;
   int batches = 0;
   const int of_cell = (1 << p.shift) - 1;
-  float cell = -FLT_MAX;
+  float cell = -INFINITY;  // (a cell without a finite logit reaches no bound)
   stream.batches([&](const uint4(&v)[U]) {
     cell = fmaxf(cell, a.template add<DT, U>(v, c));
     if (K > 0 && (batches & of_cell) == of_cell) {
       cells[(batches >> p.shift) * NT + tid] = cell;
-      cell = -FLT_MAX;
+      cell = -INFINITY;
     }
     ++batches;
   });
