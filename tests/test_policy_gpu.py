@@ -148,6 +148,30 @@ def test_masked_extreme_and_bad_rows(dtype, clipped):
     assert ref.slope[6] == 0 and ref.slope[7] == 0 and (clipped or (ref.loss[6] == np.inf and ref.loss[7] == -np.inf))
 
 
+@pytest.mark.parametrize("B", [4, 320])
+@pytest.mark.parametrize("shift", [-3e4, 1e6])
+def test_shifted_logits(B, shift):
+    """A constant added to a row changes nothing: the exponents' reference is far from 0 there."""
+    c = make(B, 5003, wl.DT_F32, 13, False, 0.02)
+    c["l"] = (c["l"] + np.float32(shift)).astype(np.float32)
+    check(c, call(c))
+
+
+@pytest.mark.parametrize("dtype", [wl.DT_BF16, wl.DT_F32])
+def test_masks_in_some_vectors_only(dtype):
+    """Threads whose logits are all near beside threads with masked ones, and scales that are far from 1."""
+    c = make(6, 30011, dtype, 14, False, 0.02)
+    l = oracle.widen_logits(c["l"], dtype).astype(np.float32)
+    l[0, 1000:1400] = -np.inf
+    l[1, 7::513] = -3.3895313892515355e38
+    l[2, 29000:] = -np.inf
+    l[3] *= 1e4
+    l[4] *= 1e-6
+    c["T"][5] = 1e-30
+    c["l"] = as_input(l, dtype)
+    check(c, call(c))
+
+
 def test_ratios_that_overflow():
     """An unclipped ratio above float32's range: an infinite loss, a gradient that stays a number."""
     c = make(2, 100, wl.DT_F32, 3)

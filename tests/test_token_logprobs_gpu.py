@@ -287,6 +287,33 @@ def test_steep_and_flat_rows(dtype):
     check_grad(c, ref, oracle.token_logprobs_gradient(c["l"], dtype, c["T"], c["tokens"], c["g"], c["h"]), grad)
 
 
+@pytest.mark.parametrize("dtype", [wl.DT_BF16, wl.DT_F32])
+def test_a_very_long_row(dtype):
+    import top_support_capture_gb300 as sfc
+
+    c = make(2, 3_000_017, 2, dtype, 12)
+    ref, a = reference(c, 64), args(c, pad=3, offset=1)
+    out = sfc.token_logprobs(*a, top=64, keep_stats=True)
+    check_values(c, ref, out, 64)
+    grad = sfc.token_logprobs_backward(*a, out.row_stats, cuda(c["g"], np.float32), cuda(c["h"], np.float32))
+    check_grad(c, ref, oracle.token_logprobs_gradient(c["l"], dtype, c["T"], c["tokens"], c["g"], c["h"]), grad)
+
+
+@pytest.mark.parametrize("shift", [-3e4, 1e6])
+def test_shifted_logits(shift):
+    """A constant added to a row changes nothing: the exponents' reference is far from 0 there."""
+    import top_support_capture_gb300 as sfc
+
+    c = make(5, 20011, 3, wl.DT_F32, 13)
+    c["l"] = (c["l"] + np.float32(shift)).astype(np.float32)
+    ref, a = reference(c, 7), args(c)
+    x = a[0].detach().requires_grad_()
+    out = sfc.token_logprobs(x, *a[1:], top=7)
+    check_values(c, ref, out, 7)
+    (grad,) = torch.autograd.grad([out.logprobs, out.entropy], x, [cuda(c["g"], np.float32), cuda(c["h"], np.float32)])
+    check_grad(c, ref, oracle.token_logprobs_gradient(c["l"], c["dtype"], c["T"], c["tokens"], c["g"], c["h"]), grad)
+
+
 def test_streams_graphs_and_repeats():
     import top_support_capture_gb300 as sfc
 
