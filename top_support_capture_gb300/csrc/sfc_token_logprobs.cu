@@ -429,12 +429,12 @@ cudaError_t choose(ScoreParams& p, int64_t B, cudaStream_t stream) {
   const int64_t vectors = p.V / Elem<DT>::kVec;
   // Few rows: slices for every SM (two or four or eight: clusters of other sizes leave SMs out; 24 x 151936 bf16 with six 6.3
   // us, four 5.7), and CTAs as large as keeps some vectors for each thread (1 x 151936: of 256 4.0 us, of 512 4.4; 64 x 151936
-  // 10.4 : 7.9). Many rows: one CTA each, of a size of which several take turns on a SM (2048 x 32000: of 128 25.7 us, of
-  // 256 26.4, of 512 32.8; 2048 x 151936 103.9, 100.6, 108.1). Groups of a CTA's threads need vectors to look at: rows
-  // below 1024 have CTAs of 128.
+  // 10.4 : 7.9). Many rows: one CTA each, of a size of which several take turns on a SM, with 20 alternatives 2048 x 32000 of 128
+  // 35 us, of 256 39, of 512 53; 1024 x 50000 f32 39, 44, 47; 2048 x 151936 118, 113, 128 (cut in two 129: each slice goes through
+  // the choice). Groups of a CTA's threads need vectors to look at: rows below 1024 have CTAs of 128.
   p.slices = 1;
   while (p.slices < kMaxSlices && 2 * p.slices * B <= 152 && vectors >= 4096 * p.slices) p.slices *= 2;
-  if (B > 304) return vectors <= 7000 ? start<DT, 128, 8>(p, B, stream) : start<DT, 256, 4>(p, B, stream);
+  if (B > 304) return p.V <= 56000 ? start<DT, 128, 8>(p, B, stream) : start<DT, 256, 4>(p, B, stream);
   if (vectors <= 1024) return start<DT, 128, 8>(p, B, stream);
   if (vectors / p.slices <= 3200) return start<DT, 256, 4>(p, B, stream);
   return start<DT, 512, 2>(p, B, stream);
