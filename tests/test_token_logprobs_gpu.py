@@ -314,6 +314,19 @@ def test_shifted_logits(shift):
     check_grad(c, ref, oracle.token_logprobs_gradient(c["l"], c["dtype"], c["T"], c["tokens"], c["g"], c["h"]), grad)
 
 
+def test_saved_tensors_that_are_moved():
+    """Hooks that keep what a backward needs elsewhere bring rows back that lie next to each other."""
+    import top_support_capture_gb300 as sfc
+
+    c = make(5, 5003, 3, wl.DT_BF16, 15)
+    ref, a = reference(c), args(c, pad=13, offset=2)
+    x = a[0].detach().requires_grad_()
+    with torch.autograd.graph.save_on_cpu():
+        out = sfc.token_logprobs(x, *a[1:], top=2)
+    (grad,) = torch.autograd.grad([out.logprobs, out.entropy], x, [cuda(c["g"], np.float32), cuda(c["h"], np.float32)])
+    check_grad(c, ref, oracle.token_logprobs_gradient(c["l"], c["dtype"], c["T"], c["tokens"], c["g"], c["h"]), grad)
+
+
 def test_streams_graphs_and_repeats():
     import top_support_capture_gb300 as sfc
 

@@ -11,7 +11,7 @@ from typing import NamedTuple
 import torch
 from torch.autograd import forward_ad
 
-from . import FLAG_TEST_STALL, MAX_GIVEN, MAX_TOP, SFC_OK, SfcError, _dtype_code, _enter, _expect, _ptr, load_library
+from . import FLAG_TEST_STALL, MAX_GIVEN, MAX_TOP, SFC_OK, SfcError, _enter, _expect, _ptr, load_library
 from .training import _check_grad, _raise, _rows_args, check_derivatives, check_rows
 
 
@@ -69,9 +69,9 @@ class _TokenLogprobs(torch.autograd.Function):
     a few microseconds for each tensor: the whole numbers do not.)"""
 
     @staticmethod
-    def forward(ctx, logits, stride, temperature, tokens, out):
+    def forward(ctx, logits, temperature, tokens, out):
         ctx.save_for_backward(logits, temperature, tokens, out.row_stats, out.top_ids)
-        ctx.stride, ctx.has = stride, (out.logprobs is not None, out.top_logprobs is not None)
+        ctx.has = out.logprobs is not None, out.top_logprobs is not None
         ctx.set_materialize_grads(False)  # none is made for what takes no part in a loss
         return tuple(t for t in (out.entropy, out.logprobs, out.top_logprobs) if t is not None)
 
@@ -81,8 +81,9 @@ class _TokenLogprobs(torch.autograd.Function):
         grads = iter(grads)
         grad_logprobs, grad_top = (next(grads) if has else None for has in ctx.has)
         if grad_logprobs is None and grad_top is None and grad_entropy is None:
-            return (None,) * 5
+            return (None,) * 4
         logits, temperature, tokens, stats, top_ids = ctx.saved_tensors
+        row = check_rows("logits", logits)  # (hooks on saved tensors may have laid them out anew)
         dev, (B, V) = logits.device, logits.shape
         stream, context = _enter(dev, None)  # autograd runs a backward on its forward's stream
         with context:
@@ -100,11 +101,11 @@ class _TokenLogprobs(torch.autograd.Function):
                 grad_entropy = grad_entropy.to(torch.float32).contiguous()
             grad = torch.empty((B, V), dtype=logits.dtype, device=dev)
             rc = load_library().sfc_token_logprobs_backward(
-                logits.data_ptr(), _dtype_code(logits), B, V, ctx.stride, temperature.data_ptr(), _ptr(tokens),
-                0 if tokens is None else tokens.numel() // B, stats.data_ptr(), _ptr(grad_logprobs), _ptr(grad_entropy), grad.data_ptr(), V, stream)
+                *_rows_args(logits, row, temperature), _ptr(tokens), 0 if tokens is None else tokens.numel() // B, stats.data_ptr(),
+                _ptr(grad_logprobs), _ptr(grad_entropy), grad.data_ptr(), V, stream)
         if rc != SFC_OK:
             _raise("sfc_token_logprobs_backward", rc)
-        return grad, None, None, None, None
+        return grad, None, None, None
 
 
 def token_logprobs(logits, temperature, tokens=None, top: int = 0, keep_stats: bool = False, stream=None) -> TokenLogprobs:
@@ -125,7 +126,7 @@ def token_logprobs(logits, temperature, tokens=None, top: int = 0, keep_stats: b
         _, context = _enter(logits.device, stream, logits, temperature, tokens)
         with context:
             out = _forward(logits, row, temperature, tokens, M, top, None, True)
-            floats = iter(_TokenLogprobs.apply(logits, row, temperature, tokens, out))
+            floats = iter(_TokenLogprobs.apply(logits, temperature, tokens, out))
             entropy = next(floats)
             return TokenLogprobs(next(floats) if M else None, entropy, out.top_ids, next(floats) if top else None, out.row_status)
     return _forward(logits, row, temperature, tokens, M, top, stream, keep_stats)
