@@ -57,7 +57,7 @@ def check_clipped(before, out, max_norm):
         assert np.all(np.abs(got - b * scale) <= limit)
 
 
-SIZES = [[1], [0], [3, 0, 5], [8], [4096], [64000, 64000], [1, 2, 3, 7, 8, 9, 15, 16, 17], [131072], [131073, 5], [16384 * 3 + 1, 16383, 16384 * 2],
+SIZES = [[1], [0], [3, 0, 5], [8], [4096], [64000, 64000], [1, 2, 3, 7, 8, 9, 15, 16, 17], [1] * 16, [16384 * 32], [16384 * 32 + 1], [8192 * 32 + 3], [20000] * 15, [131072], [131073, 5], [16384 * 3 + 1, 16383, 16384 * 2],
          [3000001], [5000, 1] * 30, [40000, 7, 0, 300] * 64, [700] * 1001, [3] * 2500, [12_000_001, 1_000_003, 5]]
 
 

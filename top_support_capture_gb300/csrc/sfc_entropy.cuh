@@ -195,9 +195,6 @@ __device__ __forceinline__ void dsmem_send(uint32_t addr, const float4& v, uint3
                "f"(v.y), "f"(v.z), "f"(v.w), "r"(bar)
                : "memory");
 }
-// The arrival of a cluster barrier that orders nothing but the start of its CTAs.
-__device__ __forceinline__ void cluster_arrive_started() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
-
 // n <= 32 statistics in shared memory, merged by a whole warp (the lanes past them repeat the first with no mass).
 __device__ __forceinline__ EntropyStats merge_shared(const float4* part, int n, float c) {
   const int lane = threadIdx.x & 31;

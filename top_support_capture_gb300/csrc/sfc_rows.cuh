@@ -20,6 +20,8 @@ namespace sfc {
 // The two halves of a cluster barrier (release / acquire).
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// The arrival of a cluster barrier that orders nothing but the start of its CTAs.
+__device__ __forceinline__ void cluster_arrive_started() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
 
 constexpr float kLog2e = 1.4426950408889634f;
 
