@@ -192,6 +192,11 @@ def test_streams_and_graphs():
     other = sfc.grad_norm(sets[0], stream=side)
     torch.cuda.current_stream().wait_stream(side)
     assert torch.equal(other, first[0])
+    moved = [torch.zeros_like(o) for o in outs[0]]
+    side.wait_stream(torch.cuda.current_stream())
+    other = sfc.clip_grad_norm(sets[0], 1.0, out=moved, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(other, first[0]) and all(torch.equal(p, q) for p, q in zip(moved, outs[0]))
     graphs = []
     for s, o in zip(sets, outs):
         graph = torch.cuda.CUDAGraph()

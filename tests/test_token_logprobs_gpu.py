@@ -314,6 +314,23 @@ def test_shifted_logits(shift):
     check_grad(c, ref, oracle.token_logprobs_gradient(c["l"], c["dtype"], c["T"], c["tokens"], c["g"], c["h"]), grad)
 
 
+def test_differentiable_on_another_stream():
+    import top_support_capture_gb300 as sfc
+
+    c = make(4, 200_003, 3, wl.DT_BF16, 16)
+    ref, a = reference(c, 4), args(c)
+    g, h = cuda(c["g"], np.float32), cuda(c["h"], np.float32)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    x = a[0].detach().requires_grad_()
+    out = sfc.token_logprobs(x, *a[1:], top=4, stream=side)
+    with torch.cuda.stream(side):
+        (grad,) = torch.autograd.grad([out.logprobs, out.entropy], x, [g, h])
+    torch.cuda.current_stream().wait_stream(side)
+    check_values(c, ref, out, 4)
+    check_grad(c, ref, oracle.token_logprobs_gradient(c["l"], c["dtype"], c["T"], c["tokens"], c["g"], c["h"]), grad)
+
+
 def test_saved_tensors_that_are_moved():
     """Hooks that keep what a backward needs elsewhere bring rows back that lie next to each other."""
     import top_support_capture_gb300 as sfc
