@@ -11,7 +11,7 @@ from typing import NamedTuple
 import torch
 from torch.autograd import forward_ad
 
-from . import FLAG_TEST_STALL, MAX_GIVEN, MAX_TOP, SFC_OK, SfcError, _enter, _expect, _ptr, load_library
+from . import FLAG_TEST_STALL, MAX_GIVEN, MAX_TOP, SFC_OK, SfcError, _dtype_code, _enter, _expect, _ptr, load_library
 from .training import _check_grad, _raise, _rows_args, check_derivatives, check_rows
 
 
@@ -47,18 +47,23 @@ def check_tokens(logits, tokens, most=MAX_GIVEN):
 
 
 def _forward(logits, stride, temperature, tokens, M, top, stream, keep_stats):
-    dev, B = logits.device, logits.shape[0]
+    dev, (B, V) = logits.device, logits.shape
     stream, context = _enter(dev, stream, logits, temperature, tokens)
-    f32, i32 = torch.float32, torch.int32
+    logprobs = ids = lps = stats = to_tokens = to_logprobs = to_ids = to_lps = to_stats = None
     with context:
-        logprobs = torch.empty(tokens.shape, dtype=f32, device=dev) if M else None
-        entropy = torch.empty(B, dtype=f32, device=dev)
-        ids = torch.empty((B, top), dtype=i32, device=dev) if top else None
-        lps = torch.empty((B, top), dtype=f32, device=dev) if top else None
-        stats = torch.empty((B, 4), dtype=f32, device=dev) if keep_stats else None
-        status = torch.empty(B, dtype=i32, device=dev)
-        rc = load_library().sfc_token_logprobs(*_rows_args(logits, stride, temperature), _ptr(tokens), M, top, _ptr(logprobs),
-                                               entropy.data_ptr(), _ptr(ids), _ptr(lps), _ptr(stats), status.data_ptr(), stream)
+        if M:
+            logprobs = torch.empty(tokens.shape, dtype=torch.float32, device=dev)
+            to_tokens, to_logprobs = tokens.data_ptr(), logprobs.data_ptr()
+        entropy = torch.empty(B, dtype=torch.float32, device=dev)
+        if top:
+            ids, lps = torch.empty((B, top), dtype=torch.int32, device=dev), torch.empty((B, top), dtype=torch.float32, device=dev)
+            to_ids, to_lps = ids.data_ptr(), lps.data_ptr()
+        if keep_stats:
+            stats = torch.empty((B, 4), dtype=torch.float32, device=dev)
+            to_stats = stats.data_ptr()
+        status = torch.empty(B, dtype=torch.int32, device=dev)
+        rc = load_library().sfc_token_logprobs(logits.data_ptr(), _dtype_code(logits), B, V, stride, temperature.data_ptr(), to_tokens, M, top,
+                                               to_logprobs, entropy.data_ptr(), to_ids, to_lps, to_stats, status.data_ptr(), stream)
     if rc != SFC_OK:
         _raise("sfc_token_logprobs", rc)
     return TokenLogprobs(logprobs, entropy, ids, lps, status, stats)
@@ -171,25 +176,25 @@ def policy_loss_and_grad(logits, temperature, tokens, advantages, grad_loss, old
     same temperature; without them the loss is the weighted cross-entropy. ``grad`` may give the [B, V] tensor to write (not
     the logits themselves). Outside autograd. See include/sfc.h."""
     row = check_rows("logits", logits)
-    dev, B = logits.device, logits.shape[0]
-    f32 = torch.float32
+    dev, f32, (B, V) = logits.device, torch.float32, logits.shape
     _expect("temperature", temperature, dev, f32, numel=B)
     _expect("tokens", tokens, dev, torch.int32, shape=(B,))
     _expect("advantages", advantages, dev, f32, numel=B)
     _expect("grad_loss", grad_loss, dev, f32, numel=B)
     if old_logprobs is not None:
         _expect("old_logprobs", old_logprobs, dev, f32, numel=B)
-    grad_row = logits.shape[1] if grad is None else _check_grad(grad, logits)
+    grad_row = V if grad is None else _check_grad(grad, logits)
     stream, context = _enter(dev, stream, logits, temperature, tokens, advantages, grad_loss, old_logprobs, grad)
     with context:
-        loss, logprobs, entropy = (torch.empty(B, dtype=f32, device=dev) for _ in range(3))
-        status = torch.empty(B, dtype=torch.int32, device=dev)
+        loss, logprobs = torch.empty(B, dtype=f32, device=dev), torch.empty(B, dtype=f32, device=dev)
+        entropy, status = torch.empty(B, dtype=f32, device=dev), torch.empty(B, dtype=torch.int32, device=dev)
         if grad is None:
-            grad = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
+            grad = torch.empty((B, V), dtype=logits.dtype, device=dev)
         rc = load_library().sfc_policy_forward_backward(
-            *_rows_args(logits, row, temperature), tokens.data_ptr(), _ptr(old_logprobs), advantages.data_ptr(), clip_low, clip_high,
-            entropy_weight, FLAG_TEST_STALL if test_stall else 0, grad_loss.data_ptr(), loss.data_ptr(), logprobs.data_ptr(),
-            entropy.data_ptr(), status.data_ptr(), grad.data_ptr(), grad_row, stream)
+            logits.data_ptr(), _dtype_code(logits), B, V, row, temperature.data_ptr(), tokens.data_ptr(),
+            None if old_logprobs is None else old_logprobs.data_ptr(), advantages.data_ptr(), clip_low, clip_high, entropy_weight,
+            FLAG_TEST_STALL if test_stall else 0, grad_loss.data_ptr(), loss.data_ptr(), logprobs.data_ptr(), entropy.data_ptr(),
+            status.data_ptr(), grad.data_ptr(), grad_row, stream)
     if rc != SFC_OK:
         _raise("sfc_policy_forward_backward", rc)
     return PolicyGradOutput(loss, logprobs, entropy, grad, status)
