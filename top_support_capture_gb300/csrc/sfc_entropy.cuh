@@ -76,10 +76,12 @@ struct EntropyAcc {
   }
 };
 
-// The sums of vectors whose logits are known to be near: |x c| <= kNear for all of them, and none above m. The exponent is one
-// fused step then, d' = x c - M with M = m c rounded: against another reference, which `finish` takes out again, and every
-// d' is a number, so that none is held.
-constexpr float kNear = 1e18f;
+// The sums of vectors whose logits are known to be near: none above m, |m c| <= kNearTop and |x c| <= kNear for all of them. The
+// exponent is one fused step then, d' = x c - M with M = m c rounded: against another reference, which is off by M's rounding
+// rho, at most half (2^24 and below have steps of 1), and which `finish` takes out again: 2^rho and its inverse are near 1, and
+// w' - rho s' subtracts numbers of the size of half the mass. (Larger references do not do: from 2^31 on 2^rho may be infinite or
+// 0.) kNear keeps every d' a number, so that none is held: its exponential is 0 long before.
+constexpr float kNearTop = 0x1p24f, kNear = 1e18f;
 
 struct NearAcc {
   uint64_t c2, minus_M2, s2 = 0, w2 = 0;
@@ -148,7 +150,7 @@ __device__ __forceinline__ bool add_kept(EntropyAcc& a, const uint4* kept, int n
     low = smaller<DT>(low, v);
   }
   const float most = Elem<DT>::vmax(top);
-  const bool near = fmaxf(fabsf(most * c), fabsf(vmin<DT>(low) * c)) <= kNear;
+  const bool near = fabsf(most * c) <= kNearTop && fabsf(vmin<DT>(low) * c) <= kNear;
   if (near) {
     NearAcc sums(most, c);
 #pragma unroll 4
@@ -260,7 +262,7 @@ struct RowGradient {
       return Out<DT>::pack(x);
     }
   };
-  __device__ __forceinline__ bool moderate() const { return fabsf(m * c) <= kNear && fabsf(a) <= kNear && fabsf(b) <= kNear; }
+  __device__ __forceinline__ bool moderate() const { return fabsf(m * c) <= kNearTop && fabsf(a) <= kNear && fabsf(b) <= kNear; }
 };
 
 // One vector of a gradient row to `to`, which lies `shift` bytes past a 16-byte boundary; by whole warps (see store_shifted).
