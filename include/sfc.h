@@ -422,7 +422,8 @@ int sfc_token_logprobs(const void* logits, int dtype, int64_t B, int64_t V, int6
  *
  * tokens          [B, M] int32, 0 <= M <= SFC_MAX_GIVEN + SFC_MAX_TOP. Ids outside [0, V) pass no gradient on, nor do tokens
  *                 whose logit is -inf (their log-probability is a constant).
- * grad_logprobs   [B, M] float32, or NULL: all 0. grad_entropy [B] float32, or NULL: all 0.
+ * grad_logprobs   [B, M] float32, or NULL: all 0. grad_entropy [B] float32, or NULL: all 0. Where one of them is finite and its
+ *                 quotient by T overflows, the quotient is held at the largest float32.
  * grad_logits     [B, grad_stride] elements of `dtype` out, the first V of each row are written, each rounded once;
  *                 aligned to the element size. Must not overlap the logits. BADPARAM rows get zeros.
  */
@@ -451,7 +452,8 @@ int sfc_token_logprobs_backward(const void* logits, int dtype, int64_t B, int64_
  *                 +inf or none is finite; SFC_ROW_TIMEOUT when a bounded wait of the kernel for its own copies gave up
  *                 (not expected to happen). Such rows' gradients are 0.
  * A token whose logit is -inf has rho = 0, or without old_logprobs the loss +inf (A > 0), and passes no gradient on. A ratio
- * above the largest float32 that is not clipped makes the loss +inf; the gradient's slope is then held at that number.
+ * above the largest float32 that is not clipped makes the loss +inf; the gradient's slope is then held at that number, as is a
+ * finite grad_loss over T that overflows.
  * grad_logits     as in sfc_token_logprobs_backward.
  * Every array is a device pointer owned by the caller; nothing is allocated; results are deterministic.
  * Returns SFC_OK or a negative code (nothing enqueued).

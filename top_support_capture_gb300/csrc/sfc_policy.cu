@@ -64,6 +64,7 @@ __global__ void __launch_bounds__(NT, MINB) policy_kernel(const __grid_constant_
   __shared__ float4 table[kMaxSlices];  // (m, s, w) of the slices
   __shared__ float4 gradient;           // (m, c, a, b) of the row's
   __shared__ float slope_at_token;
+  __shared__ bool lifted;
   __shared__ int outcome;
   const int tid = threadIdx.x, lane = tid & 31, wp = tid >> 5, S = p.slices, rank = blockIdx.y;
   const int64_t r = blockIdx.x;
@@ -150,10 +151,11 @@ __global__ void __launch_bounds__(NT, MINB) policy_kernel(const __grid_constant_
       if (p.entropy_weight != 0.f) loss -= p.entropy_weight * H;
     }
     if (lane == 0) {
-      const float scale = up * inv_T, g = held(slope * scale);
+      const float scale = fabsf(up) < INFINITY ? held(up * inv_T) : up, g = held(slope * scale);
       if (live) {
         const RowGradient dense(all.m, all.s, ln_s, H, g, -p.entropy_weight * scale, c);
         gradient = make_float4(dense.m, dense.c, dense.a, dense.b);
+        lifted = dense.lifted;
         slope_at_token = g;
       }
       outcome = live;
@@ -169,13 +171,15 @@ __global__ void __launch_bounds__(NT, MINB) policy_kernel(const __grid_constant_
   live = outcome;
   // nothing of the CTA's is still in flight when it ends
   if (KEEP && !live && tid == 0 && !p.stall) mbar_wait(&full, 0);
-  const RowGradient dense(gradient);
+  const RowGradient dense(gradient, lifted);
   unsigned char* grad = p.grad + r * p.grad_stride * Elem<DT>::kBytes;
   unsigned char* out = grad + static_cast<int64_t>(row.head) * Elem<DT>::kBytes;
   const int shift = static_cast<int>(reinterpret_cast<uintptr_t>(out) & 15);
   auto put = [&](int at, const uint4& w) { store_vector<DT>(out + static_cast<int64_t>(at) * 16, w, shift, at < v1); };
   if (!live) {
     for (int i = v0 + tid; i - lane < v1; i += NT) put(i, make_uint4(0u, 0u, 0u, 0u));
+  } else if (dense.lifted) {
+    write_lifted<DT, NT>(dense, row, out, shift, v0, v1);
   } else if (KEEP && DT == 0 && shift != 0) {
     for (int i = tid; i - lane < mine; i += NT) put(v0 + i, dense.template vector<DT>(kept[min(i, mine - 1)]));
   } else if (KEEP && near && dense.moderate()) {

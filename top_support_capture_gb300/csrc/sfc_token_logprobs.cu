@@ -348,7 +348,7 @@ __global__ void __launch_bounds__(NT, MINB) score_backward_kernel(const __grid_c
   const float4 st = p.stats[r];
   const float T = p.temperature[r], c = exponent_scale(T), inv_T = fminf(1.f / T, FLT_MAX);
   const bool live = st.x == st.x;  // rows without a log-probability pass no gradient on
-  const float h = p.grad_entropy ? p.grad_entropy[r] * inv_T : 0.f;
+  float h = p.grad_entropy ? p.grad_entropy[r] * inv_T : 0.f;
   float own_x = 0.f;
   if (tid < p.M) {  // a masked token's log-probability is the constant -inf
     const int32_t id = p.tokens[r * p.M + tid];
@@ -361,6 +361,16 @@ __global__ void __launch_bounds__(NT, MINB) score_backward_kernel(const __grid_c
   float G = 0.f;
   for (int j = lane; j < p.M; j += 32) G += gs[j];
   G = warp_total(G);
+  if (large(G, h)) {  // quotients that overflow are held (uniform; upstream gradients that are not finite stay)
+    auto hold = [](float q, float up) { return fabsf(up) < INFINITY ? held(q) : q; };
+    if (p.grad_entropy) h = hold(h, p.grad_entropy[r]);
+    __syncthreads();
+    if (tid < p.M && ids[tid] >= 0 && p.grad_logprobs) gs[tid] = hold(gs[tid], p.grad_logprobs[r * p.M + tid]);
+    __syncthreads();
+    G = 0.f;
+    for (int j = lane; j < p.M; j += 32) G += gs[j];
+    G = warp_total(G);
+  }
   const RowGradient dense(st.x, st.y, logf(st.y), st.z, G, h, c);
   unsigned char* grad = p.grad + r * p.grad_stride * Elem<DT>::kBytes;
   unsigned char* out = grad + static_cast<int64_t>(row.head) * Elem<DT>::kBytes;
@@ -368,6 +378,8 @@ __global__ void __launch_bounds__(NT, MINB) score_backward_kernel(const __grid_c
   if (!live) {
     for (int i = v0 + tid; i - lane < v1; i += NT)
       store_vector<DT>(out + static_cast<int64_t>(i) * 16, make_uint4(0u, 0u, 0u, 0u), shift, i < v1);
+  } else if (dense.lifted) {
+    write_lifted<DT, NT>(dense, row, out, shift, v0, v1);
   } else {
     stream.each([&](const uint4& w, int i) {
       store_vector<DT>(out + static_cast<int64_t>(i) * 16, dense.template vector<DT>(w), shift, i < v1);
