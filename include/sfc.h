@@ -480,9 +480,7 @@ int sfc_policy_forward_backward(const void* logits, int dtype, int64_t B, int64_
  * norm            float32 device scalar out.
  * workspace       device scratch of sfc_grad_norm_workspace_size(n) bytes, 8-byte aligned, of any content, used by one
  *                 call at a time.
- * A bounded wait of the kernel for its own stores that gave up (not expected to happen) makes the norm NaN and leaves the
- * outputs as they were. Results are deterministic. Returns SFC_OK or a negative code (nothing enqueued on SFC_EINVAL and
- * SFC_EWORKSPACE).
+ * Results are deterministic. Returns SFC_OK or a negative code (nothing enqueued on SFC_EINVAL and SFC_EWORKSPACE).
  */
 size_t sfc_grad_norm_workspace_size(int64_t n);
 int sfc_grad_norm(const void* const* grads, const int64_t* counts, const int32_t* dtypes, int64_t n, float* norm,

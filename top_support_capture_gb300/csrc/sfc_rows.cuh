@@ -20,8 +20,18 @@ namespace sfc {
 // The two halves of a cluster barrier (release / acquire).
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-// The arrival of a cluster barrier that orders nothing but the start of its CTAs.
+// The arrival of a cluster barrier that orders no memory, such as that of CTAs which have started.
 __device__ __forceinline__ void cluster_arrive_started() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+// The arrival of a CTA whose first warp alone has stored what the other CTAs are to see behind the barrier: a release waits for
+// all that its warp has in flight.
+__device__ __forceinline__ void cluster_arrive_first_warp() {
+  if (threadIdx.x < 32) {
+    __syncwarp();
+    cluster_arrive();
+  } else {
+    cluster_arrive_started();
+  }
+}
 
 constexpr float kLog2e = 1.4426950408889634f;
 
