@@ -52,6 +52,28 @@ constexpr int kKeepBytes = 212992;  // shared memory of one SM that keeps logits
 constexpr uint32_t kStallPolls = 16;
 constexpr float kLate = -1.f;  // in place of a mass: a copy did not arrive
 
+// The bound of a wait for the other slices' statistics: above that of a slice for its own copy, which says so when it gives up. A
+// CTA that hears nothing for so long (not expected to happen) looks at the whole row itself, so that a row's CTAs all come to the
+// same outcome.
+constexpr uint32_t kJoinPolls = 4 * kWaitPolls;
+
+template <int DT>
+__device__ __noinline__ float4 row_stats(const unsigned char* row, int64_t V, float c) {  // by a whole warp, in two passes
+  const int lane = threadIdx.x & 31;
+  float m = -FLT_MAX;
+  for (int64_t i = lane; i < V; i += 32) m = fmaxf(m, Elem<DT>::load1(row, i));
+  m = warp_max(m);
+  double s = 0.0, w = 0.0;
+  for (int64_t i = lane; i < V; i += 32) {
+    const float d = (Elem<DT>::load1(row, i) - m) * c, e = ex2_approx(d);
+    s += e;
+    w += e * fmaxf(d, kFar);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kFull, s, o), w += __shfl_xor_sync(kFull, w, o);
+  return make_float4(m, static_cast<float>(s), static_cast<float>(w), 0.f);
+}
+
 // KEEP: the slice's vectors lie in dynamic shared memory (16 bytes for each).
 template <int DT, int NT, int MINB, bool KEEP>
 __global__ void __launch_bounds__(NT, MINB) policy_kernel(const __grid_constant__ PolicyParams p) {
@@ -122,10 +144,13 @@ __global__ void __launch_bounds__(NT, MINB) policy_kernel(const __grid_constant_
       if (S > 1) {
         if (tid < S) dsmem_send(dsmem_addr(&table[rank], tid), make_float4(all.m, all.s, all.w, 0.f), dsmem_addr(&joined, tid));
         __syncwarp();
-        late = !__all_sync(kFull, mbar_wait(&joined, 0));
-        if (late) mbar_wait(&joined, 0);  // nothing is on its way to a CTA that has ended
-        late = late || __any_sync(kFull, table[lane < S ? lane : 0].y == kLate);
-        all = merge_shared(table, S, c);
+        if (__all_sync(kFull, mbar_wait(&joined, 0, kJoinPolls))) {
+          late = __any_sync(kFull, table[lane < S ? lane : 0].y == kLate);
+          all = merge_shared(table, S, c);
+        } else if (!late) {
+          const float4 v = row_stats<DT>(row.row, p.V, c);
+          all = EntropyStats{v.x, v.y, v.z};
+        }
       }
       live = stats_valid(all.m, all.s) && !late;
       if (!live) status = late ? SFC_ROW_TIMEOUT : SFC_ROW_BADPARAM;
