@@ -54,6 +54,12 @@ __device__ __forceinline__ uint32_t dsmem_add(uint32_t addr, uint32_t n) {  // t
   return v;
 }
 
+__device__ __forceinline__ uint32_t ld_volatile(const uint32_t* shared) {
+  uint32_t v;
+  asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(v) : "r"(smem_addr(shared)) : "memory");
+  return v;
+}
+
 template <int DT>
 __device__ __forceinline__ uint64_t ckey_of(float x, int64_t id) {  // 0: not an alternative (-inf)
   return x > -INFINITY ? make_ckey(Keys<DT>::key(x), static_cast<uint32_t>(id)) : 0ull;
@@ -128,7 +134,7 @@ __global__ void __launch_bounds__(NT, MINB) score_kernel(const __grid_constant__
   const int32_t token = rank == 0 && tid < p.M ? p.tokens[r * p.M + tid] : -1;
   const bool given = token >= 0 && token < p.V;
   const float xt = given ? row.at(token) : 0.f;
-  if (tid == 0) count = 0;
+  if (tid == 0) count = 0;  // (of the first CTA: that of all)
   const float c = exponent_scale(T);
   EntropyAcc a;
   int batches = 0;
@@ -180,7 +186,7 @@ __global__ void __launch_bounds__(NT, MINB) score_kernel(const __grid_constant__
       if (tid < S) {
         const uint32_t bar = dsmem_addr(&joined, tid);
         dsmem_send(dsmem_addr(&table[rank], tid), make_float4(all.m, all.s, all.w, 0.f), bar);
-        dsmem_send(dsmem_addr(&bounds[rank], tid), make_float4(own.x, own.y, 0.f, 0.f), bar);
+        dsmem_send(dsmem_addr(&bounds[rank], tid), make_float4(own.x, own.y, __uint_as_float(ld_volatile(&count)), 0.f), bar);
       }
       __syncwarp();
       late = !__all_sync(kFull, mbar_wait(&joined, 0));
@@ -203,7 +209,8 @@ __global__ void __launch_bounds__(NT, MINB) score_kernel(const __grid_constant__
   if (K > 0 && valid) {
     const uint32_t counter = S > 1 ? dsmem_addr(&count, 0) : smem_addr(&count);
     const uint32_t places = S > 1 ? dsmem_addr(pool, 0) : smem_addr(pool);
-    auto add = [&](uint32_t n) { return S > 1 ? dsmem_add(counter, n) : atomicAdd(&count, n); };
+    // What the counter stood at came with the first CTA's statistics: places depend on that value, so that no CTA adds before it.
+    auto add = [&](uint32_t n) { return S > 1 ? dsmem_add(counter, n) - __float_as_uint(bounds[0].z) : atomicAdd(&count, n); };
     auto place = [&](uint32_t at, float x, int64_t id) {
       if (at < kPool) dsmem_st64(places + at * 8, ckey_of<DT>(x, id));
     };
