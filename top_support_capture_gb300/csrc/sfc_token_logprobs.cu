@@ -179,7 +179,6 @@ __global__ void __launch_bounds__(NT, MINB) score_kernel(const __grid_constant__
     own = make_float2(cut[0], cut[1]);
   }
   float bound = own.x;
-  bool late = false;
   if (S > 1) {
     cluster_wait();
     if (wp == 0) {
@@ -189,23 +188,25 @@ __global__ void __launch_bounds__(NT, MINB) score_kernel(const __grid_constant__
         dsmem_send(dsmem_addr(&bounds[rank], tid), make_float4(own.x, own.y, __uint_as_float(ld_volatile(&count)), 0.f), bar);
       }
       __syncwarp();
-      late = !__all_sync(kFull, mbar_wait(&joined, 0));
-      if (late) mbar_wait(&joined, 0);  // nothing is on its way to a CTA that has ended
-      all = merge_shared(table, S, c);
-      float low = bounds[0].y;
-      bound = bounds[0].x;
-      for (int i = 1; i < S; ++i) {
-        bound = fmaxf(bound, bounds[i].x);
-        low = fminf(low, bounds[i].y);
+      if (__all_sync(kFull, mbar_wait(&joined, 0, 2 * kWaitPolls))) {
+        all = merge_shared(table, S, c);
+        float low = bounds[0].y;
+        bound = bounds[0].x;
+        for (int i = 1; i < S; ++i) {
+          bound = fmaxf(bound, bounds[i].x);
+          low = fminf(low, bounds[i].y);
+        }
+        if (lane == 0) joint = make_float4(all.m, all.s, all.w, fmaxf(bound, low));
+      } else {  // the first CTA: SFC_ROW_TIMEOUT; without another's alternatives, it finds them all one by one
+        if (lane == 0) joint = make_float4(-FLT_MAX, kLate, 0.f, 0.f);
+        if (lane == 0 && K > 0) dsmem_add(dsmem_addr(&count, 0), kPool + 1);
       }
-      if (lane == 0) joint = make_float4(all.m, late ? kLate : all.s, all.w, fmaxf(bound, low));
     }
     __syncthreads();
     all = EntropyStats{joint.x, joint.y, joint.z};
     bound = joint.w;
-    late = all.s == kLate;
   }
-  const bool valid = stats_valid(all.m, all.s);  // uniform over the cluster (but for waits that gave up)
+  const bool valid = stats_valid(all.m, all.s), late = all.s == kLate;  // uniform over the cluster (but for waits that gave up)
   if (K > 0 && valid) {
     const uint32_t counter = S > 1 ? dsmem_addr(&count, 0) : smem_addr(&count);
     const uint32_t places = S > 1 ? dsmem_addr(pool, 0) : smem_addr(pool);
