@@ -472,7 +472,7 @@ int sfc_policy_forward_backward(const void* logits, int dtype, int64_t B, int64_
  *
  * grads, counts, dtypes   HOST arrays of n entries, read during the call: the tensors' device addresses (aligned to their
  *                 element size; NULL where the count is 0), elements and SFC_BF16 / SFC_F32 codes. A tensor is `count`
- *                 elements in a row. 0 <= n <= 2^20, 2^44 elements in all.
+ *                 elements in a row. 0 <= n <= 2^20, 2^43 elements in all.
  * max_norm        >= 0; infinity: nothing is scaled.
  * out, out_dtypes HOST arrays of n entries: where each clipped tensor is written and its type (rounded once). A tensor's own
  *                 address and type clips it in place (then nothing is written where scale is 1). No byte of an output may

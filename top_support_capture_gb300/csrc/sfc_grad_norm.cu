@@ -422,7 +422,9 @@ cudaError_t run(const List& l, float max_norm, float* norm, double* partial, cud
   return cudaSuccess;
 }
 
-constexpr int64_t kMaxTensors = 1 << 20, kMaxElements = int64_t{1} << 44;  // chunks are counted in 32 bits
+constexpr int64_t kMaxTensors = 1 << 20, kMaxElements = int64_t{1} << 43;
+// (f32 makes the most chunks, and each tensor may end in a partial one)
+static_assert(kMaxElements / (kChunk * 4) + kMaxTensors <= INT32_MAX, "chunks are counted in 32 bits");
 
 size_t workspace_bytes_of(int64_t n) { return static_cast<size_t>(n / kMany + 1) * kCtas * sizeof(double); }
 
