@@ -26,18 +26,43 @@ def _dense(t):
     return True
 
 
+def _listed(tensors):
+    return [tensors] if isinstance(tensors, torch.Tensor) else list(tensors)
+
+
+def pair(grads, out):
+    """The gradients that there are (entries None left out) and each one's output: the entry in its place of an ``out`` that is as
+    long as ``grads``, or of one that has an entry for each gradient there is."""
+    grads, out = _listed(grads), _listed(out)
+    there, places = [g for g in grads if g is not None], range(len(out))
+    if len(out) == len(grads):
+        if len(there) < len(grads):
+            places = [i for i in places if grads[i] is not None]
+            out = [out[i] for i in places]
+    elif len(out) != len(there):
+        raise SfcError(f"out must hold {len(grads)} tensors" + (f" (or {len(there)}, one for each gradient there is)" if len(there) < len(grads) else "")
+                       + f", got {len(out)}")
+    if len([o for o in out if o is not None]) < len(out):
+        raise SfcError(f"out[{next(i for i, o in zip(places, out) if o is None)}] is None beside a gradient")
+    return there, out
+
+
 def check_tensors(name, tensors):
     """The tensors as a list (entries None left out), each on one CUDA device and dense; and whether all are contiguous."""
-    tensors = [t for t in ([tensors] if isinstance(tensors, torch.Tensor) else tensors) if t is not None]
+    tensors = [t for t in _listed(tensors) if t is not None]
+    return tensors, check_listed(name, tensors)
+
+
+def check_listed(name, tensors):
     if not tensors:
         raise SfcError(f"{name} holds no tensor")
-    plain = _all_plain(tensors)
-    if not plain:
-        device = tensors[0].device
-        if device.type != "cuda":
-            raise SfcError(f"{name} must be CUDA tensors, got {device}")
-        check_layouts(name, tensors, device)
-    return tensors, plain
+    if _all_plain(tensors):
+        return True
+    device = tensors[0].device
+    if device.type != "cuda":
+        raise SfcError(f"{name} must be CUDA tensors, got {device}")
+    check_layouts(name, tensors, device)
+    return False
 
 
 def _all_plain(tensors):
@@ -85,19 +110,21 @@ def grad_norm(grads, stream=None):
 
 
 def clip_grad_norm(grads, max_norm: float, out=None, stream=None):
-    """Scales ``grads`` so that their global norm is at most ``max_norm``, in place, or into the tensors of ``out`` (as many, of
-    as many elements; bf16 or f32 each, as the optimizer wants them). Returns the norm before clipping, a float32 scalar
-    tensor. No host synchronisation. See include/sfc.h."""
+    """Scales ``grads`` so that their global norm is at most ``max_norm``, in place, or into the tensors of ``out`` (each of as many
+    elements as its gradient; bf16 or f32, as the optimizer wants them). Beside entries None of ``grads`` ``out`` may be as long as
+    they are, then its entries there are left alone, or have one entry for each gradient there is. Returns the norm before
+    clipping, a float32 scalar tensor. No host synchronisation. See include/sfc.h."""
     max_norm = float(max_norm)
     if not max_norm >= 0.0:
         raise SfcError(f"max_norm must be >= 0, got {max_norm}")
-    grads, plain = check_tensors("grads", grads)
-    lists = _arrays(grads)
     if out is None:
+        grads, _ = check_tensors("grads", grads)
+        lists = _arrays(grads)
         return _run(grads, lists, grads, lists, max_norm, stream)
-    out, out_plain = check_tensors("out", out)
-    to = _arrays(out)
-    if len(out) != len(grads) or to[1] != lists[1] or out[0].device != grads[0].device or not (plain and out_plain):
+    grads, out = pair(grads, out)
+    plain, out_plain = check_listed("grads", grads), check_listed("out", out)
+    lists, to = _arrays(grads), _arrays(out)
+    if to[1] != lists[1] or out[0].device != grads[0].device or not (plain and out_plain):
         check_out(grads, out)
     return _run(grads, lists, out, to, max_norm, stream)
 
