@@ -9,7 +9,7 @@ from operator import attrgetter
 import torch
 from torch.autograd import forward_ad
 
-from . import SFC_OK, SfcError, _dtype_code, _enter, load_library
+from . import SFC_BF16, SFC_F32, SFC_OK, SfcError, _enter, load_library
 from .training import _raise
 
 _dtype, _requires_grad = attrgetter("dtype"), attrgetter("requires_grad")
@@ -91,14 +91,19 @@ def check_layouts(name, tensors, device):
             raise SfcError(f"{name}[{i}] is a forward-mode dual tensor: there is no forward-mode derivative")
 
 
-def _arrays(tensors):
+_CODES = {torch.bfloat16: SFC_BF16, torch.float32: SFC_F32}
+
+
+def _arrays(tensors, name="grads"):
     """(addresses, counts, dtype codes) as the library reads them."""
     dtypes = list(map(_dtype, tensors))
-    if dtypes.count(dtypes[0]) == len(dtypes):
-        codes = array("i", [_dtype_code(tensors[0])]) * len(dtypes)
-    else:
-        of = {t.dtype: _dtype_code(t) for t in map(tensors.__getitem__, map(dtypes.index, set(dtypes)))}
-        codes = array("i", map(of.__getitem__, dtypes))
+    try:
+        if dtypes.count(dtypes[0]) == len(dtypes):
+            codes = array("i", [_CODES[dtypes[0]]]) * len(dtypes)
+        else:
+            codes = array("i", map(_CODES.__getitem__, dtypes))
+    except KeyError as e:
+        raise SfcError(f"{name} must be bfloat16 or float32, got {e.args[0]}") from None
     return array("Q", map(_Tensor.data_ptr, tensors)), array("q", map(_Tensor.numel, tensors)), codes
 
 
@@ -123,7 +128,7 @@ def clip_grad_norm(grads, max_norm: float, out=None, stream=None):
         return _run(grads, lists, grads, lists, max_norm, stream)
     grads, out = pair(grads, out)
     plain, out_plain = check_listed("grads", grads), check_listed("out", out)
-    lists, to = _arrays(grads), _arrays(out)
+    lists, to = _arrays(grads), _arrays(out, "out")
     if to[1] != lists[1] or out[0].device != grads[0].device or not (plain and out_plain):
         check_out(grads, out)
     return _run(grads, lists, out, to, max_norm, stream)
