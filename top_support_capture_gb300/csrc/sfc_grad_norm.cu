@@ -176,16 +176,12 @@ __global__ void __launch_bounds__(kThreads, 4) grad_norm_kernel(const __grid_con
   if (threadIdx.x == 0) p.partial[p.slot + b] = sum;
 }
 
-// All CTAs' sums, by a whole CTA: the same order and bits wherever it is called.
+// All CTAs' sums, by a whole CTA: the same order and bits wherever it is called. In thread 0.
 __device__ __forceinline__ double total_norm(const double* partial, int slots) {
   __shared__ double red[kThreads / 32];
-  __shared__ double norm;
   double sum = 0.0;
   for (int i = threadIdx.x; i < slots; i += kThreads) sum += __ldcg(partial + i);
-  sum = block_total(sum, red);
-  if (threadIdx.x == 0) norm = sqrt(sum);
-  __syncthreads();
-  return norm;
+  return sqrt(block_total(sum, red));
 }
 
 __global__ void __launch_bounds__(kThreads) finish_norm_kernel(const double* partial, int slots, float* norm) {
@@ -270,13 +266,32 @@ __device__ __forceinline__ void scale_chunk(const Tensor& t, int chunk, float sc
   }
 }
 
-__device__ __forceinline__ float scale_of(double norm, float max_norm) {  // NaN stays
+// The scale; NaN stays. One below the smallest normal number has too few bits for the ordinary numbers that huge gradients
+// become: it is given as the negative of its 2^126-fold.
+__device__ __forceinline__ float scale_of(double norm, float max_norm) {
   const double ratio = max_norm / (norm + 1e-6);
-  return max_norm == INFINITY || ratio >= 1.0 ? 1.f : static_cast<float>(ratio);
+  const float scale = max_norm == INFINITY || ratio >= 1.0 ? 1.f : static_cast<float>(ratio);
+  return scale < FLT_MIN && max_norm > 0.f ? -static_cast<float>(ratio * 0x1p126) : scale;
+}
+
+// A chunk by such a scale, element by element: the second factor is exact. (Out of line: hardly any call needs it.)
+__device__ __noinline__ void scale_tiny(const void* in, void* out, int64_t first, int64_t end, bool in_bf16, bool out_bf16, float scale) {
+#pragma unroll 1
+  for (int64_t i = first + threadIdx.x; i < end; i += kThreads) {
+    const float x = in_bf16 ? get(static_cast<const __nv_bfloat16*>(in) + i) : get(static_cast<const float*>(in) + i);
+    const float y = x * scale * 0x1p-126f;
+    if (out_bf16) put(static_cast<__nv_bfloat16*>(out) + i, y);
+    else put(static_cast<float*>(out) + i, y);
+  }
 }
 
 __device__ __forceinline__ void clip_chunk(const Tensor& t, int chunk, float scale) {
   if (scale == 1.f && t.in == t.out) return;  // in place: nothing to do
+  if (scale < 0.f) {
+    const int64_t per = kChunk * (t.dtype == SFC_BF16 ? 8 : 4), first = chunk * per;
+    scale_tiny(t.in, t.out, first, min(first + per, t.count), t.dtype == SFC_BF16, t.out_dtype == SFC_BF16, -scale);
+    return;
+  }
   if (t.dtype == SFC_BF16) {
     if (t.out_dtype == SFC_BF16) scale_chunk<__nv_bfloat16, __nv_bfloat16>(t, chunk, scale);
     else scale_chunk<__nv_bfloat16, float>(t, chunk, scale);
@@ -290,24 +305,29 @@ __device__ __forceinline__ void clip_chunk(const Tensor& t, int chunk, float sca
 // (534 M elements f32 to bf16, both calls: 785 us, with four 1046; f32 to f32 954 : 1013; bf16 to f32 669 : 671).
 template <int CAP>
 __global__ void __launch_bounds__(kThreads, 3) clip_kernel(const __grid_constant__ Tensors<CAP> p) {
+  __shared__ float scale;
   wait_for_last();
   const double norm = total_norm(p.partial, p.slots);
-  if (blockIdx.x == 0 && threadIdx.x == 0) *p.norm = static_cast<float>(norm);
-  const float scale = scale_of(norm, p.max_norm);
+  if (threadIdx.x == 0) {
+    scale = scale_of(norm, p.max_norm);
+    if (blockIdx.x == 0) *p.norm = static_cast<float>(norm);
+  }
+  __syncthreads();
   const int64_t b = blockIdx.x;
   each_chunk(p, static_cast<int>(b * p.chunks / gridDim.x), static_cast<int>((b + 1) * p.chunks / gridDim.x), true,
              [&](const Tensor& t, int chunk) { clip_chunk(t, chunk, scale); });
 }
 
 // Short lists of a megabyte at most in one launch: a cluster whose CTAs give one another their sums, and then clip the chunks
-// that they have read (two tables of 64000 bf16: 5.7 us, in two launches 7.0, and 2.6 us less of the calling thread). The exchange
-// is a cluster barrier, behind which every CTA knows the same: sums sent by stores that the receiver's barrier counts took 5.4 us,
-// but wait in software, and a CTA whose wait gave up would leave its chunks as they are while the others clip theirs.
+// that they have read (two tables of 64000 bf16: 5.4 us, in two launches 7.0, and 2.6 us less of the calling thread). The exchange
+// is a cluster barrier, behind which every CTA knows the same: sums sent by stores that the receiver's barrier counts would save
+// 0.3 us, but wait in software, and a CTA whose wait gave up would leave its chunks as they are while the others clip theirs.
 constexpr int kShortCtas = 8, kShortChunks = 32;
 
 template <bool CLIP>
 __global__ void __launch_bounds__(kThreads, 2) short_kernel(const __grid_constant__ Tensors<kFew> p) {
-  __shared__ double red[kThreads / 32], table[kShortCtas], norm;
+  __shared__ double red[kThreads / 32], table[kShortCtas];
+  __shared__ float scale;
   const int tid = threadIdx.x, rank = blockIdx.x;
   cluster_arrive_started();
   const int c0 = rank * p.chunks / kShortCtas, c1 = (rank + 1) * p.chunks / kShortCtas;
@@ -324,12 +344,12 @@ __global__ void __launch_bounds__(kThreads, 2) short_kernel(const __grid_constan
   if (tid == 0) {
     double total = 0.0;
     for (int i = 0; i < kShortCtas; ++i) total += table[i];
-    norm = sqrt(total);
+    const double norm = sqrt(total);
+    if (CLIP) scale = scale_of(norm, p.max_norm);
     if (rank == 0) *p.norm = static_cast<float>(norm);
   }
   if (!CLIP) return;
   __syncthreads();
-  const float scale = scale_of(norm, p.max_norm);
   each_chunk(p, c0, c1, true, [&](const Tensor& t, int chunk) { clip_chunk(t, chunk, scale); });
 }
 
