@@ -467,8 +467,10 @@ int sfc_policy_forward_backward(const void* logits, int dtype, int64_t B, int64_
 /*
  * The global norm of a model's gradients, and their clipping by it:
  *   norm = sqrt(sum over all tensors and elements of x^2),  scale = min(1, max_norm / (norm + 1e-6)),  out_i = grads_i scale
- * The sum is held in 64 bits: no element of the types' range overflows it or is lost from it. A norm that is not finite
- * scales as the formula has it (infinite: finite elements become 0 and infinite ones NaN; NaN: all become NaN).
+ * A thread's squares are summed in 32 bits, in batches of 32 at most and then compensated; batches outside [2^-100, 2^100] and
+ * the threads' sums in 64. The norm is within 8 half steps of float32 (2^-24 each) of the exact one over the types' whole range;
+ * above the largest float32 it is reported as infinite, and scales as the number that it is. A norm that is not finite because
+ * an element is not scales as the formula has it (infinite: finite elements become 0 and infinite ones NaN; NaN: all become NaN).
  *
  * grads, counts, dtypes   HOST arrays of n entries, read during the call: the tensors' device addresses (aligned to their
  *                 element size; NULL where the count is 0), elements and SFC_BF16 / SFC_F32 codes. A tensor is `count`

@@ -136,22 +136,27 @@ __device__ __forceinline__ float vmin(const uint4& v) {
   return x[0];
 }
 
-// One thread's share (every NT-th) of n vectors in shared memory. The extremes come first: the sums then have no rescaling and
-// no step that waits for the one before. Returns whether the thread's logits are near.
+// One thread's share (every NT-th) of n vectors in shared memory; by whole warps. The extremes come first: the sums then have no
+// rescaling and no step that waits for the one before. A warp takes one form of the sums (of threads that see nothing but a mask's
+// fill beside others it would go through both). Returns whether each |x c| is at most kNear.
 template <int DT, int NT>
 __device__ __forceinline__ bool add_kept(EntropyAcc& a, const uint4* kept, int n, float c) {
   const int tid = threadIdx.x;
-  if (tid >= n) return true;
-  uint4 top = kept[tid], low = top;
+  float most = 0.f, least = 0.f;
+  if (tid < n) {
+    uint4 top = kept[tid], low = top;
 #pragma unroll 4
-  for (int k = tid + NT; k < n; k += NT) {
-    const uint4 v = kept[k];
-    top = larger<DT>(top, v);
-    low = smaller<DT>(low, v);
+    for (int k = tid + NT; k < n; k += NT) {
+      const uint4 v = kept[k];
+      top = larger<DT>(top, v);
+      low = smaller<DT>(low, v);
+    }
+    most = Elem<DT>::vmax(top), least = vmin<DT>(low);
   }
-  const float most = Elem<DT>::vmax(top);
-  const bool near = fabsf(most * c) <= kNearTop && fabsf(vmin<DT>(low) * c) <= kNear;
-  if (near) {
+  const bool near = fmaxf(fabsf(most * c), fabsf(least * c)) <= kNear;
+  const bool short_form = __all_sync(kFull, near && fabsf(most * c) <= kNearTop);
+  if (tid >= n) return true;
+  if (short_form) {
     NearAcc sums(most, c);
 #pragma unroll 4
     for (int k = tid; k < n; k += NT) sums.template add<DT>(kept[k]);
@@ -175,6 +180,7 @@ __device__ __forceinline__ void prefetch_l2(const void* from, uint32_t bytes) { 
 struct EntropyStats {
   float m, s, w;
 
+  // In 32 bits: no log-probability of the row is smaller than ln s in size (z - max z <= 0), so the rounding is one of the result's.
   __device__ __forceinline__ float log_sum() const { return logf(s); }
   __device__ __forceinline__ float entropy(float ln_s) const { return fmaxf(ln_s - kLn2 * (w / s), 0.f); }
 };

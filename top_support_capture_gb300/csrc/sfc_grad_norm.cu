@@ -10,7 +10,8 @@
 // addition a batch took more than the memory's time: 534 M bf16 elements 396 us, so 150, 7.1 TB/s), the threads in 64. The
 // CTAs' sums lie in the workspace, and whoever needs the norm adds them up in the same fixed order. A batch whose sum lies outside
 // [2^-100, 2^100], where squares may overflow or lose bits, is summed in 64 bits by itself: the norm holds over the whole
-// range of its elements.
+// range of its elements. Roundings: 8 of a lane's chain, 2 that join the lanes, 2 of the compensated sum, in half steps of the
+// sum and so half as many of the norm, and the norm's own: 7 half steps, 2^-21.
 #include <cuda_runtime.h>
 
 #include <algorithm>

@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(NT, MINB) policy_kernel(const __grid_constant_
   const bool sound = temperature_valid(T) && token >= -1 && token < p.V && fabsf(A) < INFINITY && fabsf(old) < INFINITY;
   int status = sound ? SFC_ROW_OK : SFC_ROW_BADPARAM;
   bool live = sound && token >= 0, late = false;  // uniform over the row's CTAs
-  bool near = false;  // this thread's kept logits are
+  bool near = false;  // this thread's kept logits lie within kNear
   if (live) {
     EntropyAcc a;
     if (KEEP) {
