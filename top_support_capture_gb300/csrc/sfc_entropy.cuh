@@ -177,6 +177,13 @@ __device__ __forceinline__ void prefetch_l2(const void* from, uint32_t bytes) { 
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(from), "r"(bytes) : "memory");
 }
 
+// x - m over T, as divide(x - m); a difference of finite logits that passes the largest number is taken by halves.
+template <class F>
+__device__ __forceinline__ float below_max(float x, float m, F divide) {
+  const float d = x - m;
+  return d == -INFINITY && x > -INFINITY ? divide(0.5f * x - 0.5f * m) * 2.f : divide(d);
+}
+
 struct EntropyStats {
   float m, s, w;
 

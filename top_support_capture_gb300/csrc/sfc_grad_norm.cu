@@ -272,7 +272,7 @@ __device__ __forceinline__ void scale_chunk(const Tensor& t, int chunk, float sc
 __device__ __forceinline__ float scale_of(double norm, float max_norm) {
   const double ratio = max_norm / (norm + 1e-6);
   const float scale = max_norm == INFINITY || ratio >= 1.0 ? 1.f : static_cast<float>(ratio);
-  return scale < FLT_MIN && max_norm > 0.f ? -static_cast<float>(ratio * 0x1p126) : scale;
+  return scale < FLT_MIN && ratio > 0.0 ? -static_cast<float>(ratio * 0x1p126) : scale;
 }
 
 // A chunk by such a scale, element by element: the second factor is exact. (Out of line: hardly any call needs it.)

@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(NT, MINB) policy_kernel(const __grid_constant_
     if (live) {
       ln_s = all.log_sum();
       H = all.entropy(ln_s);
-      const float z = (xt - all.m) * inv_T;
+      const float z = below_max(xt, all.m, [&](float d) { return d * inv_T; });
       lp = z - ln_s;
       if (p.old_logprobs) {
         // lp - old with the quotient's remainder, and the near numbers subtracted first: rho is as exact as its exponent

@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(NT, MINB) score_kernel(const __grid_constant__
   if (rank != 0) return;
   const bool ok = valid && !wrong;
   const float nan = __int_as_float(0x7fc00000), ln_s = all.log_sum();
-  auto logprob = [&](float x) { return (x - all.m) / T - ln_s; };
+  auto logprob = [&](float x) { return below_max(x, all.m, [&](float d) { return d / T; }) - ln_s; };
   if (tid < p.M) p.logprobs[r * p.M + tid] = !ok ? nan : given ? logprob(xt) : 0.f;
   if (tid == 0) {
     const float H = all.entropy(ln_s);
@@ -449,13 +449,14 @@ cudaError_t choose(ScoreParams& p, int64_t B, cudaStream_t stream) {
   const int64_t vectors = p.V / Elem<DT>::kVec;
   // Few rows: slices for every SM (two or four or eight: clusters of other sizes leave SMs out; 24 x 151936 bf16 with six 6.3
   // us, four 5.7), and CTAs as large as keeps some vectors for each thread (1 x 151936: of 256 4.0 us, of 512 4.4; 64 x 151936
-  // 10.4 : 7.9). Twice the slices do no better: 64 x 151936 in two of 512 7.6 us, with 5 alternatives 10.3, in four of 256 7.5 and
-  // 10.5, in eight of 128 7.7 and 11.2; 128 rows in one 11.1 and 13.5, in two of 256 11.7 and 14.8; 256 rows 17.8 and 21.3, 19.1
-  // and 23.3. Many rows: one CTA each, of a size of which several take turns on a SM, without alternatives : with 20. bf16, 2048
-  // rows in CTAs of 128 and of 256: x 32000 26.0 : 35.3 and 26.2 : 38.8, x 56000 43.1 : 52.8 and 42.1 : 54.0, x 65000 48.8 : 57.8
-  // and 47.3 : 58.8, x 151936 106.6 : 118.2 and 100.5 : 113.6 (of 512 128, cut in two 129: each slice goes through the choice).
-  // f32, 1024 rows: x 50000 35.1 : 39.6 and 37.7 : 44.1, x 129280 82.0 : 88.1 and 85.5 : 93.4 (the bound is the one that bf16
-  // wants). Groups of a CTA's threads need vectors to look at: rows below 1024 have CTAs of 128.
+  // 10.4 : 7.9). Twice the slices: 64 x 151936 in two of 512 7.6 us, with 5 alternatives 10.3, in four of 256 7.5 and 10.5, in
+  // eight of 128 7.7 and 11.2; 128 rows in one of 512 11.1 and 13.5, in two of 256 11.7 and 14.8; 200 rows 17.5 and 21.1, 15.3 and
+  // 18.8; 256 rows 17.8 and 21.3, 19.1 and 23.3. Many rows: one CTA each, of a size of which several take turns on a SM. Without
+  // alternatives and with 20, 2048 bf16 rows in CTAs of 128 : of 256: x 32000 26.0 and 35.3 : 26.2 and 38.8, x 56000 43.1 and 52.8 :
+  // 42.1 and 54.0, x 65000 48.8 and 57.8 : 47.3 and 58.8, x 151936 106.6 and 118.2 : 100.5 and 113.6 (of 512 128 with 20, of 256 cut
+  // in two 129: each slice goes through the choice); 1024 f32 rows: x 50000 35.1 and 39.6 : 37.7 and 44.1, x 129280 82.0 and 88.1 :
+  // 85.5 and 93.4 (the bound is the one that bf16 wants). Groups of a CTA's threads need vectors to look at: rows below 1024 have
+  // CTAs of 128.
   p.slices = 1;
   while (p.slices < kMaxSlices && 2 * p.slices * B <= 152 && vectors >= 4096 * p.slices) p.slices *= 2;
   if (B > 304) return p.V <= 56000 ? start<DT, 128, 8>(p, B, stream) : start<DT, 256, 4>(p, B, stream);
